@@ -391,8 +391,9 @@ def _run_tables(s):
     old = (cached + p - 1) // p
     need = (cached + new + p - 1) // p - old
     off = need.cumsum(0) - need
-    fits = off + need <= s["num_free"]
-    taken = torch.where(fits, off + need, torch.zeros_like(off)).amax().reshape(1)
+    end = off + need
+    fits = (need == 0) | (end <= s["num_free"])          # one that needs no page is always served
+    taken = torch.where(end <= s["num_free"], end, torch.zeros_like(end)).amax().reshape(1)
     cu = torch.cat((torch.zeros_like(new[:1]), new.cumsum(0)))
     src = s["src"][s["src_rows"].long()] if s["src_rows"] is not None else s["src"][:n]
     e = torch.arange(s["blocks"], device="cuda")
