@@ -21,16 +21,21 @@ SAW_ERR_UNSUPPORTED = 2
 SAW_ERR_CUDA = 3
 SAW_ERR_DEVICE_INDEX = 4
 SAW_ERR_DEVICE_TIMEOUT = 5
+SAW_ERR_DEVICE_PAGES = 6
 SAW_STEP_EARLY_PAGES = 1
 SAW_FMT_F16_INPUT = 1
 SAW_FMT_BF16_META = 2
+SAW_FMT_OUT_INPUT = 4
+SAW_ROPE_NONE, SAW_ROPE_LINEAR, SAW_ROPE_NTK, SAW_ROPE_YARN, SAW_ROPE_BANDS = range(5)
 
 EXPORTS = ("saw_status_string", "saw_cache_bytes", "saw_quantize_append", "saw_decode_plan",
            "saw_decode_workspace_bytes", "saw_paged_decode_int4", "saw_decode_step",
            "saw_paged_decode_int4_noalloc", "saw_bf16_cache_bytes", "saw_bf16_append",
            "saw_decode_bf16_workspace_bytes", "saw_paged_decode_bf16", "saw_prefill_attn_int4",
            "saw_quantize_append_ex", "saw_paged_decode_int4_ex", "saw_decode_step_ex",
-           "saw_prefill_attn_int4_ex", "saw_paged_decode_int4_noalloc_ex")
+           "saw_prefill_attn_int4_ex", "saw_paged_decode_int4_noalloc_ex", "saw_build_tables",
+           "saw_rope_table", "saw_rope_append", "saw_prefix_decode_workspace_bytes",
+           "saw_prefix_decode_int4")
 
 _lib = None
 
@@ -85,6 +90,20 @@ def lib() -> C.CDLL:
     L.saw_prefill_attn_int4.restype = i32
     L.saw_prefill_attn_int4.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i32,
                                         i32, i32, i32, i32, i32, f32, P, P, P]
+    f64 = C.c_double
+    L.saw_build_tables.restype = i32
+    L.saw_build_tables.argtypes = [P, i32, i32, P, P, P, P, i32, P, i32, i32, i32, i32, P, i32, P,
+                                   P, P, P, P, P, P]
+    L.saw_rope_table.restype = i32
+    L.saw_rope_table.argtypes = [P, i32, i32, f64, i32, f64, i32, f64, f64, f32, P]
+    L.saw_rope_append.restype = i32
+    L.saw_rope_append.argtypes = [P, i64, P, i64, P, i64, P, P, i32, i32, i32, P, i32, i32, i32,
+                                  i32, P, i64, P, P, i32, i32, i32, i32, i32, i32, P, P]
+    L.saw_prefix_decode_workspace_bytes.restype = sz
+    L.saw_prefix_decode_workspace_bytes.argtypes = [i32] * 8
+    L.saw_prefix_decode_int4.restype = i32
+    L.saw_prefix_decode_int4.argtypes = [P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
+                                         i32, i32, i32, i32, i32, i32, f32, P, P, sz, i32, P, P]
     # the *_ex calls: the same arguments plus `formats` before dev_status
     for name in ("saw_quantize_append", "saw_paged_decode_int4", "saw_decode_step",
                  "saw_prefill_attn_int4", "saw_paged_decode_int4_noalloc"):
@@ -324,6 +343,164 @@ def saw_prefill_attn_int4(q: torch.Tensor, cu_q_lens: torch.Tensor, k_cache: tor
         d, num_pages, page_size, int(rotate_k), int(rotate_v), block_h, float(sm_scale),
         _ptr(out), _ptr(dev_status), _stream(q, stream)])
     _raise(rc, "saw_prefill_attn_int4")
+
+
+# ---------------------------------------------------------------- a serving step
+# These calls run once or more per layer on small batches, where the host's
+# share of a call is what a user waits for: pointers are passed as plain
+# integers and every check is one comparison.
+
+def _dev(t: torch.Tensor) -> None:
+    """The library launches on the current device: it has to be the tensors'."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _i32(t, what: str, n: int | None = None):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{what} must have {n} entries, not {t.numel()}")
+    return t.data_ptr()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(t: torch.Tensor, stream):
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def saw_build_tables(cached_lens, new_lens: torch.Tensor, free_pages: torch.Tensor, num_free,
+                     page_size: int, num_pages: int, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, cu_q_lens: torch.Tensor, slot_mapping: torch.Tensor,
+                     positions=None, pages_taken=None, src_tables=None, src_rows=None,
+                     dev_status=None, stream=None) -> None:
+    """Block tables [B, max_blocks], slot_mapping and positions [max_tokens],
+    seq_lens [B] and cu_q_lens [B + 1] (all int32) of a batch from its lengths
+    [B] and a list of free pages; num_free: int32 [1] or None (all of the
+    list).  src_tables [R, blocks] with src_rows [B]: the requests' tables so
+    far (None: nothing cached; block_tables itself: extended in place)."""
+    _dev(new_lens)
+    B = new_lens.numel()
+    rows, blocks = src_tables.shape if src_tables is not None else (0, 0)
+    if block_tables.shape[0] != B:
+        raise ValueError(f"block_tables must have {B} rows, not {block_tables.shape[0]}")
+    rc = lib().saw_build_tables(
+        _i32(src_tables, "src_tables"), rows, blocks, _i32(src_rows, "src_rows", B),
+        _i32(cached_lens, "cached_lens", B), _i32(new_lens, "new_lens"),
+        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(num_free, "num_free", 1), B,
+        slot_mapping.numel(), num_pages, page_size, _i32(block_tables, "block_tables"),
+        block_tables.shape[1], _i32(seq_lens, "seq_lens", B),
+        _i32(cu_q_lens, "cu_q_lens", B + 1), _i32(slot_mapping, "slot_mapping"),
+        _i32(positions, "positions", slot_mapping.numel()), _i32(pages_taken, "pages_taken", 1),
+        _i32(dev_status, "dev_status"), _raw_stream(new_lens, stream))
+    _raise(rc, "saw_build_tables")
+
+
+def saw_rope_table(cos_sin: torch.Tensor, base: float = 10000.0, scaling: int = SAW_ROPE_NONE,
+                   factor: float = 1.0, orig_max_pos: int = 0, low: float = 0.0,
+                   high: float = 0.0, att_scale: float = 0.0, stream=None) -> None:
+    """Fill cos_sin (float32 [max_pos, rope_dim]): cosines of the rope_dim/2
+    pairs, then sines.  scaling: one of SAW_ROPE_*; see include/saw_int4.h."""
+    _dev(cos_sin)
+    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be contiguous float32 [max_pos, rope_dim]")
+    rc = lib().saw_rope_table(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], base,
+                              scaling, factor, orig_max_pos, low, high, att_scale,
+                              _raw_stream(cos_sin, stream))
+    _raise(rc, "saw_rope_table")
+
+
+def _rows(t: torch.Tensor, like: torch.Tensor, what: str) -> int:
+    """Checks rows [T, heads, D] with only the token dimension strided."""
+    s = t.stride()
+    if t.dtype is not like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2] \
+            or s[2] != 1 or (s[1] != t.shape[2] and t.shape[1] != 1):
+        raise ValueError(f"{what} must be [T, heads, D] rows like k's type, each token's contiguous")
+    # (a single token's stride is whatever the view says; it is never used)
+    return s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def saw_rope_append(q, k: torch.Tensor, v, positions: torch.Tensor, cos_sin: torch.Tensor,
+                    slot_mapping: torch.Tensor, q_out, k_cache: torch.Tensor, v_cache,
+                    num_pages: int, page_size: int, rotate_k: bool, rotate_v: bool, block_h: int,
+                    interleaved: bool = False, dev_status=None, stream=None,
+                    meta_bf16: bool = False) -> None:
+    """Rotary positions on q and k, then the append of k and v.  q, q_out:
+    [T, Hq, D], k, v: [T, Hkv, D], bfloat16 or float16, token dim strided;
+    q (with q_out) and v may be None; q_out may be q.  positions,
+    slot_mapping: int32 [T]; cos_sin: float32 [max_pos, rope_dim]."""
+    _dev(k)
+    T, hkv, d = k.shape
+    fmt = _formats(k, meta_bf16)
+    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be contiguous float32 [max_pos, rope_dim]")
+    qs = qos = hq = 0
+    if q is not None:
+        hq = q.shape[1]
+        qs, qos = _rows(q, k, "q"), _rows(q_out, k, "q_out")
+        if q_out.shape[1] != hq:
+            raise ValueError("q_out must have q's heads")
+    if v is not None and v.shape[1] != hkv:
+        raise ValueError("v must have k's heads")
+    rc = lib().saw_rope_append(
+        _at(q), qs, k.data_ptr(), _rows(k, k, "k"), _at(v), _rows(v, k, "v") if v is not None else 0,
+        _i32(positions, "positions", T), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+        1 if interleaved else 0, _i32(slot_mapping, "slot_mapping", T), T, hq, hkv, d,
+        _at(q_out) if q is not None else None, qos, k_cache.data_ptr(),
+        _at(v_cache) if v is not None else None, num_pages, page_size, int(rotate_k),
+        int(rotate_v), block_h, fmt, _i32(dev_status, "dev_status"), _raw_stream(k, stream))
+    _raise(rc, "saw_rope_append")
+
+
+def saw_prefix_decode_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int,
+                                      num_kv_heads: int, head_dim: int, page_size: int,
+                                      max_prefix_len: int, max_own_len: int) -> int:
+    return int(lib().saw_prefix_decode_workspace_bytes(num_seqs, num_groups, num_q_heads,
+                                                       num_kv_heads, head_dim, page_size,
+                                                       max_prefix_len, max_own_len))
+
+
+def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           cu_group_seqs: torch.Tensor, prefix_lens: torch.Tensor,
+                           max_prefix_len: int, max_own_len: int, num_kv_heads: int,
+                           num_pages: int, page_size: int, rotate_k: bool, rotate_v: bool,
+                           block_h: int, out: torch.Tensor, workspace=None, sm_scale: float = 0.0,
+                           dev_status=None, stream=None, meta_bf16: bool = False) -> None:
+    """Decode of groups of sequences that share their first pages.  q:
+    bfloat16 or float16 [B, Hq, 128] contiguous; out: the same shape, float32
+    or q's type; cu_group_seqs: int32 [groups + 1], prefix_lens: int32
+    [groups]; workspace: saw_prefix_decode_workspace_bytes() bytes,
+    zero-filled before its first use."""
+    _dev(q)
+    B, hq, d = q.shape
+    fmt = _formats(q, meta_bf16)
+    if out.dtype is q.dtype:
+        fmt |= SAW_FMT_OUT_INPUT
+    elif out.dtype is not torch.float32:
+        raise ValueError("out must be float32 or q's type")
+    if not (q.is_contiguous() and out.is_contiguous() and out.shape == q.shape):
+        raise ValueError("q and out must be contiguous and of one shape")
+    groups = prefix_lens.numel()
+    if block_tables.shape[0] != B:
+        raise ValueError(f"block_tables must have {B} rows, not {block_tables.shape[0]}")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = lib().saw_prefix_decode_int4(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _i32(block_tables, "block_tables"), block_tables.shape[1], _i32(seq_lens, "seq_lens", B),
+        _i32(cu_group_seqs, "cu_group_seqs", groups + 1), _i32(prefix_lens, "prefix_lens"),
+        groups, B, max_prefix_len, max_own_len, hq, num_kv_heads, d, num_pages, page_size,
+        int(rotate_k), int(rotate_v), block_h, sm_scale, out.data_ptr(), _at(workspace), ws_bytes,
+        fmt, _i32(dev_status, "dev_status"), _raw_stream(q, stream))
+    _raise(rc, "saw_prefix_decode_int4")
 
 
 # ---------------------------------------------------------------- *_ex twins

@@ -50,10 +50,17 @@
 //    split of a (sequence, kv-head) to finish merges them, normalizes and
 //    applies the inverse rotation to V's output.  With one split the CTA
 //    finishes the row itself.  No CTA waits for another.
+//  * SHARED (saw_prefix_decode_int4's second pass): the sequence's first
+//    whole pages that its group shares were attended by the prefix kernel;
+//    this CTA attends over the rest, and the merge takes the prefix kernel's
+//    partials as further splits.  It is launched right behind that kernel and
+//    waits for it only when it merges, so its page copies overlap the other's
+//    tail.
 #include <type_traits>
 
 #include "saw_device.cuh"
 #include "saw_int4.h"
+#include "saw_prefix.cuh"
 #include "saw_quant_row.cuh"
 
 namespace saw {
@@ -214,9 +221,10 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves
 // zero in the second half of the D dims, v >= 4 one of the second, zero in
 // the first half; each column's output is its own half.  The tensor cores do the
 // zero products; every per-tile cost is shared by the two kv-heads.
-template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false>
+template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
   static_assert(!APPEND || D == kHeadDim, "the fused step is built for head_dim 128");
+  static_assert(!SHARED || (D == kHeadDim && !APPEND && !PAIR), "the shared-prefix pass is built for head_dim 128");
   static_assert(!PAIR || (!PACKED && !APPEND), "pairs use the wide form, without the fused step");
   using C = Cfg<D, P, PAIR>;
   using DM = Dims<D>;
@@ -227,8 +235,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // unless the caller declared that it writes neither the tables nor the
   // pages: then the page copies start first and the wait comes just before q
   // and the new token are read (and before anything is written).
+  // SHARED behind a prefix kernel: that kernel writes only the partials read
+  // by the merge and itself waited for everything before it, so nothing here
+  // waits until then.
+  const bool behind = SHARED && p.prefix.ctas > 0;
   const bool early = p.early_pages != 0;
-  if (!early) pdl_wait_then_release();
+  if (!early && !behind) pdl_wait_then_release();
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
   int32_t* stage_ok = reinterpret_cast<int32_t*>(smem + C::kOffOk);
@@ -257,18 +269,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     if (split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     L = 0;
   }
+  PrefixGroup pg{0, 0, 0, 0, 0, 0, 0};
+  uint32_t prefix_tiles = 0;
+  int skip_pages = 0;
+  if constexpr (SHARED) {
+    // max_seq_len bounds the whole sequence here, max_own_len what follows
+    // the prefix.  A length inside the prefix is an error (0: an idle row).
+    pg = prefix_find_seq(p.prefix, seq, P, p.group, p.num_kv_heads, p.num_seqs, lane,
+                         p.dev_status, &prefix_tiles);
+    if (L < pg.tokens || L - pg.tokens > p.max_own_len) {
+      if (L != 0 && split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+      pg.tokens = 0;
+      L = 0;
+    }
+    if (!behind) pg.tokens = 0;  // no prefix pass ran: every page is read here
+    L -= pg.tokens;
+    skip_pages = pg.tokens / P;
+  }
   const int n_pages = (L + P - 1) / P;
   const int p_begin = split * p.pages_per_split;
   const int p_end = min(n_pages, p_begin + p.pages_per_split);
   const bool direct = (p.num_splits == 1);
 
-  if (p_begin >= p_end) {
-    // nothing to attend over here; an empty sequence still owes a zero row
-    if (split == 0 && n_pages == 0) {
-      if (early) pdl_wait_then_release();
-      for (int idx = tid; idx < G * kOutD; idx += kThreads)
-        p.out[(int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx] = 0.0f;
+  auto store_out = [&](int idx, float o) {
+    const int64_t at = (int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx;
+    if constexpr (SHARED) {
+      // the one rounding of a 16-bit output
+      if (p.out16) {
+        p.out16[at] = p.in_f16 ? __half_as_ushort(__float2half_rn(o))
+                               : __bfloat16_as_ushort(__float2bfloat16_rn(o));
+        return;
+      }
     }
+    p.out[at] = o;
+  };
+  // (a sequence that ends with its prefix still merges the prefix's partials)
+  if (p_begin >= p_end && !(SHARED && split == 0 && n_pages == 0 && pg.tokens > 0)) {
+    // nothing to attend over here; an empty sequence still owes a zero row
+    if (early || behind) {
+      // (behind a prefix kernel every CTA waits, so that this grid does not
+      // complete before that one)
+      if (behind || (split == 0 && n_pages == 0)) pdl_wait_then_release();
+    }
+    if (split == 0 && n_pages == 0)
+      for (int idx = tid; idx < G * kOutD; idx += kThreads) store_out(idx, 0.0f);
     return;
   }
 
@@ -282,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   uint8_t* ring = smem + warp * kStages * C::kStage;
   uint64_t* wbars = bars + warp * kStages;
   int32_t* wok = stage_ok + warp * kStages;
-  const int32_t* btab = p.block_tables + int64_t(seq) * p.max_blocks;
+  const int32_t* btab = p.block_tables + int64_t(seq) * p.max_blocks + skip_pages;
 
   // the (page, kv-head) chunk index of this warp's step i (-1: invalid page)
   auto chunk_id = [&](int i) {
@@ -973,7 +1017,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // what lets the last arrival wait for the others' partials below.  The
   // returned count is needed only after the CTA's own reduction, so the
   // round trip overlaps it.
-  const int ns = (n_pages + p.pages_per_split - 1) / p.pages_per_split;  // splits with pages
+  // splits with pages (one that only merges the prefix counts too)
+  const int ns = SHARED ? max((n_pages + p.pages_per_split - 1) / p.pages_per_split, 1)
+                        : (n_pages + p.pages_per_split - 1) / p.pages_per_split;
   uint32_t* tk = p.tickets + 2 * (int64_t(seq) * p.num_kv_heads + kvh);  // {arrived, published}
   uint32_t arrived = 0;
   if (!direct && tid == 0)
@@ -1071,9 +1117,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       if (w < nw) num += red_acc[(w * kMaxGroup + h) * kRedStride + red_col(dd)] * wgt[w * kMaxGroup + h];
-    if (direct) {
+    if (direct && !SHARED) {
       const float den = tot[h];
       qs[h * D + dd] = (den > 0.0f) ? num / den : 0.0f;
+    } else if (direct) {
+      qs[h * D + dd] = num;
     } else {
       // publish the partial, and keep it here in case this split merges
       // (den and M stay in tot)
@@ -1087,6 +1135,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
   }
 
+  bool merge_ok = true;
   if (!direct) {
     if (tid == 0) {
       // merge protocol, part 2: the split whose arrival completed the count
@@ -1102,6 +1151,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       // publish: release (cumulative over the barrier above) orders this
       // CTA's partials before the count the merging split waits for
       if (tid == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(tk + 1) : "memory");
+      if (behind) pdl_wait_then_release();
       return;
     }
     // ---- the last split to arrive: wait (bounded) until every other split
@@ -1125,7 +1175,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       flag[1] = ok ? 1 : 0;  // a word of its own: flag[0] may still be read
     }
     __syncthreads();
-    const bool merge_ok = flag[1] != 0;
+    merge_ok = flag[1] != 0;
+  }
+  int np = 0;                     // partials of the prefix pass, after the splits'
+  int pre_row = 0;                // this sequence's first row in its unit
+  const float4* pre_o = nullptr;  // the first of them
+  const float2* pre_ml = nullptr;
+  if constexpr (SHARED) {
+    if (behind) pdl_wait_then_release();  // the prefix kernel's partials are complete
+    if (pg.tokens > 0) {
+      const uint32_t chunk = prefix_chunk(prefix_tiles, p.prefix.ctas);
+      const int per = prefix_seqs_per_block(p.group);
+      const int blk = (seq - pg.first) / per;
+      const uint32_t u = uint32_t(kvh) * pg.blocks + blk;
+      const uint32_t t0 = pg.tile0 + u * pg.tiles;
+      const uint32_t c0 = t0 / chunk, c1 = (t0 + pg.tiles - 1) / chunk;
+      np = int(c1 - c0) + 1;
+      pre_row = (seq - pg.first - blk * per) * p.group;
+      const int64_t slot = int64_t(pg.unit0) + u + c0;
+      pre_o = reinterpret_cast<const float4*>(p.prefix.part) + prefix_part_index(slot, 0);
+      pre_ml = reinterpret_cast<const float2*>(p.prefix.part_ml) + slot * kPrefixRows;
+    }
+    __syncthreads();  // tot and qs are complete (one split: nothing above met)
+  }
+  if (!direct || SHARED) {
+    const int nt = ns + np;
     // item = (head, 4 dims); four threads per item share the splits.  Every
     // load is issued before any is used (one round of L2 latency).
     constexpr int kMaxSplitsPerThread = 8;
@@ -1134,7 +1208,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const int t = base + tid;
       const int item = t >> 2, part = t & 3;
       const bool active = item < G * kItems;
-      const int h = active ? item / kItems : 0, ch = item % kItems;
+      // (SHARED: heads side by side, as the prefix's partials lie)
+      const int h = !active ? 0 : SHARED ? item % G : item / kItems;
+      const int ch = !active ? 0 : SHARED ? item / G : item % kItems;
       const int64_t row0 = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits;
       const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row0;
       const float4* po = reinterpret_cast<const float4*>(p.part_o + row0 * D) + ch;
@@ -1142,13 +1218,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       float M = -INFINITY;
       float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float den = 0.0f;
-      for (int sp0 = part; sp0 < ns; sp0 += 4 * kMaxSplitsPerThread) {
+      for (int sp0 = part; sp0 < nt; sp0 += 4 * kMaxSplitsPerThread) {
         float2 v[kMaxSplitsPerThread];
         float4 o[kMaxSplitsPerThread];
 #pragma unroll
         for (int u = 0; u < kMaxSplitsPerThread; ++u) {
           const int sp = sp0 + 4 * u;
           const bool mine = sp == split;
+          if constexpr (SHARED) {
+            if (sp >= ns) {
+              const bool in = active && sp < nt;
+              const int row = pre_row + h;
+              v[u] = in ? __ldcg(pre_ml + int64_t(sp - ns) * kPrefixRows + row) : make_float2(-INFINITY, 0.0f);
+              o[u] = in ? __ldcg(pre_o + prefix_part_index(sp - ns, row >> 7) + ch * 128 + (row & 127))
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              continue;
+            }
+          }
           const bool in = active && sp < ns && (mine || merge_ok);
           v[u] = !in ? make_float2(-INFINITY, 0.0f)
                      : mine ? make_float2(tot[2 * kMaxGroup + h], tot[h]) : __ldcg(&ml[sp]);
@@ -1207,17 +1293,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   for (int idx = tid; idx < G * kOutD; idx += kThreads) {
     const int h = idx / kOutD, dd = idx - h * kOutD;
     const float o = PAIR ? qs[h * D + (h >> 2) * kOutD + dd] : qs[idx];
-    p.out[(int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx] = o * post;
+    store_out(idx, o * post);
   }
 }
 
 // Launched with programmatic stream serialization: the kernel may start while
 // the previous kernel in the stream drains; it waits for it (griddepcontrol)
 // before reading anything.
-template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false>
+template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false>
 cudaError_t launch_p(const DecodeParams& p, cudaStream_t stream) {
   using C = Cfg<D, P, PAIR>;
-  auto kernel = paged_decode_kernel<D, P, PACKED, APPEND, BFM, PAIR>;
+  auto kernel = paged_decode_kernel<D, P, PACKED, APPEND, BFM, PAIR, SHARED>;
   cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
@@ -1237,6 +1323,10 @@ cudaError_t launch_p(const DecodeParams& p, cudaStream_t stream) {
 template <int D, int P, bool BFM>
 cudaError_t launch_page_m(const DecodeParams& p, cudaStream_t stream) {
   const bool packed = p.group <= kMaxGroup / 2;
+#ifdef SAW_DECODE_SHARED
+  return packed ? launch_p<D, P, true, false, BFM, false, true>(p, stream)
+                : launch_p<D, P, false, false, BFM, false, true>(p, stream);
+#else
   if constexpr (D == kHeadDim) {
     if (p.append)
       return packed ? launch_p<D, P, true, true, BFM>(p, stream)
@@ -1244,6 +1334,7 @@ cudaError_t launch_page_m(const DecodeParams& p, cudaStream_t stream) {
   }
   return packed ? launch_p<D, P, true, false, BFM>(p, stream)
                 : launch_p<D, P, false, false, BFM>(p, stream);
+#endif
 }
 
 template <int D>
@@ -1261,7 +1352,13 @@ cudaError_t launch_dim(const DecodeParams& p, cudaStream_t stream) {
 
 #define SAW_CAT2(a, b) a##b
 #define SAW_CAT(a, b) SAW_CAT2(a, b)
-#ifndef SAW_DECODE_OTHER_DIMS
+#if defined(SAW_DECODE_SHARED)
+// the shared-prefix decode's second pass
+cudaError_t SAW_CAT(launch_paged_decode_shared_w, SAW_DECODE_WARPS)(const DecodeParams& p,
+                                                                    cudaStream_t stream) {
+  return launch_dim<kHeadDim>(p, stream);
+}
+#elif !defined(SAW_DECODE_OTHER_DIMS)
 // head_dim 128 (and the fused decode step)
 cudaError_t SAW_CAT(launch_paged_decode_w, SAW_DECODE_WARPS)(const DecodeParams& p,
                                                              cudaStream_t stream) {

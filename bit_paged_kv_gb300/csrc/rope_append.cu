@@ -1,0 +1,289 @@
+// rope_append.cu -- rotary positions on q and k fused with the rotated,
+// quantized append of k and v, and the table of cosines and sines it reads.
+//
+// Rotary: the first r = rope_dim elements of a head are r/2 pairs; pair i of
+// a token at position p is turned by the angle p w_i:
+//   y0 = RN(RN(x0 c) - RN(x1 s)),  y1 = RN(RN(x1 c) + RN(x0 s)),
+// in binary32, products rounded separately, so the result is fixed to the
+// bit by the table.  Pairs are (i, i + r/2) or, interleaved, (2i, 2i + 1).
+// k goes on in binary32 into the append's butterfly and quantizer (the rule
+// of saw_quantize_append from "widen to binary32" on); q is rounded once, to
+// the input type.
+#include "saw_device.cuh"
+#include "saw_int4.h"
+#include "saw_quant_row.cuh"
+
+namespace saw {
+namespace {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ------------------------------------------------------------ table
+//
+// The angle of position p is p w_i / 2 pi turns.  turns_i arrives as a 64-bit
+// binary fraction, so p * turns_i modulo 2^64 is the exact angle modulo one
+// turn (error below p 2^-64 turns); its top two bits, rounded, are the
+// quarter, the rest an angle within 1/8 turn that binary32 holds to 2^-27
+// turns: no large argument ever reaches the sine.
+constexpr int kTableThreads = 256;
+
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const RopeTableParams p) {
+  pdl_wait_then_release();
+  __shared__ uint64_t turns[kRopeMaxPairs];
+  for (int i = threadIdx.x; i < p.pairs; i += kTableThreads) turns[i] = p.turns[i];
+  __syncthreads();
+  const int quads = p.pairs / 4;  // four pairs per thread
+  const int64_t items = int64_t(p.max_pos) * quads;
+  for (int64_t it = int64_t(blockIdx.x) * kTableThreads + threadIdx.x; it < items;
+       it += int64_t(gridDim.x) * kTableThreads) {
+    const int64_t pos = it / quads;
+    const int i0 = int(it - pos * quads) * 4;
+    float cv[4], sv[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t hi = uint32_t((uint64_t(pos) * turns[i0 + k]) >> 32);
+      const uint32_t quarter = (hi + 0x20000000u) >> 30;
+      const float x = float(int32_t(hi - (quarter << 30))) * 0x1p-31f;  // half turns, |x| <= 1/4
+      float s, c;
+      sincospif(x, &s, &c);
+      const bool odd = quarter & 1;
+      const float a = odd ? s : c, b = odd ? c : s;
+      cv[k] = ((quarter + 1) & 2) ? -a : a;  // quarters 1 and 2
+      sv[k] = (quarter & 2) ? -b : b;        // quarters 2 and 3
+      cv[k] *= p.att;
+      sv[k] *= p.att;
+    }
+    float* row = p.cos_sin + pos * (2 * p.pairs);
+    *reinterpret_cast<float4*>(row + i0) = make_float4(cv[0], cv[1], cv[2], cv[3]);
+    *reinterpret_cast<float4*>(row + p.pairs + i0) = make_float4(sv[0], sv[1], sv[2], sv[3]);
+  }
+}
+
+// ------------------------------------------------------------ one row per warp
+//
+// Lane l holds elements E l .. E l + E - 1 (E = D / 32).  Any size, layout and
+// stride; the bulk kernel takes over for large batches.
+constexpr int kRowWarps = 4;
+
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t* src, bool f16, float (&x)[D / 32]) {
+  constexpr int E = D / 32;
+  if constexpr (E == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(src);
+    x[0] = in_lo(w, f16);
+    x[1] = in_hi(w, f16);
+  } else {
+    uint32_t ws[E / 2];
+    if constexpr (E == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(src);
+      ws[0] = w.x;
+      ws[1] = w.y;
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(src);
+      ws[0] = w.x;
+      ws[1] = w.y;
+      ws[2] = w.z;
+      ws[3] = w.w;
+    }
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+      x[2 * j] = in_lo(ws[j], f16);
+      x[2 * j + 1] = in_hi(ws[j], f16);
+    }
+  }
+}
+
+// Turns the lane's elements in place.  cs: the token's row of the table.
+template <int D>
+__device__ __forceinline__ void turn_row(float (&x)[D / 32], const float* cs, int r, bool inter,
+                                         int lane) {
+  constexpr int E = D / 32;
+  const int half = r >> 1;
+  const int d0 = E * lane;
+  if (inter) {
+    if (d0 < r) {
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const int i = (d0 + e) >> 1;
+        const float c = __ldg(cs + i), s = __ldg(cs + half + i);
+        const float a = x[e], b = x[e + 1];
+        x[e] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+        x[e + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+      }
+    }
+  } else {
+    // the partner element sits `half` elements away, half / E lanes (r is a
+    // multiple of 16, so half is one of E)
+    const bool low = d0 < half, in = d0 < r;
+    const int hop = half / E;
+    const int from = in ? (low ? lane + hop : lane - hop) : lane;
+    const int i0 = low ? d0 : d0 - half;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float o = __shfl_sync(kAll, x[e], from);
+      if (in) {
+        const float c = __ldg(cs + i0 + e), s = __ldg(cs + half + i0 + e);
+        const float u = __fmul_rn(x[e], c), v = __fmul_rn(o, s);
+        x[e] = low ? __fsub_rn(u, v) : __fadd_rn(u, v);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kRowWarps) rope_append_row_kernel(const RopeParams p) {
+  pdl_wait_then_release();
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int hkv = p.num_kv_heads;
+  const int per = p.num_q_heads + hkv * p.num_tensors;  // rows of a token: q heads, k, v
+  const int64_t gw = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (gw >= int64_t(p.num_tokens) * per) return;
+  const int t = int(gw / per), j = int(gw - int64_t(t) * per);
+  const bool f16 = p.in_f16 != 0;
+  const bool is_q = j < p.num_q_heads;
+  const int tensor = is_q || j < p.num_q_heads + hkv ? 0 : 1;
+  const int hd = is_q ? j : j - p.num_q_heads - tensor * hkv;
+  const bool turned = is_q || tensor == 0;
+
+  int32_t slot = -1, pos = 0;
+  if (!is_q) slot = p.slot_mapping[t];
+  if (turned) {
+    pos = p.positions[t];
+    if (pos < 0 || pos >= p.max_pos) {  // the token is skipped and reported
+      if (lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+      return;
+    }
+  }
+  if (!is_q) {
+    if (slot == -1) return;
+    if (slot < 0 || int64_t(slot) >= p.num_slots) {
+      if (lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+      return;
+    }
+    if (!turned) {  // V of a token whose position is bad is skipped with its K
+      const int32_t q = p.positions[t];
+      if (q < 0 || q >= p.max_pos) return;
+    }
+  }
+  const uint16_t* src = is_q ? p.q + int64_t(t) * p.q_stride
+                             : (tensor ? p.v + int64_t(t) * p.v_stride : p.k + int64_t(t) * p.k_stride);
+  float x[E];
+  load_row<D>(src + int64_t(hd) * D + E * lane, f16, x);
+  if (turned)
+    turn_row<D>(x, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, p.interleaved != 0, lane);
+
+  if (is_q) {
+    uint16_t* dst = p.q_out + int64_t(t) * p.q_out_stride + int64_t(hd) * D + E * lane;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) w[e / 2] = f16 ? pack_half2(x[e], x[e + 1]) : pack_bf162(x[e], x[e + 1]);
+    if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
+    else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+
+  if (tensor ? p.rotate_v : p.rotate_k) {
+    const int h = p.block_h;
+#pragma unroll
+    for (int s = 1; s < E; s <<= 1) {
+      if (s < h) {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (!(i & s)) {
+            const float a = x[i], b = x[i + s];
+            x[i] = __fadd_rn(a, b);
+            x[i + s] = __fsub_rn(a, b);
+          }
+      }
+    }
+    for (int s = E; s < h; s <<= 1) {
+      const int m = s / E;
+      const bool upper = (lane & m) != 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float o = __shfl_xor_sync(kAll, x[i], m);
+        x[i] = upper ? __fsub_rn(o, x[i]) : __fadd_rn(x[i], o);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = __fmul_rn(x[i], p.c_h);
+  }
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int i = 1; i < E; ++i) {
+    mn = fminf(mn, x[i]);
+    mx = fmaxf(mx, x[i]);
+  }
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) {
+    mn = fminf(mn, __shfl_xor_sync(kAll, mn, m));
+    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, m));
+  }
+  const RowMeta m = row_meta(mn, mx, p.meta_bf16 != 0);
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    int q = __float2int_rn(__fmul_rn(__fsub_rn(x[i], m.z), m.rcp));
+    q = min(max(q, 0), 15);
+    codes |= uint32_t(q) << (4 * i);
+  }
+  const int P = p.page_size;
+  const int page = slot >> p.page_shift, off = slot & (P - 1);
+  uint8_t* chunk = (tensor ? p.v_cache : p.k_cache) + (int64_t(page) * hkv + hd) * int64_t(P * (D / 2 + 4));
+  if constexpr (E == 2) chunk[off * (D / 2) + lane] = uint8_t(codes);
+  else if constexpr (E == 4) reinterpret_cast<uint16_t*>(chunk + off * (D / 2))[lane] = uint16_t(codes);
+  else reinterpret_cast<uint32_t*>(chunk + off * (D / 2))[lane] = codes;
+  if (lane == 0)
+    *reinterpret_cast<uint32_t*>(chunk + P * (D / 2) + 4 * off) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
+}
+
+template <int D>
+cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
+  const int64_t warps = int64_t(p.num_tokens) * (p.num_q_heads + p.num_kv_heads * p.num_tensors);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((warps + kRowWarps - 1) / kRowWarps));
+  cfg.blockDim = dim3(32 * kRowWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_append_row_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t stream) {
+  const int64_t items = int64_t(p.max_pos) * (p.pairs / 4);
+  const int64_t want = (items + kTableThreads - 1) / kTableThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(want < int64_t(8) * sms ? want : int64_t(8) * sms));
+  cfg.blockDim = dim3(kTableThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_table_kernel, p);
+}
+
+cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream) {
+  (void)sms;
+  switch (p.head_dim) {
+    case 64: return launch_rows<64>(p, stream);
+    case 128: return launch_rows<128>(p, stream);
+    case 256: return launch_rows<256>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace saw

@@ -175,6 +175,7 @@ const char* saw_status_string(int32_t status) {
     case SAW_ERR_CUDA: return "SAW_ERR_CUDA";
     case SAW_ERR_DEVICE_INDEX: return "SAW_ERR_DEVICE_INDEX";
     case SAW_ERR_DEVICE_TIMEOUT: return "SAW_ERR_DEVICE_TIMEOUT";
+    case SAW_ERR_DEVICE_PAGES: return "SAW_ERR_DEVICE_PAGES";
     default: return "SAW_ERR_UNKNOWN";
   }
 }
@@ -534,6 +535,288 @@ int32_t saw_prefill_attn_int4(const void* q, const int32_t* cu_q_lens, const voi
                                   max_seq_len, num_q_heads, num_kv_heads, head_dim, num_pages,
                                   page_size, rotate_k, rotate_v, block_h, sm_scale, out, 0,
                                   dev_status, stream);
+}
+
+// ---------------------------------------------------------------- shared prefix
+
+namespace {
+
+// How a shared-prefix decode runs: the decode kernel's split plan covers
+// `plan_len` tokens per sequence, its workspace comes first, then the prefix
+// pass's partials.
+struct PrefixPlan {
+  int32_t ctas;         // 0: no prefix pass, every sequence reads its own pages
+  int32_t plan_len;
+  size_t split_bytes, part_bytes, ml_bytes;
+};
+
+int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                    int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                    int32_t max_prefix_len, int32_t max_own_len, PrefixPlan* out) {
+  if (num_seqs < 0 || num_groups < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
+      max_prefix_len < 0 || max_own_len < 0 || int64_t(max_prefix_len) + max_own_len > INT32_MAX)
+    return SAW_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads) return SAW_ERR_INVALID_ARG;
+  if (head_dim != kHeadDim || !page_size_ok(page_size) ||
+      num_q_heads / num_kv_heads > saw::kMaxGroup || num_seqs > 65535 || num_kv_heads > 65535)
+    return SAW_ERR_UNSUPPORTED;
+  PrefixPlan p{};
+  p.ctas = 0;
+  p.plan_len = max_prefix_len + max_own_len;
+  p.split_bytes = saw_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                             page_size, p.plan_len, 0);
+  p.split_bytes = (p.split_bytes + 255) / 256 * 256;
+  *out = p;
+  return SAW_OK;
+}
+
+}  // namespace
+
+size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t page_size,
+                                         int32_t max_prefix_len, int32_t max_own_len) {
+  PrefixPlan plan;
+  if (plan_prefix(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, page_size,
+                  max_prefix_len, max_own_len, &plan) != SAW_OK)
+    return 0;
+  return plan.split_bytes + plan.part_bytes + plan.ml_bytes;
+}
+
+int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* cu_group_seqs,
+                               const int32_t* prefix_lens, int32_t num_groups, int32_t num_seqs,
+                               int32_t max_prefix_len, int32_t max_own_len, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                               int32_t page_size, int32_t rotate_k, int32_t rotate_v,
+                               int32_t block_h, float sm_scale, void* out, void* workspace,
+                               size_t workspace_bytes, int32_t formats, int32_t* dev_status,
+                               void* stream) {
+  const bool out16 = (formats & SAW_FMT_OUT_INPUT) != 0;
+  formats &= ~int32_t(SAW_FMT_OUT_INPUT);
+  PrefixPlan plan;
+  int32_t rc = plan_prefix(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, page_size,
+                           max_prefix_len, max_own_len, &plan);
+  if (rc != SAW_OK) return rc;
+  if (num_seqs > 0 && num_groups > 0 && (!cu_group_seqs || !prefix_lens))
+    return SAW_ERR_INVALID_ARG;
+  if (max_blocks_per_seq < 0 || int64_t(max_blocks_per_seq) * page_size < max_prefix_len)
+    return SAW_ERR_INVALID_ARG;
+  const size_t need = plan.split_bytes + plan.part_bytes + plan.ml_bytes;
+  if (num_seqs > 0 && need > 0 &&
+      (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return SAW_ERR_INVALID_ARG;
+  saw::DecodeParams p{};
+  // (the tables need not hold max_prefix_len + max_own_len tokens, which may
+  // belong to different sequences: the kernel checks each length against them)
+  rc = prepare_decode(p, q, k_cache, v_cache, block_tables, INT32_MAX, seq_lens,
+                      num_seqs, plan.plan_len, num_q_heads, num_kv_heads, head_dim, num_pages,
+                      page_size, rotate_k, rotate_v, block_h, sm_scale, static_cast<float*>(out),
+                      workspace, workspace_bytes, 0, formats, dev_status);
+  if (rc != SAW_OK || num_seqs == 0) return rc;
+  if (out16) p.out16 = static_cast<uint16_t*>(out);
+  p.max_blocks = max_blocks_per_seq;
+  p.max_seq_len = int32_t(std::min<int64_t>(int64_t(max_prefix_len) + max_own_len,
+                                            int64_t(max_blocks_per_seq) * page_size));
+  p.max_own_len = max_own_len;
+  p.prefix.cu_groups = cu_group_seqs;
+  p.prefix.prefix_lens = prefix_lens;
+  p.prefix.num_groups = num_groups;
+  p.prefix.max_prefix_len = max_prefix_len;
+  p.prefix.ctas = plan.ctas;
+  const cudaError_t err = p.warps == 4   ? saw::launch_paged_decode_shared_w4(p, static_cast<cudaStream_t>(stream))
+                          : p.warps == 8 ? saw::launch_paged_decode_shared_w8(p, static_cast<cudaStream_t>(stream))
+                                         : saw::launch_paged_decode_shared_w16(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- tables
+
+int32_t saw_build_tables(const int32_t* src_tables, int32_t num_src_rows, int32_t src_blocks,
+                         const int32_t* src_rows, const int32_t* cached_lens,
+                         const int32_t* new_lens, const int32_t* free_pages, int32_t max_free,
+                         const int32_t* num_free, int32_t num_seqs, int32_t max_tokens,
+                         int32_t num_pages, int32_t page_size, int32_t* block_tables,
+                         int32_t max_blocks_per_seq, int32_t* seq_lens, int32_t* cu_q_lens,
+                         int32_t* slot_mapping, int32_t* positions, int32_t* pages_taken,
+                         int32_t* dev_status, void* stream) {
+  if (num_seqs < 0 || max_tokens < 0 || num_pages < 0 || max_free < 0 || max_blocks_per_seq < 0 ||
+      num_src_rows < 0 || src_blocks < 0)
+    return SAW_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size) || num_seqs > 65535) return SAW_ERR_UNSUPPORTED;
+  if (int64_t(num_pages) * page_size > INT32_MAX ||
+      int64_t(max_blocks_per_seq) * page_size > INT32_MAX)
+    return SAW_ERR_UNSUPPORTED;
+  if (!cu_q_lens || (max_tokens > 0 && !slot_mapping) || (max_free > 0 && !free_pages))
+    return SAW_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!new_lens || !seq_lens || (max_blocks_per_seq > 0 && !block_tables)))
+    return SAW_ERR_INVALID_ARG;
+  // every CTA reads the lengths while others write the results
+  if (seq_lens && (seq_lens == cached_lens || seq_lens == new_lens)) return SAW_ERR_INVALID_ARG;
+  if (src_tables && src_tables == block_tables &&
+      (src_rows || src_blocks != max_blocks_per_seq || num_src_rows < num_seqs))
+    return SAW_ERR_INVALID_ARG;
+  saw::TablesParams p{};
+  p.src_tables = src_tables;
+  p.src_rows = src_rows;
+  p.cached_lens = cached_lens;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.num_free = num_free;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.cu_q_lens = cu_q_lens;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.pages_taken = pages_taken;
+  p.dev_status = dev_status;
+  p.num_src_rows = num_src_rows;
+  p.src_blocks = src_blocks;
+  p.max_free = max_free;
+  p.num_seqs = num_seqs;
+  p.max_tokens = max_tokens;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+  const int sms = sm_count();
+  const cudaError_t err = saw::launch_build_tables(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- rotary
+
+int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double base,
+                       int32_t scaling, double factor, int32_t orig_max_pos, double low,
+                       double high, float att_scale, void* stream) {
+  if (max_pos < 0 || rope_dim <= 0) return SAW_ERR_INVALID_ARG;
+  if (rope_dim % 16 || rope_dim > 2 * saw::kRopeMaxPairs) return SAW_ERR_UNSUPPORTED;
+  if (!(base > 1.0) || std::isinf(base) || !(factor > 0.0) || std::isinf(factor))
+    return SAW_ERR_INVALID_ARG;
+  if (!(att_scale >= 0.0f) || std::isinf(att_scale)) return SAW_ERR_INVALID_ARG;
+  if (scaling < SAW_ROPE_NONE || scaling > SAW_ROPE_BANDS) return SAW_ERR_INVALID_ARG;
+  const bool ranged = scaling == SAW_ROPE_YARN || scaling == SAW_ROPE_BANDS;
+  if (ranged) {
+    if (orig_max_pos <= 0) return SAW_ERR_INVALID_ARG;
+    if (low == 0.0 && high == 0.0) {
+      low = 1.0;
+      high = scaling == SAW_ROPE_YARN ? 32.0 : 4.0;
+    }
+    if (!(low > 0.0) || !(high > low) || std::isinf(high)) return SAW_ERR_INVALID_ARG;
+  }
+  if (max_pos == 0) return SAW_OK;
+  if (!cos_sin || !aligned16(cos_sin)) return SAW_ERR_INVALID_ARG;
+
+  const double two_pi = 6.283185307179586476925286766559;
+  const double r = rope_dim;
+  saw::RopeTableParams p{};
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.pairs = rope_dim / 2;
+  double att = 1.0, b = base, lo = 0.0, hi = 0.0;
+  if (scaling == SAW_ROPE_NTK) b = base * std::pow(factor, r / (r - 2.0));
+  if (scaling == SAW_ROPE_YARN) {
+    // pair index at which a pair turns `beta` times in orig_max_pos positions
+    auto pair_of = [&](double beta) { return r * std::log(orig_max_pos / (two_pi * beta)) / (2.0 * std::log(base)); };
+    lo = std::max(std::floor(pair_of(high)), 0.0);
+    hi = std::min(std::ceil(pair_of(low)), r - 1.0);
+    att = 0.1 * std::log(factor) + 1.0;
+  }
+  for (int i = 0; i < p.pairs; ++i) {
+    double w = std::pow(b, -2.0 * i / r);
+    if (scaling == SAW_ROPE_LINEAR) w /= factor;
+    if (scaling == SAW_ROPE_YARN) {
+      const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+      w = w / factor * ramp + w * (1.0 - ramp);
+    }
+    if (scaling == SAW_ROPE_BANDS) {
+      const double turns = orig_max_pos * w / two_pi;
+      const double keep = std::min(std::max((turns - low) / (high - low), 0.0), 1.0);
+      w = (1.0 - keep) * w / factor + keep * w;
+    }
+    const double t = w / two_pi;
+    p.turns[i] = uint64_t(std::ldexp(t - std::floor(t), 64));
+  }
+  p.att = att_scale > 0.0f ? att_scale : float(att);
+  const int sms = sm_count();
+  const cudaError_t err = saw::launch_rope_table(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
+                        int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                        const int32_t* positions, const float* cos_sin, int32_t max_pos,
+                        int32_t rope_dim, int32_t interleaved, const int32_t* slot_mapping,
+                        int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, void* q_out, int64_t q_out_token_stride, void* k_cache,
+                        void* v_cache, int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                        int32_t rotate_v, int32_t block_h, int32_t formats, int32_t* dev_status,
+                        void* stream) {
+  if (num_tokens < 0 || num_kv_heads <= 0 || num_q_heads < 0 || num_pages < 0 || max_pos < 0)
+    return SAW_ERR_INVALID_ARG;
+  if (!formats_ok(formats)) return SAW_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !page_size_ok(page_size)) return SAW_ERR_UNSUPPORTED;
+  if (rope_dim <= 0 || rope_dim > head_dim) return SAW_ERR_INVALID_ARG;
+  if (rope_dim % 16) return SAW_ERR_UNSUPPORTED;
+  if ((rotate_k != 0 && rotate_k != 1) || (rotate_v != 0 && rotate_v != 1) ||
+      (interleaved != 0 && interleaved != 1))
+    return SAW_ERR_INVALID_ARG;
+  const bool has_v = v != nullptr, has_q = q != nullptr && num_q_heads > 0;
+  if (rotate_k || (has_v && rotate_v)) {
+    if (!pow2(block_h) || block_h > head_dim || head_dim % block_h) return SAW_ERR_INVALID_ARG;
+    if (!block_h_ok(block_h)) return SAW_ERR_UNSUPPORTED;
+  }
+  if (int64_t(num_tokens) * (int64_t(num_q_heads) + 2 * int64_t(num_kv_heads)) > INT32_MAX / 2)
+    return SAW_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return SAW_OK;
+  if (!k || !positions || !cos_sin || !slot_mapping || !k_cache || (has_v && !v_cache) ||
+      (has_q && !q_out))
+    return SAW_ERR_INVALID_ARG;
+  auto rows_ok = [&](const void* x, int64_t stride, int32_t heads) {
+    return aligned16(x) && stride >= int64_t(heads) * head_dim && (stride & 7) == 0;
+  };
+  if (!rows_ok(k, k_token_stride, num_kv_heads) || !aligned16(k_cache) || !aligned16(cos_sin) ||
+      (has_v && (!rows_ok(v, v_token_stride, num_kv_heads) || !aligned16(v_cache))) ||
+      (has_q && (!rows_ok(q, q_token_stride, num_q_heads) ||
+                 !rows_ok(q_out, q_out_token_stride, num_q_heads))))
+    return SAW_ERR_INVALID_ARG;
+  if (has_q && q_out == q && q_out_token_stride != q_token_stride) return SAW_ERR_INVALID_ARG;
+  saw::RopeParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.q_stride = q_token_stride;
+  p.k_stride = k_token_stride;
+  p.v_stride = v_token_stride;
+  p.q_out_stride = q_out_token_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.slot_mapping = slot_mapping;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.dev_status = dev_status;
+  p.num_slots = int64_t(num_pages) * page_size;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = has_q ? num_q_heads : 0;
+  p.num_kv_heads = num_kv_heads;
+  p.num_tensors = has_v ? 2 : 1;
+  p.head_dim = head_dim;
+  p.rope_dim = rope_dim;
+  p.max_pos = max_pos;
+  p.interleaved = interleaved;
+  p.rotate_k = rotate_k;
+  p.rotate_v = has_v ? rotate_v : 0;
+  p.block_h = block_h;
+  p.page_size = page_size;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+  p.c_h = (rotate_k || rotate_v) ? float(1.0 / std::sqrt(double(block_h))) : 1.0f;
+  p.in_f16 = (formats & SAW_FMT_F16_INPUT) ? 1 : 0;
+  p.meta_bf16 = (formats & SAW_FMT_BF16_META) ? 1 : 0;
+  const int sms = sm_count();
+  const cudaError_t err = saw::launch_rope_append(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- BF16 baseline

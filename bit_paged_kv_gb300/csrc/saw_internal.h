@@ -45,7 +45,94 @@ struct AppendParams {
 
 cudaError_t launch_quantize_append(const AppendParams& p, int num_tensors, cudaStream_t stream);
 
+// ---------------------------------------------------------------- tables
+
+struct TablesParams {
+  const int32_t* src_tables;    // [num_src_rows][src_blocks], or NULL (nothing cached)
+  const int32_t* src_rows;      // [B] row of src_tables of each request, or NULL (row b)
+  const int32_t* cached_lens;   // [B], or NULL (all 0)
+  const int32_t* new_lens;      // [B]
+  const int32_t* free_pages;    // [max_free]
+  const int32_t* num_free;      // device [1], or NULL (max_free)
+  int32_t* block_tables;        // [B][max_blocks]; may be src_tables
+  int32_t* seq_lens;            // [B]
+  int32_t* cu_q_lens;           // [B + 1]
+  int32_t* slot_mapping;        // [max_tokens]
+  int32_t* positions;           // [max_tokens], or NULL
+  int32_t* pages_taken;         // [1], or NULL
+  int32_t* dev_status;
+  int32_t num_src_rows;
+  int32_t src_blocks;
+  int32_t max_free;
+  int32_t num_seqs;
+  int32_t max_tokens;
+  int32_t max_blocks;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t page_shift;           // page_size = 1 << page_shift
+};
+
+cudaError_t launch_build_tables(const TablesParams& p, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- rotary
+
+constexpr int kRopeMaxPairs = 128;  // rope_dim <= 256
+
+struct RopeTableParams {
+  float* cos_sin;               // [max_pos][2 * pairs]
+  int32_t max_pos;
+  int32_t pairs;
+  float att;                    // factor on every cosine and sine
+  uint64_t turns[kRopeMaxPairs];  // turns per position, 2^-64 units
+};
+
+struct RopeParams {
+  const uint16_t* q;            // [T][Hq][D] with a token stride, or NULL with num_q_heads 0
+  const uint16_t* k;            // [T][Hkv][D]
+  const uint16_t* v;            // or NULL with num_tensors 1
+  uint16_t* q_out;              // [T][Hq][D]; may be q
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements
+  const int32_t* positions;     // [T]
+  const float* cos_sin;         // [max_pos][rope_dim]
+  const int32_t* slot_mapping;  // [T]
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int32_t* dev_status;
+  int64_t num_slots;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t num_tensors;          // 2 = K and V, 1 = K only
+  int32_t head_dim;
+  int32_t rope_dim;
+  int32_t max_pos;
+  int32_t interleaved;
+  int32_t rotate_k;
+  int32_t rotate_v;
+  int32_t block_h;
+  int32_t page_size;
+  int32_t page_shift;
+  float c_h;
+  int32_t in_f16;
+  int32_t meta_bf16;
+};
+
+cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream);
+
 // ---------------------------------------------------------------- decode
+
+// Groups of sequences that share their first pages, and the partial results
+// of the pass over those pages (saw_prefix.cuh).
+struct PrefixSide {
+  const int32_t* cu_groups;     // [num_groups + 1] first sequence of each group
+  const int32_t* prefix_lens;   // [num_groups] shared tokens
+  int32_t num_groups;
+  int32_t max_prefix_len;
+  int32_t ctas;                 // CTAs of the prefix pass; 0: none ran, nothing is shared
+  float* part;                  // numerators, 128 KB per slot
+  float* part_ml;               // (m, l) per row
+};
 
 struct DecodeParams {
   const uint16_t* q;            // [B][Hq][D] bfloat16 (binary16 if in_f16) bits
@@ -89,6 +176,10 @@ struct DecodeParams {
   int32_t head_dim;             // 128, or 64 / 256
   int32_t in_f16;               // 1: q, k_new and v_new are binary16
   int32_t meta_bf16;            // 1: the caches' (scale, zero) words are bfloat16
+  // shared-prefix decode only: the groups, and the output type
+  PrefixSide prefix;
+  int32_t max_own_len;          // bound on the tokens behind the prefix
+  uint16_t* out16;              // output in the input type instead of `out`, or NULL
   // 1: head_dim 64, GQA 4: each CTA serves two neighbouring kv-heads as one
   // head_dim-128 "pair" head with 8 q-head columns (part_o rows are 128
   // floats wide, the grid has num_kv_heads / 2 rows)
@@ -101,6 +192,10 @@ cudaError_t launch_paged_decode_w16(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_paged_decode_w8(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_paged_decode_w4(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_paged_decode_dims_w16(const DecodeParams& p, cudaStream_t stream);
+// the shared-prefix decode's second pass (the same source, SAW_DECODE_SHARED)
+cudaError_t launch_paged_decode_shared_w16(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_paged_decode_shared_w8(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_paged_decode_shared_w4(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_paged_decode_dims_w8(const DecodeParams& p, cudaStream_t stream);
 // head_dim 64 and 256 append (variants.cu); bulk appends run the tiled
 // kernels of quantize_append.cu

@@ -25,7 +25,10 @@
  * saw_prefill_attn_int4 (causal attention of a chunk of queries over the
  * same cache), the *_ex forms with binary16 inputs or bfloat16 scale/zero
  * metadata, and a BF16 paged cache with the same decode (saw_bf16_*), the
- * baseline the pages compare INT4 against.
+ * baseline the pages compare INT4 against.  saw_build_tables, saw_rope_table,
+ * saw_rope_append and saw_prefix_decode_int4 make the rest of a serving step
+ * around the cache: tables and slots from lengths, rotary positions fused
+ * with the append, and a decode that reads a shared prefix once per group.
  *
  * Readings taken where the pages are silent: Sylvester ordering of H, the
  * 1/sqrt(h) scale applied after an ascending-stride butterfly, one binary16
@@ -63,7 +66,8 @@ typedef enum saw_status {
   SAW_ERR_UNSUPPORTED = 2,    /* a shape this build has no kernel for */
   SAW_ERR_CUDA = 3,           /* a CUDA runtime error at launch */
   SAW_ERR_DEVICE_INDEX = 4,   /* device-side: a slot, page id or length out of range (skipped) */
-  SAW_ERR_DEVICE_TIMEOUT = 5  /* device-side: a bounded wait on a copy ran out */
+  SAW_ERR_DEVICE_TIMEOUT = 5, /* device-side: a bounded wait on a copy ran out */
+  SAW_ERR_DEVICE_PAGES = 6    /* device-side: the list of free pages ran out (saw_build_tables) */
 } saw_status;
 
 /* Human-readable name of a status code.  Never NULL. */
@@ -384,6 +388,184 @@ int32_t saw_prefill_attn_int4_ex(const void* q, const int32_t* cu_q_lens, const 
                                  int32_t rotate_k, int32_t rotate_v, int32_t block_h,
                                  float sm_scale, float* out, int32_t formats,
                                  int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A serving step around the cache.  The pages (gist.science s.1) place the
+ * method inside engines with paged KV and continuous batching; the four calls
+ * below are the steps of such an engine next to the append and the attention.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * saw_build_tables -- block tables, slot mapping, positions, lengths and row
+ * offsets of a batch, from the requests' lengths and a list of free pages.
+ *
+ * For request b with c = cached_lens[b] cached and n = new_lens[b] new tokens:
+ *   old = ceil(c / page_size), need = ceil((c + n) / page_size) - old,
+ *   off = the sum of need over the requests before b;
+ *   block_tables[b][e] = src row's entry e for e < old, free_pages[off + e -
+ *   old] for old <= e < old + need; later entries are left as they were;
+ *   token i < n: position c + i, slot = entry * page_size + offset;
+ *   seq_lens[b] = c + n; cu_q_lens = exclusive sums of n (saw_prefill_attn_int4).
+ * slot_mapping and positions past the last token are -1 and 0, so a batch
+ * padded to max_tokens can be appended as it is.
+ *
+ * src_tables    device int32 [num_src_rows][src_blocks]: the requests' tables
+ *               so far, or NULL when nothing is cached.  May be block_tables
+ *               itself (then src_rows is NULL, src_blocks equals
+ *               max_blocks_per_seq and num_src_rows >= num_seqs): only new
+ *               entries are written.  Must not overlap it otherwise.
+ * src_rows      device int32 [num_seqs]: row of src_tables of each request
+ *               (several may name the same row: a fork of its first
+ *               ceil(cached/page_size) pages; the last of these must be full
+ *               if two requests go on to write).  NULL: row b.
+ * cached_lens, new_lens  device int32 [num_seqs]; cached_lens NULL: all 0.
+ * free_pages    device int32 [max_free], taken from the front; num_free:
+ *               device int32 [1], how many of them are free (NULL: max_free).
+ * positions, pages_taken  may be NULL.  *pages_taken: pages used of the list.
+ *
+ * A request whose pages are not all in the list gets none: its slots are -1,
+ * its positions 0, its seq_lens entry cached_lens[b], and
+ * SAW_ERR_DEVICE_PAGES is reported; later requests that need no page are
+ * served.  A request with a negative length, a length beyond
+ * max_blocks_per_seq pages, or cached tokens without a source row is refused
+ * the same way with seq_lens 0 and SAW_ERR_DEVICE_INDEX (its new tokens, if
+ * the count is not negative, keep their rows).  A page id outside [0,
+ * num_pages) gives slot -1 and SAW_ERR_DEVICE_INDEX (a free one is stored as
+ * -1); so do more tokens than max_tokens (the rows behind are dropped).
+ * page_size 16, 32 or 64; at most 65535 requests; num_pages * page_size and
+ * max_blocks_per_seq * page_size below 2^31 (else SAW_ERR_UNSUPPORTED).  The
+ * outputs must not overlap the inputs (src_tables aside).
+ */
+int32_t saw_build_tables(const int32_t* src_tables, int32_t num_src_rows, int32_t src_blocks,
+                         const int32_t* src_rows, const int32_t* cached_lens,
+                         const int32_t* new_lens, const int32_t* free_pages, int32_t max_free,
+                         const int32_t* num_free, int32_t num_seqs, int32_t max_tokens,
+                         int32_t num_pages, int32_t page_size, int32_t* block_tables,
+                         int32_t max_blocks_per_seq, int32_t* seq_lens, int32_t* cu_q_lens,
+                         int32_t* slot_mapping, int32_t* positions, int32_t* pages_taken,
+                         int32_t* dev_status, void* stream);
+
+/*
+ * saw_rope_table -- the table that saw_rope_append reads: cos_sin[p][i] =
+ * a cos(p w_i), cos_sin[p][rope_dim/2 + i] = a sin(p w_i), i < rope_dim/2, for
+ * positions p < max_pos.  device float32 [max_pos][rope_dim], 16-byte aligned.
+ * Build it once per model.
+ *
+ * w_i = base^(-2i/rope_dim), changed by `scaling` for contexts `factor` times
+ * longer than the model's:
+ *   SAW_ROPE_NONE    as it is
+ *   SAW_ROPE_LINEAR  w_i / factor
+ *   SAW_ROPE_NTK     base * factor^(rope_dim/(rope_dim-2)) for base
+ *   SAW_ROPE_YARN    w_i for pairs that turn more than `high` times within
+ *                    orig_max_pos positions, w_i / factor for those below
+ *                    `low`, a linear ramp over the pair index between (its
+ *                    ends rounded outwards); a = 0.1 ln(factor) + 1
+ *   SAW_ROPE_BANDS   the same ends, a linear ramp over the number of turns
+ * low = high = 0 means 1 and 32 (YARN) or 1 and 4 (BANDS).  a is 1 except for
+ * YARN; att_scale > 0 sets it.  Angles are exact to 2^-32 turns at any
+ * position; values are within 2^-22 of a times the true ones.
+ * rope_dim a multiple of 16, at most 256 (else SAW_ERR_UNSUPPORTED).
+ */
+#define SAW_ROPE_NONE 0
+#define SAW_ROPE_LINEAR 1
+#define SAW_ROPE_NTK 2
+#define SAW_ROPE_YARN 3
+#define SAW_ROPE_BANDS 4
+int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double base,
+                       int32_t scaling, double factor, int32_t orig_max_pos, double low,
+                       double high, float att_scale, void* stream);
+
+/*
+ * saw_rope_append -- rotary positions on q and k, then saw_quantize_append of
+ * k and v, in one launch.
+ *
+ * q, k, v       device bfloat16 (binary16 with SAW_FMT_F16_INPUT)
+ *               [num_tokens][heads][head_dim] with token strides in elements
+ *               (multiples of 8, >= heads * head_dim): slices of a fused
+ *               projection's output will do.  q may be NULL (or num_q_heads
+ *               0): k and v only.  v may be NULL: q and k only.
+ * positions     device int32 [num_tokens], each in [0, max_pos); a token with
+ *               any other is skipped (q_out row too) and reported as
+ *               SAW_ERR_DEVICE_INDEX.
+ * cos_sin       device float32 [max_pos][rope_dim]: cosines of the
+ *               rope_dim/2 pairs, then sines (saw_rope_table).
+ * rope_dim      a multiple of 16 (else SAW_ERR_UNSUPPORTED), at most head_dim:
+ *               the first rope_dim elements of a head are turned.
+ * interleaved   0: pair i is elements (i, i + rope_dim/2); 1: (2i, 2i + 1).
+ * q_out         [num_tokens][num_q_heads][head_dim], token stride
+ *               q_out_token_stride; may be q itself with the same stride.
+ * Other arguments as saw_quantize_append_ex.  A slot of -1 appends nothing;
+ * the token's q is turned all the same.
+ *
+ * Per pair, in binary32 with products rounded separately: y0 = x0 c - x1 s,
+ * y1 = x1 c + x0 s.  k is not rounded in between: its binary32 values go into
+ * the butterfly and the quantizer by saw_quantize_append's rule, so the bytes
+ * are fully determined.  q_out is rounded once to the input type.
+ */
+int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
+                        int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                        const int32_t* positions, const float* cos_sin, int32_t max_pos,
+                        int32_t rope_dim, int32_t interleaved, const int32_t* slot_mapping,
+                        int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, void* q_out, int64_t q_out_token_stride, void* k_cache,
+                        void* v_cache, int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                        int32_t rotate_v, int32_t block_h, int32_t formats, int32_t* dev_status,
+                        void* stream);
+
+/*
+ * Workspace bytes of saw_prefix_decode_int4 for these sizes on the current
+ * device; 0 when it needs none or the sizes are bad.  Zero-fill it before its
+ * first use; each call leaves it ready for the next.
+ */
+size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t page_size,
+                                         int32_t max_prefix_len, int32_t max_own_len);
+
+/*
+ * saw_prefix_decode_int4 -- saw_paged_decode_int4 for a batch in which groups
+ * of neighbouring sequences share their first pages (a system prompt, a
+ * document, samples of one prompt): the shared pages are read once per group
+ * instead of once per sequence.
+ *
+ * cu_group_seqs device int32 [num_groups + 1], ascending: group g is sequences
+ *               cu_group_seqs[g] .. cu_group_seqs[g+1] - 1.  A sequence in no
+ *               group shares nothing.
+ * prefix_lens   device int32 [num_groups]: the group's first prefix_lens[g]
+ *               tokens are the same for all its sequences.  Whole pages count
+ *               (the rest of the last page is read per sequence).  The table
+ *               rows of the group hold the same ids there (the caller's
+ *               contract; any of them may be the one read).
+ * seq_lens      device int32 [num_seqs]: all tokens, the prefix included.  0:
+ *               an idle row, its output zero.  A length below the prefix's
+ *               whole pages, beyond max_blocks_per_seq pages, or of more than
+ *               max_own_len tokens behind the prefix, is reported as
+ *               SAW_ERR_DEVICE_INDEX and treated as 0.
+ * max_prefix_len, max_own_len  host bounds on prefix_lens and on the tokens
+ *               behind a prefix's whole pages (for a sequence in no group: on
+ *               its length).  max_blocks_per_seq pages must hold max_prefix_len.
+ * out           [num_seqs][num_q_heads][128]: float32, or with
+ *               SAW_FMT_OUT_INPUT in `formats` the input type (one rounding).
+ * workspace     saw_prefix_decode_workspace_bytes(...) bytes, 16-byte
+ *               aligned, zero-filled before its first use.  Calls sharing one
+ *               must be ordered (one stream).
+ * formats       SAW_FMT_F16_INPUT, SAW_FMT_BF16_META, SAW_FMT_OUT_INPUT.
+ *
+ * A group with inconsistent entries is reported as SAW_ERR_DEVICE_INDEX and
+ * shares nothing.  Other arguments and errors as saw_paged_decode_int4;
+ * head_dim 128 and at most 8 q-heads per kv-head (else SAW_ERR_UNSUPPORTED).
+ */
+#define SAW_FMT_OUT_INPUT 4
+int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* cu_group_seqs,
+                               const int32_t* prefix_lens, int32_t num_groups, int32_t num_seqs,
+                               int32_t max_prefix_len, int32_t max_own_len, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                               int32_t page_size, int32_t rotate_k, int32_t rotate_v,
+                               int32_t block_h, float sm_scale, void* out, void* workspace,
+                               size_t workspace_bytes, int32_t formats, int32_t* dev_status,
+                               void* stream);
 
 /* ------------------------------------------------------------------------
  * BF16 baseline.  gist.science "SAW-INT4: System-Aware 4-Bit KV-Cache
