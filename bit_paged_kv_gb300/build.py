@@ -40,6 +40,7 @@ UNITS = [("saw_api.cu", "saw_api.o", []),
           ["-DSAW_DECODE_WARPS=8", "-DSAW_DECODE_SHARED"]),
          ("paged_decode.cu", "paged_decode_shared_w4.o",
           ["-DSAW_DECODE_WARPS=4", "-DSAW_DECODE_SHARED"]),
+         ("prefix_attn.cu", "prefix_attn.o", []),
          ("build_tables.cu", "build_tables.o", []),
          ("rope_append.cu", "rope_append.o", []),
          ("paged_decode_bf16.cu", "paged_decode_bf16.o", []),

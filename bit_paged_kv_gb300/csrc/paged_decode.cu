@@ -275,8 +275,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   if constexpr (SHARED) {
     // max_seq_len bounds the whole sequence here, max_own_len what follows
     // the prefix.  A length inside the prefix is an error (0: an idle row).
-    pg = prefix_find_seq(p.prefix, seq, P, p.group, p.num_kv_heads, p.num_seqs, lane,
-                         p.dev_status, &prefix_tiles);
+    bool bad = false;
+    pg = prefix_scan(p.prefix, P, p.group, p.num_kv_heads, p.num_seqs, lane,
+                     [&](const PrefixGroup& r, uint32_t) { return r.first <= seq && seq < r.end; }, &bad,
+                     &prefix_tiles);
+    if (bad && seq == 0 && split == 0 && kvh == 0 && warp == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     if (L < pg.tokens || L - pg.tokens > p.max_own_len) {
       if (L != 0 && split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
       pg.tokens = 0;
@@ -1193,7 +1196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       np = int(c1 - c0) + 1;
       pre_row = (seq - pg.first - blk * per) * p.group;
       const int64_t slot = int64_t(pg.unit0) + u + c0;
-      pre_o = reinterpret_cast<const float4*>(p.prefix.part) + prefix_part_index(slot, 0);
+      pre_o = reinterpret_cast<const float4*>(p.prefix.part) + prefix_part_index(slot);
       pre_ml = reinterpret_cast<const float2*>(p.prefix.part_ml) + slot * kPrefixRows;
     }
     __syncthreads();  // tot and qs are complete (one split: nothing above met)
@@ -1230,7 +1233,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
               const bool in = active && sp < nt;
               const int row = pre_row + h;
               v[u] = in ? __ldcg(pre_ml + int64_t(sp - ns) * kPrefixRows + row) : make_float2(-INFINITY, 0.0f);
-              o[u] = in ? __ldcg(pre_o + prefix_part_index(sp - ns, row >> 7) + ch * 128 + (row & 127))
+              o[u] = in ? __ldcg(pre_o + prefix_part_index(sp - ns) + ch * kPrefixRows + row)
                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               continue;
             }

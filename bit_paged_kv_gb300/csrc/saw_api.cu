@@ -542,12 +542,17 @@ int32_t saw_prefill_attn_int4(const void* q, const int32_t* cu_q_lens, const voi
 namespace {
 
 // How a shared-prefix decode runs: the decode kernel's split plan covers
-// `plan_len` tokens per sequence, its workspace comes first, then the prefix
-// pass's partials.
+// `plan_len` tokens per sequence.  The workspace is the split counters, the
+// split partials, then the prefix pass's partials.  The counters, which have
+// to be zero between calls, keep a region of their own of 1 MB (131072
+// (sequence, kv-head) pairs; more only for larger batches), so calls of
+// different sizes can share a workspace.
+constexpr size_t kTicketRegion = size_t(1) << 20;
 struct PrefixPlan {
   int32_t ctas;         // 0: no prefix pass, every sequence reads its own pages
   int32_t plan_len;
-  size_t split_bytes, part_bytes, ml_bytes;
+  size_t ticket_bytes, split_bytes, part_bytes, ml_bytes;
+  size_t total() const { return ticket_bytes + split_bytes + part_bytes + ml_bytes; }
 };
 
 int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
@@ -561,11 +566,27 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
       num_q_heads / num_kv_heads > saw::kMaxGroup || num_seqs > 65535 || num_kv_heads > 65535)
     return SAW_ERR_UNSUPPORTED;
   PrefixPlan p{};
-  p.ctas = 0;
-  p.plan_len = max_prefix_len + max_own_len;
+  const int sms_raw = sm_count();
+  const int64_t sms = sms_raw > 0 ? sms_raw : 148;
+  const int64_t per = saw::kPrefixRows / (num_q_heads / num_kv_heads);
+  const int64_t units = (num_groups + num_seqs / per) * num_kv_heads;  // at most
+  const int64_t tiles = ceil_div(max_prefix_len, saw::kPrefixKeys);
+  if (units * tiles > INT32_MAX) return SAW_ERR_UNSUPPORTED;
+  const bool shared = num_groups > 0 && num_seqs > 1 && max_prefix_len >= page_size;
+  if (shared) {
+    p.ctas = int32_t(sms);
+    p.plan_len = max_own_len;
+    p.part_bytes = size_t(units + sms) * saw::kPrefixRows * kHeadDim * 4;
+    p.ml_bytes = size_t(units + sms) * saw::kPrefixRows * 8;
+  } else {
+    p.plan_len = max_prefix_len + max_own_len;
+  }
   p.split_bytes = saw_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                              page_size, p.plan_len, 0);
   p.split_bytes = (p.split_bytes + 255) / 256 * 256;
+  if (p.split_bytes + p.part_bytes > 0)
+    p.ticket_bytes = std::max(kTicketRegion, saw::decode_ticket_bytes(num_seqs, num_kv_heads));
+  p.ticket_bytes = (p.ticket_bytes + 255) / 256 * 256;
   *out = p;
   return SAW_OK;
 }
@@ -580,7 +601,7 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
   if (plan_prefix(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, page_size,
                   max_prefix_len, max_own_len, &plan) != SAW_OK)
     return 0;
-  return plan.split_bytes + plan.part_bytes + plan.ml_bytes;
+  return plan.total();
 }
 
 int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v_cache,
@@ -603,7 +624,7 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
     return SAW_ERR_INVALID_ARG;
   if (max_blocks_per_seq < 0 || int64_t(max_blocks_per_seq) * page_size < max_prefix_len)
     return SAW_ERR_INVALID_ARG;
-  const size_t need = plan.split_bytes + plan.part_bytes + plan.ml_bytes;
+  const size_t need = plan.total();
   if (num_seqs > 0 && need > 0 &&
       (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return SAW_ERR_INVALID_ARG;
@@ -625,6 +646,38 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
   p.prefix.num_groups = num_groups;
   p.prefix.max_prefix_len = max_prefix_len;
   p.prefix.ctas = plan.ctas;
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + plan.ticket_bytes;
+  if (p.num_splits > 1) {
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = p.part_o + size_t(num_seqs) * num_q_heads * p.num_splits * kHeadDim;
+  }
+  if (plan.ctas > 0) {
+    ws += plan.split_bytes;
+    p.prefix.part = reinterpret_cast<float*>(ws);
+    p.prefix.part_ml = reinterpret_cast<float*>(ws + plan.part_bytes);
+    saw::PrefixParams x{};
+    x.q = p.q;
+    x.k_cache = p.k_cache;
+    x.v_cache = p.v_cache;
+    x.block_tables = block_tables;
+    x.prefix = p.prefix;
+    x.dev_status = dev_status;
+    x.max_blocks = max_blocks_per_seq;
+    x.num_seqs = num_seqs;
+    x.num_q_heads = num_q_heads;
+    x.num_kv_heads = num_kv_heads;
+    x.group = p.group;
+    x.num_pages = num_pages;
+    x.page_size = page_size;
+    x.rotate_k = rotate_k;
+    x.block_h = block_h;
+    x.c_h = p.c_h;
+    x.q_scale = p.q_scale;
+    x.in_f16 = p.in_f16;
+    x.meta_bf16 = p.meta_bf16;
+    if (saw::launch_prefix_attn(x, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return SAW_ERR_CUDA;
+  }
   const cudaError_t err = p.warps == 4   ? saw::launch_paged_decode_shared_w4(p, static_cast<cudaStream_t>(stream))
                           : p.warps == 8 ? saw::launch_paged_decode_shared_w8(p, static_cast<cudaStream_t>(stream))
                                          : saw::launch_paged_decode_shared_w16(p, static_cast<cudaStream_t>(stream));

@@ -122,6 +122,9 @@ cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream
 
 // ---------------------------------------------------------------- decode
 
+constexpr int kPrefixRows = 128;  // rows of a unit of the prefix pass
+constexpr int kPrefixKeys = 128;  // keys per tile
+
 // Groups of sequences that share their first pages, and the partial results
 // of the pass over those pages (saw_prefix.cuh).
 struct PrefixSide {
@@ -130,9 +133,33 @@ struct PrefixSide {
   int32_t num_groups;
   int32_t max_prefix_len;
   int32_t ctas;                 // CTAs of the prefix pass; 0: none ran, nothing is shared
-  float* part;                  // numerators, 128 KB per slot
+  float* part;                  // numerators, 64 KB per slot
   float* part_ml;               // (m, l) per row
 };
+
+struct PrefixParams {
+  const uint16_t* q;            // [B][Hq][128] bfloat16 (binary16 if in_f16) bits
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* block_tables;  // [B][max_blocks]
+  PrefixSide prefix;
+  int32_t* dev_status;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t rotate_k;
+  int32_t block_h;
+  float c_h;
+  float q_scale;                // sm_scale * log2(e)
+  int32_t in_f16;
+  int32_t meta_bf16;
+};
+
+cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t stream);
 
 struct DecodeParams {
   const uint16_t* q;            // [B][Hq][D] bfloat16 (binary16 if in_f16) bits

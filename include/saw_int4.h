@@ -514,8 +514,10 @@ int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
 
 /*
  * Workspace bytes of saw_prefix_decode_int4 for these sizes on the current
- * device; 0 when it needs none or the sizes are bad.  Zero-fill it before its
- * first use; each call leaves it ready for the next.
+ * device; 0 when it needs none or the sizes are bad.  Zero-fill a workspace
+ * before its first use; each call leaves it ready for the next, of whatever
+ * sizes (up to 131072 (sequence, kv-head) pairs; a larger batch wants one of
+ * its own).
  */
 size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
                                          int32_t num_q_heads, int32_t num_kv_heads,

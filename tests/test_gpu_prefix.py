@@ -260,6 +260,14 @@ def test_repeated_calls_share_a_workspace():
     for _ in range(3):
         again, st = run(s, ws=ws)
         assert st == 0 and torch.equal(first, again)
+        other, st = run(small, ws=ws)
+        assert st == 0 and torch.equal(other, alone)
+    many = setup(19, [100] * 3, [160] * 3, np.arange(1, 301) * 8, hq=32, hkv=8)
+    need = max(need, saw.saw_prefix_decode_workspace_bytes(300, 3, 32, 8, 128, 16, 160, many["max_own"]))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    alone, _ = run(many)
+    for _ in range(2):
+        assert torch.equal(run(many, ws=ws)[0], alone) and torch.equal(run(s, ws=ws)[0], first)
 
 
 def test_graph_replay_with_new_inputs_and_other_stream():
