@@ -10,9 +10,10 @@
 // on the tensor cores' side.
 //
 // Mathematics: the codes n enter S = q' n^T as they are (binary16 subnormals,
-// exact), q' -- the rotated q times a power of two -- as binary16 hi + lo
-// parts, so a score is t = s_k (q'.n) + z_k sum(q') to about 2^-22 of its
-// terms, as in the decode.  V^ = n s_V + z_V is dequantized and rounded once
+// exact), q' -- the rotated q times the softmax scale, log2 e and 2^4 -- as
+// binary16 hi + lo parts, so a score t = s_k (q'.n) + z_k sum(q') comes out in
+// base 2 to about 2^-22 of its terms, as in the decode (|q'| 2^4 saturates at
+// 65504, a score of thousands).  V^ = n s_V + z_V is dequantized and rounded once
 // to binary16 (no coarser than the 16-bit rows the cache was made from), p
 // too: O += P V^ in binary32, where sum(p s n) + sum(p z) would cancel.
 // Softmax in base 2 in binary32 with a running reference m that moves (and
@@ -20,20 +21,33 @@
 // 2^8: p <= 2^8 stays far inside binary16, and the merge's normalisation makes
 // the choice of m invisible.
 //
-// Twelve warps, specialised:
-//   0-3    softmax: thread r owns row r (tensor-memory lane r) and its 128
-//          scores in registers; p goes back over the scores' columns as the A
-//          operand of P V
-//   4-7    V expanders: one key per thread; 8-9: K expanders, two keys each
-//   10     producer: bulk copies of codes and metadata, one lane each
-//   11     MMA: one elected lane issues the products of tile i + 1's scores
+// Twenty-four warps, specialised:
+//   0-7, 8-15  softmax of even and odd tiles, run a tile apart so that one
+//          set's loads and exponentials fill the other's waits.  A warp has 16
+//          rows (half of the 32 tensor-memory lanes it can reach), a thread 2
+//          rows x 32 keys (the 16 x 256-bit access): whole rows in a warp, so
+//          no maximum crosses warps, and the per-key (s_k, z_k) cost 16 shared
+//          loads for 64 scores (one row per thread: 64 loads for 128, every
+//          lane the same words).  The running reference m of a row passes from
+//          set to set in tile order.  p goes back over the scores' columns as
+//          the A operand of P V.
+//   16-19  V expanders: one key per thread; 20-21: K expanders, two keys each
+//   22     producer: the list of work, and bulk copies of whole page chunks
+//   23     MMA: one elected lane issues the products of tile i + 1's scores
 //          before tile i's P V, so that the softmax of tile i runs behind them
+// Latency, not any unit's rate, sets the pace: a set's softmax (2 warps per
+// scheduler) and the two products it waits for follow one another.
+// The softmax warps draw registers from the others (96 and 48 a thread).
 // The 512 tensor-memory columns hold two score tiles (the second one makes the
 // overlap), O, and q' hi and lo: the score products read only K from shared
 // memory.  Operands there are unswizzled 8-row x 16-byte core matrices, two
 // tiles each of K and V.  An expander writes each 8 dims in the order 0 4 1 5
 // 2 6 3 7, the order in which masking a word of codes yields pairs; q' is
 // stored in that order and the output columns are put back when written.
+// q' is rotated by the tensor cores too: q times H, a matrix of +-1 (the
+// identity when K is not rotated) that the V expanders write; both pass
+// through the V buffers, which are free between segments.  (By shuffles, a row
+// per warp at a time, the rotation took 11000 cycles of cold, dependent code.)
 // Every wait is bounded to about a second.
 #include <type_traits>
 
@@ -46,39 +60,94 @@
 namespace saw {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftWarps = 4;
-constexpr int kWarpV = 4, kWarpK = 8, kWarpProd = 10, kWarpMma = 11;
+constexpr int kThreads = 768;
+constexpr int kSoftWarps = 16;
+constexpr int kWarpV = 16, kWarpK = 20, kWarpProd = 22, kWarpMma = 23;
+constexpr int kLaunchRegs = 80, kSoftRegs = 96, kFeedRegs = 48;
+static_assert(4 * kSoftRegs + 2 * kFeedRegs == 6 * kLaunchRegs, "register shares of six warpgroups");
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kKeys = kPrefixKeys;
-static_assert(kPrefixRows == 128 && kKeys == 128, "one row per softmax thread, one key per V expander thread");
+static_assert(kHeadDim == 128, "eight k-steps of 16");
+static_assert(kPrefixRows == 128 && kKeys == 128, "four softmax warps per 32 rows, one key per V expander thread");
 
 constexpr int kOpBytes = 128 * 128 * 2;            // one operand tile
-constexpr int kRawV = kKeys * 64, kRawKM = 2 * kKeys * 64, kRawVM = kRawKM + kKeys * 4;
-constexpr int kRawBytes = kRawVM + kKeys * 4;      // 17408
+constexpr int kRawV = kKeys * 68;                  // raw stage: the pages' K chunks, then their V chunks
+constexpr int kRawBytes = 2 * kKeys * 68;          // 17408
 constexpr int kRawStages = 4;
 constexpr int kMetas = 4;                          // tiles of (s_k, z_k) for the softmax
-constexpr int kMetaBytes = kKeys * 8 + 16;         // s[128], z[128], valid 16-key slices
+constexpr int kMetaBytes = kKeys * 8 + 16;         // (s, s, z, z) per key pair, valid 16-key slices
 constexpr int kOffK = 0, kOffV = kOffK + 2 * kOpBytes;
 constexpr int kOffRaw = kOffV + 2 * kOpBytes;
 constexpr int kOffMeta = kOffRaw + kRawStages * kRawBytes;
 constexpr int kOffOk = kOffMeta + kMetas * kMetaBytes;  // valid 16-key slices of the raw stages
-constexpr int kOffBar = kOffOk + 4 * kRawStages;
+constexpr int kOffM = kOffOk + 4 * kRawStages;          // f32 [128]: the rows' running references
+constexpr int kOffRow = kOffM + 128 * 4;                // f32x2 [4][128]: parts of sum(q'); (m, l) at the end
+constexpr int kSegs = 4;                                // segments announced ahead
+constexpr int kOffSeg = kOffRow + 4 * 128 * 8;
+constexpr int kOffBar = kOffSeg + kSegs * 48;
 enum { kRawFull = 0, kRawEmpty = kRawFull + kRawStages, kKFull = kRawEmpty + kRawStages, kKEmpty = kKFull + 2,
        kVFull = kKEmpty + 2, kPvDone = kVFull + 2, kMetaFull = kPvDone + 2, kSFull = kMetaFull + kMetas,
-       kPFull = kSFull + 2, kQFull = kPFull + 2, kMmaDone, kBars };
+       kPFull = kSFull + 2, kTurn = kPFull + 2, kSegFull = kTurn + 16, kSegEmpty = kSegFull + kSegs, kQIn = kSegEmpty + kSegs, kQRot, kQFull, kMmaDone, kBars };
 constexpr int kOffTmem = kOffBar + kBars * 8;
 constexpr int kSmem = kOffTmem + 16;
-static_assert(kOffBar % 8 == 0 && kOffMeta % 16 == 0 && kSmem <= 227 * 1024, "shared memory");
+static_assert(kOffBar % 8 == 0 && kOffMeta % 16 == 0 && kOffM % 16 == 0 && kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kColO = 256, kColQh = 384, kColQl = 448;
 
 // ------------------------------------------------------------ PTX pieces
 
-__device__ __forceinline__ void umma_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Eight k-steps of one product by one elected lane: D [+]= A B^T, B advancing
+// by kStepB per step.  (One asm block: operands are converted to uniform
+// registers per instruction, and with an election each the 24 products of a
+// tile were 13 KB of code.)
+template <int64_t kStepA, int64_t kStepB>
+__device__ __forceinline__ void umma_ss8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b64 a64;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 b, %2;\n\tmov.b64 a64, %1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s64 a64, a64, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a64, b, %3, p;\n\t"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)), "n"(kStepB), "n"(kStepA)
+      : "memory");
+}
+// The same with A in tensor memory (8 columns per step).
+template <int64_t kStepB>
+__device__ __forceinline__ void umma_ts8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b32 a32;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 b, %2;\n\tmov.b32 a32, %1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "add.s64 b, b, %5;\n\tadd.s32 a32, a32, 8;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a32], b, %3, p;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)), "n"(kStepB)
       : "memory");
 }
 __device__ __forceinline__ void commit_elect(uint64_t* bar) {
@@ -94,6 +163,21 @@ __device__ __forceinline__ void arrive_elect(uint64_t* bar) {
       "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void expect_tx_elect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_elect(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 // 32 tensor-memory columns of this thread's lane, without waiting
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, float* v) {
   asm volatile(
@@ -105,6 +189,48 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, float* v) {
         "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
         "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
+}
+// 16 lanes x 64 columns: register 4k + j of lane 4g + c is row g (j < 2) or g +
+// 8, column 8k + 2c + (j & 1) -- the layout of a 16 x 8 accumulator per k.
+__device__ __forceinline__ void tmem_ld_16x256_issue(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+// The same for 16 columns, loaded (and waited for) and stored.
+__device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t taddr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256_x2(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// 16 lanes x 32 columns: register 2k + j of lane 4g + c is row g + 8j, column 4k + c.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // keeps uses of loaded registers behind the wait above
@@ -122,63 +248,117 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// A wait of one warp; after a failure every later wait returns at once.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, bool& failed) {
+// {x, x} as a register pair, built once instead of per packed instruction.
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+// (v0, v1) = s (v0, v1) + (z qs + nm) for a key pair's sz = (s, s, z, z)
+__device__ __forceinline__ void score2(float& v0, float& v1, const float4& sz, uint64_t qs, uint64_t nm) {
+  asm("{\n\t.reg .b64 v, s, z;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tmov.b64 z, {%4, %5};\n\t"
+      "fma.rn.f32x2 z, z, %6, %7;\n\tfma.rn.f32x2 v, s, v, z;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(v0), "+f"(v1)
+      : "f"(sz.x), "f"(sz.y), "f"(sz.z), "f"(sz.w), "l"(qs), "l"(nm));
+}
+// Waits of a whole warp; after a failure every later wait returns at once.
+// The loop is a handful of instructions (forty such waits with a clock in each
+// were a fifth of the kernel's code) and bounded by its count: a try returns
+// after the suspend hint at the latest (10 us: the feeding warps park, leaving
+// their scheduler's issue slots to the others), or at once without one, 20
+// cycles or more a try -- a second, or a few.
+template <bool PARK>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, bool& failed) {
   if (failed) return false;
-  failed = !__all_sync(kAll, mbar_wait_bounded(bar, parity));
+  uint32_t ok;
+  if constexpr (PARK) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\tmov.b32 n, 0;\n\t"
+        "WAIT_AGAIN:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+        "@p bra WAIT_DONE;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 200000;\n\t@q bra WAIT_AGAIN;\n\t"
+        "WAIT_DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\tmov.b32 n, 0;\n\t"
+        "WAIT_AGAIN:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra WAIT_DONE;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 100000000;\n\t@q bra WAIT_AGAIN;\n\t"
+        "WAIT_DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  }
+  failed = !__all_sync(kAll, ok != 0);
   return !failed;
+}
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, bool& failed) {
+  return wait_warp<false>(bar, parity, failed);
+}
+__device__ __forceinline__ bool wait_parked(uint64_t* bar, uint32_t parity, bool& failed) {
+  return wait_warp<true>(bar, parity, failed);
+}
+
+// The four softmax warps that share this thread's 32 rows meet; the AND of
+// `ok` over their threads.
+__device__ __forceinline__ bool rows_sync(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(ok)), "r"(1 + int((threadIdx.x >> 5) & 3)), "r"(128)
+      : "memory");
+  return r != 0;
 }
 
 // ------------------------------------------------------------ work list
 
-struct Segment {
+struct __align__(16) Segment {
   int kvh;
   int leader;        // the group's first sequence, whose table row is read
   int seq0, rows;    // first sequence of the block; its (sequence, head) rows (at most 128)
   int tile, tiles;   // key tiles of the prefix to do
   int tokens;        // tokens of the whole prefix
+  int more;          // 0: no segment, the end
   int64_t slot;
+  int pad[2];
 };
+static_assert(sizeof(Segment) == 48, "kOffSeg");
 
-// Walks this CTA's tiles segment by segment; every warp walks for itself.
+// Walks this CTA's tiles segment by segment.  The producer warp does, and
+// announces each segment to the other warps through a ring in shared memory:
+// one copy of this code (in every role it was half of a kernel of 137 KB, and
+// instruction fetches were a fifth of all stalls).
 struct Walk {
-  PrefixGroup g;
+  PrefixGroup g;     // holds tile `at` once found
   uint32_t at, end;
-  bool have;
+  bool placed, found;
 };
 
-__device__ __forceinline__ uint32_t group_tiles(const PrefixGroup& g, int hkv) {
-  return uint32_t(g.blocks) * hkv * g.tiles;
-}
-
-// Whole warp: the group whose tiles hold `at`, and the tiles of all groups.
-__device__ __forceinline__ PrefixGroup find_tile(const PrefixParams& p, uint32_t at, int lane, uint32_t* total) {
-  bool bad = false;  // (reported by the decode kernel)
-  return prefix_scan(p.prefix, p.page_size, p.group, p.num_kv_heads, p.num_seqs, lane,
-                     [&](const PrefixGroup& r, uint32_t t) { return r.tile0 <= at && at < r.tile0 + t; }, &bad, total);
-}
-
-__device__ __forceinline__ Walk start_walk(const PrefixParams& p, int lane) {
-  Walk w;
-  uint32_t total;
-  // the chunk depends on the total, so the first look finds only that
-  (void)find_tile(p, 0xFFFFFFFFu, lane, &total);
-  const uint32_t chunk = prefix_chunk(total, p.prefix.ctas);
-  const uint64_t lo = uint64_t(blockIdx.x) * chunk;
-  w.at = uint32_t(min(lo, uint64_t(total)));
-  w.end = uint32_t(min(lo + chunk, uint64_t(total)));
-  w.have = false;
-  return w;
-}
-
+// Whole warp: the next segment, or false at the end of this CTA's piece.
 __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Segment& s, int lane) {
-  if (w.at >= w.end) return false;
-  if (!w.have || w.at >= w.g.tile0 + group_tiles(w.g, p.num_kv_heads)) {
+#pragma unroll 1
+  while (!w.placed || (w.at < w.end && !w.found)) {
+    bool bad = false;  // (reported by the decode kernel)
     uint32_t total;
-    w.g = find_tile(p, w.at, lane, &total);
-    w.have = true;
-    if (w.g.tiles <= 0) return false;  // (cannot be: the line ends with its groups)
+    const uint32_t at = w.at;
+    w.g = prefix_scan(p.prefix, p.page_size, p.group, p.num_kv_heads, p.num_seqs, lane,
+                      [&](const PrefixGroup& r, uint32_t t) { return r.tile0 <= at && at < r.tile0 + t; }, &bad, &total);
+    if (!w.placed) {  // the first look only brings the total
+      const uint32_t chunk = prefix_chunk(total, p.prefix.ctas);
+      const uint64_t lo = uint64_t(blockIdx.x) * chunk;
+      w.at = uint32_t(min(lo, uint64_t(total)));
+      w.end = uint32_t(min(lo + chunk, uint64_t(total)));
+      w.placed = true;
+    } else {
+      w.found = true;
+    }
   }
+  if (w.at >= w.end || w.g.tiles <= 0) return false;
   const uint32_t in = w.at - w.g.tile0;
   const uint32_t u = in / uint32_t(w.g.tiles);
   const int per = prefix_seqs_per_block(p.group);
@@ -192,6 +372,7 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Seg
   s.tokens = w.g.tokens;
   s.slot = int64_t(w.g.unit0) + u + blockIdx.x;
   w.at += s.tiles;
+  w.found = w.at < w.g.tile0 + uint32_t(w.g.blocks) * p.num_kv_heads * w.g.tiles;
   return true;
 }
 
@@ -223,7 +404,7 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 s, __half2 z) {
 }
 // The same through binary32, saturated to the largest binary16: rows whose
 // scale or zero binary16 does not hold exactly, or that reach beyond it.
-__device__ __noinline__ uint4 dequant8_wide(uint32_t w, float s, float z) {
+__device__ __forceinline__ uint4 dequant8_wide(uint32_t w, float s, float z) {
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -233,20 +414,48 @@ __device__ __noinline__ uint4 dequant8_wide(uint32_t w, float s, float z) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Key n of a raw tensor tile (64 code bytes per key) into an operand tile:
-// dims 8u .. 8u+7 at u * 2048 + n * 16.  widen(word) gives the 16 bytes.
-template <typename Widen>
-__device__ __forceinline__ void expand_key(const uint8_t* codes, bool ok, uint8_t* dst, int n, Widen widen) {
-#pragma unroll
+// Key n's 64 code bytes into an operand tile: dims 8u .. 8u+7 at u * 2048 +
+// n * 16.  widen(word) gives the 16 bytes.
+template <int kUnroll, typename Widen>
+__device__ __forceinline__ void expand_key(const uint8_t* codes, uint8_t* dst, int n, Widen widen) {
+#pragma unroll kUnroll
   for (int q = 0; q < 4; ++q) {
     // rotated 16-byte pieces: eight lanes' rows (64 bytes apart) then fall
     // into different banks
     const int piece = (q + (n >> 1)) & 3;
-    const uint4 w = *reinterpret_cast<const uint4*>(codes + n * 64 + 16 * piece);
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    const uint4 w = *reinterpret_cast<const uint4*>(codes + 16 * piece);
+    uint8_t* d = dst + 4 * piece * 2048 + n * 16;
+    *reinterpret_cast<uint4*>(d) = widen(w.x);
+    *reinterpret_cast<uint4*>(d + 2048) = widen(w.y);
+    *reinterpret_cast<uint4*>(d + 4096) = widen(w.z);
+    *reinterpret_cast<uint4*>(d + 6144) = widen(w.w);
+  }
+}
+
+// Column n of the rotated q -- dim d = 8 (n / 8) + {0 4 1 5 2 6 3 7}[n % 8] --
+// as row n of the B operand: H[d][j] = (-1)^popcount(d & j) within blocks of
+// h (h = 1: the identity), times 2^-4 in the pairs whose codes are n 2^-20.
+template <bool F16IN>
+__device__ __forceinline__ void write_hadamard(uint8_t* dst, int n, int h) {
+  const int at = n & 7, d = (n & ~7) + ((at >> 1) | ((at & 1) << 2));
+  const uint32_t one = ((at >> 1) & 1) ? (F16IN ? 0x2C00u : 0x3D80u) : (F16IN ? 0x3C00u : 0x3F80u);
+  uint32_t w[4];  // j & 7 = 0 .. 7
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      *reinterpret_cast<uint4*>(dst + (4 * piece + u) * 2048 + n * 16) = ok ? widen(ws[u]) : make_uint4(0u, 0u, 0u, 0u);
+  for (int t = 0; t < 4; ++t) {
+    uint32_t lo = one | ((__popc(d & (2 * t)) & 1) << 15), hi = one | ((__popc(d & (2 * t + 1) & 7) & 1) << 15);
+    if (h == 1) {
+      lo = (d & 7) == 2 * t ? one : 0u;
+      hi = (d & 7) == 2 * t + 1 ? one : 0u;
+    }
+    w[t] = lo | (hi << 16);
+  }
+  const int hb = h < 8 ? 8 : h;  // (h = 1: the group of 8 that holds d)
+#pragma unroll 1
+  for (int u = 0; u < 16; ++u) {
+    const bool in = d / hb == 8 * u / hb;
+    const uint32_t flip = h > 1 && (__popc((d >> 3) & u & (hb / 8 - 1)) & 1) ? 0x80008000u : 0u;
+    *reinterpret_cast<uint4*>(dst + u * 2048 + n * 16) =
+        in ? make_uint4(w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -254,7 +463,6 @@ __device__ __forceinline__ void expand_key(const uint8_t* codes, bool ok, uint8_
 
 template <int P, bool F16IN, bool BFM>
 __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixParams p) {
-  pdl_wait_then_release();
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + kOffTmem);
@@ -272,9 +480,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
       mbar_init(&bars[kVFull + b], 4);
       mbar_init(&bars[kPvDone + b], 1);
       mbar_init(&bars[kSFull + b], 1);
-      mbar_init(&bars[kPFull + b], kSoftWarps);
+      mbar_init(&bars[kPFull + b], kSoftWarps / 2);
     }
+    for (int b = 0; b < 16; ++b) mbar_init(&bars[kTurn + b], 1);
     for (int b = 0; b < kMetas; ++b) mbar_init(&bars[kMetaFull + b], 2);
+    for (int b = 0; b < kSegs; ++b) {
+      mbar_init(&bars[kSegFull + b], 1);
+      mbar_init(&bars[kSegEmpty + b], kThreads / 32 - 1);
+    }
+    mbar_init(&bars[kQIn], kSoftWarps + 4);
+    mbar_init(&bars[kQRot], 1);
     mbar_init(&bars[kQFull], kSoftWarps);
     mbar_init(&bars[kMmaDone], 1);
     mbar_fence_init();
@@ -284,271 +499,355 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  pdl_wait_then_release();  // nothing above reads what another kernel writes
   bool failed = false;
-  Segment sg;
-  Walk walk = start_walk(p, lane);
-  uint32_t it = 0;  // tiles of this CTA so far
+  uint32_t it = 0;    // tiles of this CTA so far
+  uint32_t segs = 0;  // and segments
+  Segment* ring = reinterpret_cast<Segment*>(smem + kOffSeg);
+  // the next announced segment, taken (every warp but the producer's)
+  auto take = [&](Segment& s) {
+    const int e = segs % kSegs;
+    if (!wait_all(&bars[kSegFull + e], (segs / kSegs) & 1, failed)) return false;
+    s = ring[e];
+    __syncwarp();
+    arrive_elect(&bars[kSegEmpty + e]);
+    return s.more != 0;
+  };
 
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------- softmax
-    const int r = 32 * warp + lane;                 // row, tensor-memory lane
-    const uint32_t tl = tmem + (uint32_t(32 * warp) << 16);
-    while (next_segment(p, walk, sg, lane)) {
+    const int par = warp >> 3;                      // tiles of this parity
+    const int quart = warp >> 2;                    // columns 32 quart .. of q' and O
+    const int r = 32 * (warp & 3) + lane;           // row, as tensor-memory lane
+    const int g = lane >> 2, c = lane & 3;
+    const int r2 = 32 * (warp & 3) + 16 * (quart & 1) + g;  // rows r2, r2 + 8 of this thread's scores
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t ts = tl + (uint32_t(16 * (quart & 1)) << 16);
+    float* rowm = reinterpret_cast<float*>(smem + kOffM);
+    uint64_t* turn = &bars[kTurn + 2 * (warp & 7)];  // [parity]: that tile's m is in rowm
+    float2* rowx = reinterpret_cast<float2*>(smem + kOffRow);
+    for (Segment sg; take(sg);) {
+      // ---- q: this thread's quarter row into the A operand (V buffer 0)
       const bool live = r < sg.rows;
-      float a, qc;
       {
-        // ---- q': rotate, scale by 2^S with max |q'| 2^S < 2^14, store
-        float v[128];
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = make_uint4(0u, 0u, 0u, 0u);
         if (live) {
           const int sq = sg.seq0 + r / p.group, h = r % p.group;
           const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (int64_t(sq) * p.num_q_heads + sg.kvh * p.group + h) * kHeadDim);
+                                 p.q + (int64_t(sq) * p.num_q_heads + sg.kvh * p.group + h) * kHeadDim) + 4 * quart;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint4 w = src[k];
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[8 * k + 2 * j] = in_lo(ws[j], F16IN);
-              v[8 * k + 2 * j + 1] = in_hi(ws[j], F16IN);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = 0.0f;
+          for (int k = 0; k < 4; ++k) w[k] = src[k];
         }
-        if (p.rotate_k) {
 #pragma unroll
-          for (int s = 1; s < 128; s <<= 1) {
-            if (s < p.block_h) {
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(smem + kOffV + (4 * quart + k) * 2048 + r * 16) = w[k];
+      }
+      fence_async_smem();
+      tc_fence_before();  // (the last segment's O has been read)
+      __syncwarp();
+      arrive_elect(&bars[kQIn]);
+      // ---- the rotated row: softmax scale and 2^4, hi and lo parts
+      wait_all(&bars[kQRot], segs & 1, failed);
+      tc_fence_after();
+      {
+        const float f = (p.rotate_k ? p.c_h : 1.0f) * p.q_scale * 16.0f;
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          float x[16];
+          tmem_ld16(tl + kColO + 32 * quart + 16 * k, x);
+          uint32_t hw[8], lw[8];
 #pragma unroll
-              for (int i = 0; i < 128; ++i)
-                if (!(i & s)) {
-                  const float x = v[i], y = v[i + s];
-                  v[i] = x + y;
-                  v[i + s] = x - y;
-                }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] *= p.c_h;
-        }
-        float mx = 0.0f, sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          mx = fmaxf(mx, fabsf(v[i]));
-          sum += v[i];
-        }
-        const int E = int((__float_as_uint(mx) >> 23) & 0xFFu);
-        const int S = min(100, max(-100, 140 - E));
-        const float up = __uint_as_float(uint32_t(127 + S) << 23);
-        // codes are n 2^-24: t = a (s_k acc + z_k qc)
-        a = p.q_scale * __uint_as_float(uint32_t(127 - S) << 23) * 16777216.0f;
-        qc = sum * up * 5.9604644775390625e-08f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          uint32_t hw[4], lw[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float f = (j & 1) ? up * 0.0625f : up;
-            const float x0 = v[8 * k + j] * f, x1 = v[8 * k + j + 4] * f;
-            const __half h0 = __float2half_rn(x0), h1 = __float2half_rn(x1);
+          for (int j = 0; j < 8; ++j) {
+            // (pairs 1 and 3 of each 8 columns carry 2^-4)
+            const float y0 = fminf(fmaxf(x[2 * j] * f, -65504.0f), 65504.0f);
+            const float y1 = fminf(fmaxf(x[2 * j + 1] * f, -65504.0f), 65504.0f);
+            sum += (y0 + y1) * ((j & 1) ? 1.0f : 0.0625f);
+            const __half h0 = __float2half_rn(y0), h1 = __float2half_rn(y1);
             hw[j] = uint32_t(__half_as_ushort(h0)) | (uint32_t(__half_as_ushort(h1)) << 16);
-            lw[j] = pack_half2(x0 - __half2float(h0), x1 - __half2float(h1));
+            lw[j] = pack_half2(y0 - __half2float(h0), y1 - __half2float(h1));
           }
-          tmem_st4u(tl + kColQh + 4 * k, hw);
-          tmem_st4u(tl + kColQl + 4 * k, lw);
+          tmem_st8u(tl + kColQh + 16 * quart + 8 * k, hw);
+          tmem_st8u(tl + kColQl + 16 * quart + 8 * k, lw);
         }
         tmem_wait_st();
+        rowx[quart * 128 + r] = make_float2(sum, 0.0f);
       }
+      ++segs;
       tc_fence_before();
       __syncwarp();
       arrive_elect(&bars[kQFull]);
+      failed = !rows_sync(!failed);  // rowx
+      uint64_t qs[2];  // a row's sum(q'), twice
+      float m[2];      // and reference
+      float2 l[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x += rowx[k * 128 + r2 + 8 * i].x;
+        qs[i] = twice(x);
+        m[i] = 0.0f;
+        l[i] = make_float2(0.0f, 0.0f);
+      }
 
-      float m = -INFINITY, l = 0.0f;
-      for (int i = 0; i < sg.tiles; ++i, ++it) {
-        const int b = it & 1;
+      const uint32_t first = it, end = it + sg.tiles;
+      const uint32_t at_s = ts + 128 * par;
+      for (it = first + ((first ^ par) & 1); it < end; it += 2) {
         wait_all(&bars[kMetaFull + (it & (kMetas - 1))], (it / kMetas) & 1, failed);
-        wait_all(&bars[kSFull + b], (it >> 1) & 1, failed);
+        wait_all(&bars[kSFull + par], (it >> 1) & 1, failed);
         tc_fence_after();
-        const uint32_t col = tl + 128 * b;
-        float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_issue(col + 32 * c, s + 32 * c);
+        float s[64];  // [4 k + 2 i + column]: scores, minus m
+        tmem_ld_16x256_issue(at_s, s);
+        tmem_ld_16x256_issue(at_s + 64, s + 32);
         const uint8_t* meta = smem + kOffMeta + (it & (kMetas - 1)) * kMetaBytes;
-        const float4* ms = reinterpret_cast<const float4*>(meta);
-        const float4* mz = ms + kKeys / 4;
-        const int okm = *reinterpret_cast<const int*>(meta + kKeys * 8);
+        const float4* msz = reinterpret_cast<const float4*>(meta) + c;  // (s, s, z, z) of a key pair
+        uint64_t nm[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) nm[i] = twice(-m[i]);
         tmem_wait_ld();
+        pin32(s);
+        pin32(s + 32);
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) pin32(s + 32 * c);
-        const float2 qc2 = make_float2(qc, qc);
-        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int k = 0; k < 16; ++k) {
+          const float4 sz = msz[4 * k];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float4 sk = ms[j], zk = mz[j];
-          const float2 x = fma2(make_float2(sk.x, sk.y), make_float2(s[4 * j], s[4 * j + 1]),
-                                mul2(qc2, make_float2(zk.x, zk.y)));
-          const float2 y = fma2(make_float2(sk.z, sk.w), make_float2(s[4 * j + 2], s[4 * j + 3]),
-                                mul2(qc2, make_float2(zk.z, zk.w)));
-          s[4 * j] = x.x;
-          s[4 * j + 1] = x.y;
-          s[4 * j + 2] = y.x;
-          s[4 * j + 3] = y.y;
+          for (int i = 0; i < 2; ++i) {
+            float* v = &s[4 * k + 2 * i];
+            score2(v[0], v[1], sz, qs[i], nm[i]);
+            t4[2 * i + (k & 1)] = max3(t4[2 * i + (k & 1)], v[0], v[1]);
+          }
         }
+        const int okm = *reinterpret_cast<const int*>(meta + kKeys * 8);
         if (okm != 0xFF) {  // keys past the prefix or on a bad page
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (!((okm >> (j >> 4)) & 1)) s[j] = -INFINITY;
-        }
+          for (int i = 0; i < 4; ++i) t4[i] = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 128; j += 8) {
+          for (int k = 0; k < 16; ++k) {
+            const bool in = (okm >> (k >> 1)) & 1;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) top4[c] = max3(top4[c], s[j + 2 * c], s[j + 2 * c + 1]);
-        }
-        const float top = a * fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-        // move the reference when the maximum outgrew it (first tile: always)
-        const bool move = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(kAll, move)) {
-          const float f = move ? ex2(m - top) : 1.0f;  // 0 while m is -inf
-          l *= f;
-          if (i > 0 && wait_all(&bars[kPvDone + (b ^ 1)], ((it - 1) >> 1) & 1, failed)) {
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              float o[16];
-              tmem_ld16(tl + kColO + 16 * c, o);
-              uint32_t ow[16];
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float2 x = mul2(make_float2(o[j], o[j + 1]), make_float2(f, f));
-                ow[j] = __float_as_uint(x.x);
-                ow[j + 1] = __float_as_uint(x.y);
-              }
-              tmem_st16u(tl + kColO + 16 * c, ow);
+            for (int i = 0; i < 2; ++i) {
+              float* v = &s[4 * k + 2 * i];
+              v[0] = in ? v[0] : -INFINITY;
+              v[1] = in ? v[1] : -INFINITY;
+              t4[2 * i] = max3(t4[2 * i], v[0], v[1]);
             }
           }
-          if (move) m = top;
         }
-        const float nm = m == -INFINITY ? 0.0f : -m;
-        const float2 a2 = make_float2(a, a), nm2 = make_float2(nm, nm);
-        float2 la = make_float2(0.0f, 0.0f), lb = la;
+        float top[2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(t4[2 * i], t4[2 * i + 1]);
+          top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+        }
+        // ---- the reference: the other set may have moved it in the tile
+        // before, and this tile moves it when its maximum outgrew it (the first
+        // tile to its maximum).  Both are rare, so the scores above are taken
+        // against the one known here, and shifted if it was not the last word.
+        if (it > first) wait_all(&turn[par ^ 1], ((it - 1) >> 1) & 1, failed);
+        float now[2];
+        bool move = it == first;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          now[i] = it > first ? rowm[r2 + 8 * i] : 0.0f;
+          move = move || now[i] != m[i] || top[i] > 8.0f;
+        }
+        if (__any_sync(kAll, move)) {
+          float f[2], sh[2];
+          bool grow = it == first;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float at = m[i] + top[i];  // this tile's maximum
+            const bool g1 = it == first ? top[i] > -INFINITY : at > now[i] + 8.0f;
+            const float to = g1 ? at : now[i];
+            f[i] = ex2(now[i] - to);
+            sh[i] = m[i] - to;
+            const float fl = ex2(sh[i]);
+            l[i] = mul2(l[i], make_float2(fl, fl));
+            m[i] = to;
+            grow = grow || g1;
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              s[4 * k + 2 * i] += sh[i];
+              s[4 * k + 2 * i + 1] += sh[i];
+            }
+          if (__any_sync(kAll, grow)) {
+            if (it > first && wait_all(&bars[kPvDone + (par ^ 1)], ((it - 1) >> 1) & 1, failed)) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < 8; ++q) {
+                float o[8];
+                tmem_ld_16x256_x2(ts + kColO + 16 * q, o);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) o[4 * k + j] *= f[j >> 1];
+                tmem_st_16x256_x2(ts + kColO + 16 * q, o);
+              }
+            }
+            if (c == 0) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) rowm[r2 + 8 * i] = m[i];
+            }
+          }
+        }
+        __syncwarp();
+        arrive_elect(&turn[par]);
+#pragma unroll
+        for (int kq = 0; kq < 2; ++kq) {
           uint32_t pw[16];
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const int k = 32 * c + 2 * j;
-            const float2 x = fma2(a2, make_float2(s[k], s[k + 1]), nm2);
-            const float2 y = fma2(a2, make_float2(s[k + 2], s[k + 3]), nm2);
-            const float2 px = make_float2(ex2(x.x), ex2(x.y)), py = make_float2(ex2(y.x), ex2(y.y));
-            la = add2(la, px);
-            lb = add2(lb, py);
-            pw[j] = pack_half2(px.x, px.y);
-            pw[j + 1] = pack_half2(py.x, py.y);
-          }
-          tmem_st16u(col + 16 * c, pw);
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float* v = &s[32 * kq + 4 * k + 2 * i];
+              const float2 e = make_float2(ex2(v[0]), ex2(v[1]));
+              l[i] = add2(l[i], e);
+              pw[2 * k + i] = pack_half2(e.x, e.y);
+            }
+          tmem_st_16x128(at_s + 32 * kq, pw);
         }
         tmem_wait_st();
-        l += (la.x + la.y) + (lb.x + lb.y);
         tc_fence_before();
         __syncwarp();
-        arrive_elect(&bars[kPFull + b]);
+        arrive_elect(&bars[kPFull + par]);
       }
+      it = end;
       // ---- the partial result, once the last P V has completed
-      wait_all(&bars[kPvDone + ((it - 1) & 1)], ((it - 1) >> 1) & 1, failed);
-      tc_fence_after();
-      float4* part = reinterpret_cast<float4*>(p.prefix.part) + prefix_part_index(sg.slot) + r;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int i = 0; i < 2; ++i) {
+        float v = l[i].x + l[i].y;
+        v += __shfl_xor_sync(kAll, v, 1);
+        v += __shfl_xor_sync(kAll, v, 2);
+        if (c == 0) rowx[par * 128 + r2 + 8 * i] = make_float2(m[i], v);
+      }
+      wait_all(&bars[kPvDone + ((it - 1) & 1)], ((it - 1) >> 1) & 1, failed);
+      failed = !rows_sync(!failed);
+      tc_fence_after();
+      {
+        float4* part = reinterpret_cast<float4*>(p.prefix.part) + prefix_part_index(sg.slot) + 8 * quart * 128 + r;
         float o[32];
-        tmem_ld32_issue(tl + kColO + 32 * c, o);
+        tmem_ld32_issue(tl + kColO + 32 * quart, o);
         tmem_wait_ld();
         pin32(o);
         if (live) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             // columns of 8 dims: 0 4 1 5 2 6 3 7
-            __stcg(part + (8 * c + 2 * k) * 128, make_float4(o[8 * k], o[8 * k + 2], o[8 * k + 4], o[8 * k + 6]));
-            __stcg(part + (8 * c + 2 * k + 1) * 128, make_float4(o[8 * k + 1], o[8 * k + 3], o[8 * k + 5], o[8 * k + 7]));
+            __stcg(part + 2 * k * 128, make_float4(o[8 * k], o[8 * k + 2], o[8 * k + 4], o[8 * k + 6]));
+            __stcg(part + (2 * k + 1) * 128, make_float4(o[8 * k + 1], o[8 * k + 3], o[8 * k + 5], o[8 * k + 7]));
           }
         }
       }
-      if (live)
+      if (live && quart == 0) {
+        // rowm is the reference that O refers to; nothing counted: m = -inf
+        const float2 x = rowx[r], y = rowx[128 + r];
+        const float mm = rowm[r];
+        const float ll = (x.y > 0.0f ? x.y * ex2(x.x - mm) : 0.0f) + (y.y > 0.0f ? y.y * ex2(y.x - mm) : 0.0f);
         __stcg(reinterpret_cast<float2*>(p.prefix.part_ml) + sg.slot * kPrefixRows + r,
-               failed ? make_float2(-INFINITY, 0.0f) : make_float2(m, l));
+               failed || !(ll > 0.0f) ? make_float2(-INFINITY, 0.0f) : make_float2(mm, ll));
+      }
+      failed = !rows_sync(!failed);  // rowx has been read
     }
     if (failed && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
-  } else if (warp == kWarpProd) {
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
+  if (warp == kWarpProd) {
     // ---------------------------------------------------------- producer
     constexpr int kChunk = P * 68;
     constexpr int kPages = kKeys / P;               // pages per tile
-    while (!failed && next_segment(p, walk, sg, lane)) {
+    constexpr int kAhead = 32 / kPages;             // tiles whose page ids a warp holds
+    Walk walk{{}, 0u, 0u, false, false};
+    for (bool more = true; more && !failed; ++segs) {
+      Segment sg{};
+      more = next_segment(p, walk, sg, lane);
+      sg.more = more;
+      const int e = segs % kSegs;
+      if (segs >= kSegs && !wait_parked(&bars[kSegEmpty + e], ((segs / kSegs) - 1) & 1, failed)) break;
+      if (lane == 0) ring[e] = sg;
+      __syncwarp();
+      arrive_elect(&bars[kSegFull + e]);
+      if (!more) break;
       const int32_t* btab = p.block_tables + int64_t(sg.leader) * p.max_blocks;
       const int n_pages = sg.tokens / P;
+      int ids = -1;
       for (int i = 0; i < sg.tiles; ++i, ++it) {
         const int st = it % kRawStages;
-        // lane l: page l / 4 of the tile; K codes, V codes, K words, V words
-        const int pg = lane >> 2, kind = lane & 3;
-        const int lp = (sg.tile + i) * kPages + pg;
-        int id = -1;
-        if (pg < kPages && lp < n_pages) {
-          id = btab[lp];
-          if (id < 0 || id >= p.num_pages) {
-            if (kind == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
-            id = -1;
+        if (i % kAhead == 0) {  // one page per lane
+          const int lp = (sg.tile + i) * kPages + lane;
+          ids = -1;
+          if (lp < n_pages && lp < (sg.tile + sg.tiles) * kPages) {
+            ids = btab[lp];
+            if (ids < 0 || ids >= p.num_pages) {
+              report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+              ids = -1;
+            }
           }
         }
-        const uint32_t have = __ballot_sync(kAll, id >= 0 && kind == 0);  // bit 4 pg
-        if (it >= kRawStages && !wait_all(&bars[kRawEmpty + st], ((it / kRawStages) - 1) & 1, failed)) break;
-        uint8_t* raw = smem + kOffRaw + st * kRawBytes;
+        // (lane g of the tile's pages says whether page g is there)
+        const int id_l = __shfl_sync(kAll, ids, (i % kAhead) * kPages + (lane % kPages));
+        const uint32_t have = __ballot_sync(kAll, id_l >= 0 && lane < kPages);
+        if (it >= kRawStages && !wait_parked(&bars[kRawEmpty + st], ((it / kRawStages) - 1) & 1, failed)) break;
+        const uint32_t raw = smem_u32(smem + kOffRaw + st * kRawBytes);
+        const uint32_t bar = smem_u32(&bars[kRawFull + st]);
         if (lane == 0) {
           int okm = 0;
 #pragma unroll
           for (int g = 0; g < kPages; ++g)
-            if ((have >> (4 * g)) & 1) okm |= ((1 << (P / 16)) - 1) << (g * (P / 16));
+            if ((have >> g) & 1) okm |= ((1 << (P / 16)) - 1) << (g * (P / 16));
           raw_ok[st] = okm;
-          if (have)
-            mbar_arrive_expect_tx(&bars[kRawFull + st], uint32_t(__popc(have)) * (2 * kChunk));
-          else
-            mbar_arrive(&bars[kRawFull + st]);
+          if (!have) mbar_arrive(&bars[kRawFull + st]);
         }
         __syncwarp();
-        if (id >= 0) {
-          const int64_t off = (int64_t(id) * p.num_kv_heads + sg.kvh) * kChunk;
-          const uint8_t* src = (kind & 1 ? p.v_cache : p.k_cache) + off + (kind >> 1 ? P * 64 : 0);
-          uint8_t* dst = raw + (kind == 0 ? 0 : kind == 1 ? kRawV : kind == 2 ? kRawKM : kRawVM) +
-                         pg * (kind >> 1 ? P * 4 : P * 64);
-          bulk_g2s(dst, src, kind >> 1 ? P * 4 : P * 64, &bars[kRawFull + st]);
+        // a page's chunk (codes and metadata) per copy, issued by one elected
+        // lane of the converged warp: the copy takes uniform registers, and 32
+        // lanes issuing their own cost 6000 cycles a tile
+        if (have) {
+          expect_tx_elect(bar, uint32_t(__popc(have)) * (2 * kChunk));
+#pragma unroll
+          for (int g = 0; g < kPages; ++g) {
+            if (!((have >> g) & 1)) continue;
+            const int id = __shfl_sync(kAll, id_l, g);
+            const int64_t off = (int64_t(id) * p.num_kv_heads + sg.kvh) * kChunk;
+            bulk_elect(raw + g * kChunk, p.k_cache + off, kChunk, bar);
+            bulk_elect(raw + kRawV + g * kChunk, p.v_cache + off, kChunk, bar);
+          }
         }
         __syncwarp();
       }
     }
-    if (failed && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
-    // the CTA must not exit while a copy into its shared memory is in flight
-    for (uint32_t i = it > kRawStages ? it - kRawStages : 0; i < it; ++i)
-      (void)mbar_wait_bounded(&bars[kRawFull + i % kRawStages], (i / kRawStages) & 1);
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------- MMA issue
     constexpr uint32_t id_s = umma_idesc_f16(128, kKeys);
     constexpr uint32_t id_o = umma_idesc_f16(128, kHeadDim) | kUmmaBMnMajor;
     const uint32_t k0 = smem_u32(smem + kOffK), v0 = smem_u32(smem + kOffV);
-    uint32_t segs = 0;
     auto score = [&](uint32_t t) {  // S of tile t into buffer t & 1
       const int b = t & 1;
       if (!wait_all(&bars[kKFull + b], (t >> 1) & 1, failed)) return;
       tc_fence_after();
       const uint64_t bd = umma_desc(k0 + b * kOpBytes, 2048, 128);
-#pragma unroll
-      for (int ks = 0; ks < kHeadDim / 16; ++ks)
-        umma_ts_elect(tmem + 128 * b, tmem + kColQh + 8 * ks, bd + ks * (4096 >> 4), id_s, ks > 0);
-#pragma unroll
-      for (int ks = 0; ks < kHeadDim / 16; ++ks)
-        umma_ts_elect(tmem + 128 * b, tmem + kColQl + 8 * ks, bd + ks * (4096 >> 4), id_s, true);
+      umma_ts8<(4096 >> 4)>(tmem + 128 * b, tmem + kColQh, bd, id_s, false);
+      umma_ts8<(4096 >> 4)>(tmem + 128 * b, tmem + kColQl, bd, id_s, true);
       commit_elect(&bars[kSFull + b]);
       commit_elect(&bars[kKEmpty + b]);
     };
-    while (!failed && next_segment(p, walk, sg, lane)) {
+    // q' = q H^T in the input type
+    constexpr uint32_t id_q = umma_idesc_f16(128, kHeadDim) | (F16IN ? 0u : (1u << 7) | (1u << 10));
+    for (Segment sg; take(sg);) {
+      if (!wait_all(&bars[kQIn], segs & 1, failed)) break;
+      tc_fence_after();
+      {
+        const uint64_t ad = umma_desc(v0, 2048, 128), bd = umma_desc(v0 + kOpBytes, 2048, 128);
+        umma_ss8<(4096 >> 4), (4096 >> 4)>(tmem + kColO, ad, bd, id_q, false);
+        commit_elect(&bars[kQRot]);
+      }
       if (!wait_all(&bars[kQFull], segs & 1, failed)) break;
       ++segs;
       score(it);
@@ -559,39 +858,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
         if (!wait_all(&bars[kPFull + b], (it >> 1) & 1, failed)) break;
         tc_fence_after();
         const uint64_t bd = umma_desc(v0 + b * kOpBytes, 128, 2048);
-#pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          umma_ts_elect(tmem + kColO, tmem + 128 * b + 8 * ks, bd + ks * (256 >> 4), id_o, i > 0 || ks > 0);
+        umma_ts8<(256 >> 4)>(tmem + kColO, tmem + 128 * b, bd, id_o, i > 0);
         commit_elect(&bars[kPvDone + b]);
       }
     }
-    if (failed && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
-    // every MMA has completed before tensor memory is released
-    commit_elect(&bars[kMmaDone]);
-    (void)mbar_wait_bounded(&bars[kMmaDone], 0);
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- expanders
     const bool is_v = warp < kWarpK;
-    while (!failed && next_segment(p, walk, sg, lane)) {
+    for (Segment sg; take(sg); ++segs) {
+      if (is_v) {
+        // the rotation matrix, once the last segment is done with the buffers
+        if (it > 0 && !wait_parked(&bars[kPvDone + ((it - 1) & 1)], ((it - 1) >> 1) & 1, failed)) break;
+        write_hadamard<F16IN>(smem + kOffV + kOpBytes, tid - 32 * kWarpV, p.rotate_k ? p.block_h : 1);
+        fence_async_smem();
+        __syncwarp();
+        arrive_elect(&bars[kQIn]);
+        if (!wait_parked(&bars[kQFull], segs & 1, failed)) break;
+      }
       for (int i = 0; i < sg.tiles; ++i, ++it) {
         const int st = it % kRawStages, b = it & 1;
-        if (!wait_all(&bars[kRawFull + st], (it / kRawStages) & 1, failed)) break;
+        if (!wait_parked(&bars[kRawFull + st], (it / kRawStages) & 1, failed)) break;
         const uint8_t* raw = smem + kOffRaw + st * kRawBytes;
         const int okm = raw_ok[st];
         if (is_v) {
           const int n = tid - 32 * kWarpV;          // key of the tile
           const bool ok = (okm >> (n >> 4)) & 1;
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(raw + kRawVM + 4 * n);
+          const uint8_t* chunk = raw + kRawV + (n / P) * (P * 68);
+          const uint8_t* codes = chunk + (n % P) * 64;
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(chunk + P * 64 + 4 * (n % P));
           const float sf = meta_lo(w, BFM), zf = meta_hi(w, BFM);
           // every value below binary16's largest; bfloat16 words also exact in
           // it (eight significant bits: from 2^-17 up)
           bool plain = fmaf(15.0f, sf, fabsf(zf)) <= 65504.0f;
           if (BFM) plain = plain && (sf == 0.0f || sf >= 0x1p-17f) && (zf == 0.0f || fabsf(zf) >= 0x1p-17f);
           const __half2 s = __float2half2_rn(sf), z = __float2half2_rn(zf);
-          if (it >= 2 && !wait_all(&bars[kPvDone + b], ((it >> 1) - 1) & 1, failed)) break;
-          expand_key(raw + kRawV, ok, smem + kOffV + b * kOpBytes, n,
-                     [&](uint32_t x) { return plain ? dequant8(x, s, z) : dequant8_wide(x, sf, zf); });
+          if (it >= 2 && !wait_parked(&bars[kPvDone + b], ((it >> 1) - 1) & 1, failed)) break;
+          uint8_t* dst = smem + kOffV + b * kOpBytes;
+          if (__all_sync(kAll, plain && ok))
+            expand_key<4>(codes, dst, n, [&](uint32_t x) { return dequant8(x, s, z); });
+          else  // (a key past the prefix or on a bad page: zeros, whatever lies there)
+            expand_key<1>(codes, dst, n, [&](uint32_t x) {
+              return ok ? dequant8_wide(x, sf, zf) : make_uint4(0u, 0u, 0u, 0u);
+            });
           fence_async_smem();
           __syncwarp();
           arrive_elect(&bars[kVFull + b]);
@@ -599,16 +907,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
           // K: codes as they are; scales and zeros for the softmax.  Meta slot
           // it % 4 was read for tile it - 4: its P was used by the P V that
           // precedes the scores of tile it - 2, whose end freed this K buffer.
-          if (it >= 2 && !wait_all(&bars[kKEmpty + b], ((it >> 1) - 1) & 1, failed)) break;
+          if (it >= 2 && !wait_parked(&bars[kKEmpty + b], ((it >> 1) - 1) & 1, failed)) break;
           uint8_t* meta = smem + kOffMeta + (it & (kMetas - 1)) * kMetaBytes;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int n = tid - 32 * kWarpK + 64 * u;
             const bool ok = (okm >> (n >> 4)) & 1;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(raw + kRawKM + 4 * n);
-            reinterpret_cast<float*>(meta)[n] = ok ? meta_lo(w, BFM) : 0.0f;
-            reinterpret_cast<float*>(meta)[kKeys + n] = ok ? meta_hi(w, BFM) : 0.0f;
-            expand_key(raw, ok, smem + kOffK + b * kOpBytes, n, [](uint32_t x) { return codes8(x); });
+            const uint8_t* chunk = raw + (n / P) * (P * 68);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(chunk + P * 64 + 4 * (n % P));
+            float* sz = reinterpret_cast<float*>(meta) + 4 * (n >> 1) + (n & 1);  // (s, s, z, z) of a key pair
+            sz[0] = ok ? meta_lo(w, BFM) * 1048576.0f : 0.0f;  // 2^24 of the codes, 2^-4 of q'
+            sz[2] = ok ? meta_hi(w, BFM) : 0.0f;
+            // (codes of a key that does not count: any number, its score is masked)
+            expand_key<4>(chunk + (n % P) * 64, smem + kOffK + b * kOpBytes, n, [](uint32_t x) { return codes8(x); });
           }
           if (tid == 32 * kWarpK) *reinterpret_cast<int*>(meta + kKeys * 8) = okm;
           fence_async_smem();
@@ -619,7 +930,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
         arrive_elect(&bars[kRawEmpty + st]);
       }
     }
-    if (failed && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
+  }
+  if (failed && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
+  if (warp == kWarpProd) {
+    // the CTA must not exit while a copy into its shared memory is in flight
+    for (uint32_t i = it > kRawStages ? it - kRawStages : 0; i < it; ++i)
+      (void)mbar_wait_bounded(&bars[kRawFull + i % kRawStages], (i / kRawStages) & 1);
+  } else if (warp == kWarpMma) {
+    // every MMA has completed before tensor memory is released
+    commit_elect(&bars[kMmaDone]);
+    (void)mbar_wait_bounded(&bars[kMmaDone], 0);
+  }
+  __syncwarp();
   }
 
   tc_fence_before();
@@ -633,6 +955,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
 template <int P, bool F16IN, bool BFM>
 cudaError_t launch_f(const PrefixParams& p, cudaStream_t stream) {
   auto kernel = prefix_attn_kernel<P, F16IN, BFM>;
+  // the softmax warps' larger share is drawn from the launch's registers: with
+  // fewer than kLaunchRegs a thread it would never be granted
+  static const bool regs_ok = [&] {
+    cudaFuncAttributes at{};
+    return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs == kLaunchRegs;
+  }();
+  if (!regs_ok) return cudaErrorLaunchOutOfResources;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};

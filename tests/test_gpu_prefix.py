@@ -112,7 +112,7 @@ def test_batches(sizes, pre):
     check(setup(7, sizes, pre, rng.integers(1, 200, sum(sizes)), hq=8, hkv=2), f"{len(sizes)}x{pre[0]}")
 
 
-@pytest.mark.parametrize("rk,rv,h", [(1, 1, 128), (1, 0, 128), (0, 0, 128), (0, 1, 64), (1, 1, 16)])
+@pytest.mark.parametrize("rk,rv,h", [(1, 1, 128), (1, 0, 128), (0, 0, 128), (0, 1, 64), (1, 1, 64), (1, 0, 32), (1, 1, 16)])
 @pytest.mark.parametrize("dt,meta", [(torch.bfloat16, True), (torch.float16, False)])
 def test_rotations_and_formats(rk, rv, h, dt, meta):
     rng = np.random.default_rng(h)
