@@ -270,15 +270,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     L = 0;
   }
   PrefixGroup pg{0, 0, 0, 0, 0, 0, 0};
-  uint32_t prefix_tiles = 0;
   int skip_pages = 0;
   if constexpr (SHARED) {
     // max_seq_len bounds the whole sequence here, max_own_len what follows
     // the prefix.  A length inside the prefix is an error (0: an idle row).
     bool bad = false;
-    pg = prefix_scan(p.prefix, P, p.group, p.num_kv_heads, p.num_seqs, lane,
-                     [&](const PrefixGroup& r, uint32_t) { return r.first <= seq && seq < r.end; }, &bad,
-                     &prefix_tiles);
+    uint32_t total;
+    pg = prefix_scan<false>(p.prefix, P, p.group, p.num_kv_heads, p.num_seqs, lane,
+                            [&](const PrefixGroup& r, uint32_t) { return r.first <= seq && seq < r.end; }, &bad,
+                            &total);
     if (bad && seq == 0 && split == 0 && kvh == 0 && warp == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     if (L < pg.tokens || L - pg.tokens > p.max_own_len) {
       if (L != 0 && split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
@@ -294,18 +294,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   const int p_end = min(n_pages, p_begin + p.pages_per_split);
   const bool direct = (p.num_splits == 1);
 
-  auto store_out = [&](int idx, float o) {
-    const int64_t at = (int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx;
-    if constexpr (SHARED) {
-      // the one rounding of a 16-bit output
-      if (p.out16) {
-        p.out16[at] = p.in_f16 ? __half_as_ushort(__float2half_rn(o))
-                               : __bfloat16_as_ushort(__float2bfloat16_rn(o));
-        return;
-      }
-    }
-    p.out[at] = o;
-  };
   // (a sequence that ends with its prefix still merges the prefix's partials)
   if (p_begin >= p_end && !(SHARED && split == 0 && n_pages == 0 && pg.tokens > 0)) {
     // nothing to attend over here; an empty sequence still owes a zero row
@@ -314,8 +302,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       // complete before that one)
       if (behind || (split == 0 && n_pages == 0)) pdl_wait_then_release();
     }
-    if (split == 0 && n_pages == 0)
-      for (int idx = tid; idx < G * kOutD; idx += kThreads) store_out(idx, 0.0f);
+    if (split == 0 && n_pages == 0) {
+      const int64_t row = (int64_t(seq) * p.num_q_heads + hq0) * kOutD;
+      for (int idx = tid; idx < G * kOutD; idx += kThreads) {
+        if (SHARED && p.out16)
+          p.out16[row + idx] = 0;
+        else
+          p.out[row + idx] = 0.0f;
+      }
+    }
     return;
   }
 
@@ -1114,17 +1109,184 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
   }
   __syncthreads();
+
+  if constexpr (SHARED) {
+    // ---- SHARED: a warp per head from here, lane l holding dims 4 l .. + 3.
+    // This split's partial, the other splits' and the prefix pass's are
+    // weighted by 2^(m - M) / l, the inverse rotation runs in shuffles.
+    constexpr int kHeads = (kMaxGroup + kWarps - 1) / kWarps;  // per warp
+    float4 num[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = warp + i * kWarps;
+      if (h >= G) continue;
+      const float z = tot[kMaxGroup + h];
+      float v[4] = {z, z, z, z};
+#pragma unroll 4
+      for (int w = 0; w < nw; ++w) {
+        const float f = wgt[w * kMaxGroup + h];
+        const float* a = red_acc + (w * kMaxGroup + h) * kRedStride + red_col(4 * lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(a[e], f, v[e]);
+      }
+      num[i] = make_float4(v[0], v[1], v[2], v[3]);
+      if (!direct) {
+        const int64_t row = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits + split;
+        reinterpret_cast<float4*>(p.part_o + row * D)[lane] = num[i];
+        if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * row) = make_float2(tot[2 * kMaxGroup + h], tot[h]);
+      }
+    }
+    bool merge_ok = true;
+    if (!direct) {
+      __syncthreads();  // every partial is written
+      if (tid == 0) {
+        const uint32_t done = arrived + 1u;
+        if (done > uint32_t(ns)) report(p.dev_status, SAW_ERR_DEVICE_INDEX);  // not zero-filled
+        bool ok = done == uint32_t(ns);
+        *flag = ok;
+        if (!ok) {
+          // publish: release (cumulative over the barrier above)
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(tk + 1) : "memory");
+        } else {
+          const uint32_t want = uint32_t(ns - 1);
+          const long long t0 = clock64();
+          while (!(ok = (ld_acquire_u32(tk + 1) == want))) {
+            if (clock64() - t0 > kWaitLimitCycles) break;
+            __nanosleep(32);
+          }
+          if (ok) {
+            tk[0] = 0u;  // every split has counted and published: ready for the next call
+            tk[1] = 0u;
+          } else {
+            report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
+          }
+          flag[1] = ok ? 1 : 0;
+        }
+      }
+      __syncthreads();
+      if (*flag == 0) {
+        if (behind) pdl_wait_then_release();
+        return;
+      }
+      merge_ok = flag[1] != 0;
+    }
+    // the prefix pass's partials of these rows: np of them from slot `slot` on
+    int np = 0, row0 = 0;
+    int64_t slot = 0;
+    if (pg.tokens > 0) {
+      bool bad = false;
+      uint32_t total;
+      const PrefixGroup at = prefix_scan<true>(
+          p.prefix, P, p.group, p.num_kv_heads, p.num_seqs, lane,
+          [&](const PrefixGroup& r, uint32_t) { return r.first <= seq && seq < r.end; }, &bad, &total);
+      const uint32_t chunk = prefix_chunk(total, p.prefix.ctas);
+      const int per = prefix_seqs_per_block(p.group);
+      const int blk = (seq - at.first) / per;
+      const uint32_t u = uint32_t(kvh) * at.blocks + blk;
+      const uint32_t t0 = at.tile0 + u * at.tiles;
+      const uint32_t c0 = t0 / chunk, c1 = (t0 + at.tiles - 1) / chunk;
+      np = int(c1 - c0) + 1;
+      row0 = (seq - at.first - blk * per) * p.group;
+      slot = int64_t(at.unit0) + u + c0;
+    }
+    if (behind) pdl_wait_then_release();  // the prefix kernel is complete
+    const float4* po = reinterpret_cast<const float4*>(p.prefix.part) + prefix_part_index(slot) + row0 + lane * kPrefixRows;
+    const float2* pm = reinterpret_cast<const float2*>(p.prefix.part_ml) + slot * kPrefixRows + row0;
+    const int others = merge_ok && !direct ? ns : 0;  // splits, this one among them
+    const int nt = others + np;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = warp + i * kWarps;
+      if (h >= G) continue;
+      const int64_t srow = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits;
+      float M = tot[2 * kMaxGroup + h], den = tot[h];
+      float4 o = num[i];
+      // partial j of nt: a split's, or the prefix's
+      for (int j0 = 0; j0 < nt; j0 += 32) {
+        const int j = j0 + lane;
+        float2 x = make_float2(-INFINITY, 0.0f);
+        if (j < others) {
+          if (j != split) x = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + srow + j);
+        } else if (j < nt) {
+          x = __ldcg(pm + int64_t(j - others) * kPrefixRows + h);
+        }
+        float Mn = fmaxf(M, x.x);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(kFull, Mn, d));
+        const float Mu = (Mn == -INFINITY) ? 0.0f : Mn;
+        const float f = ex2(x.x - Mu), keep = ex2(M - Mu);
+        float dl = x.y * f;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) dl += __shfl_xor_sync(kFull, dl, d);
+        den = den * keep + dl;
+        o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+        M = Mn;
+        const int n = min(32, nt - j0);
+        constexpr int kBatch = 8;  // loads in flight
+        for (int b0 = 0; b0 < n; b0 += kBatch) {
+          float4 v[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int jj = j0 + b0 + b;
+            v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (jj < others) {
+              if (jj != split) v[b] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (srow + jj) * D) + lane);
+            } else if (jj < nt && b0 + b < n) {
+              v[b] = __ldcg(po + prefix_part_index(jj - others) + h);
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const float wj = __shfl_sync(kFull, f, (b0 + b) & 31);
+            o.x = fmaf(v[b].x, wj, o.x);
+            o.y = fmaf(v[b].y, wj, o.y);
+            o.z = fmaf(v[b].z, wj, o.z);
+            o.w = fmaf(v[b].w, wj, o.w);
+          }
+        }
+      }
+      const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+      float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+      if (p.rotate_v) {
+        const float a0 = x[0] + x[1], a1 = x[0] - x[1], a2 = x[2] + x[3], a3 = x[2] - x[3];
+        x[0] = a0 + a2;
+        x[2] = a0 - a2;
+        x[1] = a1 + a3;
+        x[3] = a1 - a3;
+        for (int s = 4; s < p.block_h; s <<= 1) {
+          const float sign = (lane & (s >> 2)) ? -1.0f : 1.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = fmaf(x[e], sign, __shfl_xor_sync(kFull, x[e], s >> 2));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= p.c_h;
+      }
+      const int64_t at = (int64_t(seq) * p.num_q_heads + hq0 + h) * D + 4 * lane;
+      if (p.out16) {  // the one rounding of a 16-bit output
+        uint2 w;
+        if (p.in_f16) {
+          w = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+          w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+        *reinterpret_cast<uint2*>(p.out16 + at) = w;
+      } else {
+        *reinterpret_cast<float4*>(p.out + at) = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    return;
+  }
+
   for (int idx = tid; idx < G * D; idx += kThreads) {
     const int h = idx / D, dd = idx - h * D;
     float num = tot[kMaxGroup + h];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       if (w < nw) num += red_acc[(w * kMaxGroup + h) * kRedStride + red_col(dd)] * wgt[w * kMaxGroup + h];
-    if (direct && !SHARED) {
+    if (direct) {
       const float den = tot[h];
       qs[h * D + dd] = (den > 0.0f) ? num / den : 0.0f;
-    } else if (direct) {
-      qs[h * D + dd] = num;
     } else {
       // publish the partial, and keep it here in case this split merges
       // (den and M stay in tot)
@@ -1138,7 +1300,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
   }
 
-  bool merge_ok = true;
   if (!direct) {
     if (tid == 0) {
       // merge protocol, part 2: the split whose arrival completed the count
@@ -1154,7 +1315,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       // publish: release (cumulative over the barrier above) orders this
       // CTA's partials before the count the merging split waits for
       if (tid == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(tk + 1) : "memory");
-      if (behind) pdl_wait_then_release();
       return;
     }
     // ---- the last split to arrive: wait (bounded) until every other split
@@ -1178,31 +1338,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       flag[1] = ok ? 1 : 0;  // a word of its own: flag[0] may still be read
     }
     __syncthreads();
-    merge_ok = flag[1] != 0;
-  }
-  int np = 0;                     // partials of the prefix pass, after the splits'
-  int pre_row = 0;                // this sequence's first row in its unit
-  const float4* pre_o = nullptr;  // the first of them
-  const float2* pre_ml = nullptr;
-  if constexpr (SHARED) {
-    if (behind) pdl_wait_then_release();  // the prefix kernel's partials are complete
-    if (pg.tokens > 0) {
-      const uint32_t chunk = prefix_chunk(prefix_tiles, p.prefix.ctas);
-      const int per = prefix_seqs_per_block(p.group);
-      const int blk = (seq - pg.first) / per;
-      const uint32_t u = uint32_t(kvh) * pg.blocks + blk;
-      const uint32_t t0 = pg.tile0 + u * pg.tiles;
-      const uint32_t c0 = t0 / chunk, c1 = (t0 + pg.tiles - 1) / chunk;
-      np = int(c1 - c0) + 1;
-      pre_row = (seq - pg.first - blk * per) * p.group;
-      const int64_t slot = int64_t(pg.unit0) + u + c0;
-      pre_o = reinterpret_cast<const float4*>(p.prefix.part) + prefix_part_index(slot);
-      pre_ml = reinterpret_cast<const float2*>(p.prefix.part_ml) + slot * kPrefixRows;
-    }
-    __syncthreads();  // tot and qs are complete (one split: nothing above met)
-  }
-  if (!direct || SHARED) {
-    const int nt = ns + np;
+    const bool merge_ok = flag[1] != 0;
     // item = (head, 4 dims); four threads per item share the splits.  Every
     // load is issued before any is used (one round of L2 latency).
     constexpr int kMaxSplitsPerThread = 8;
@@ -1211,9 +1347,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const int t = base + tid;
       const int item = t >> 2, part = t & 3;
       const bool active = item < G * kItems;
-      // (SHARED: heads side by side, as the prefix's partials lie)
-      const int h = !active ? 0 : SHARED ? item % G : item / kItems;
-      const int ch = !active ? 0 : SHARED ? item / G : item % kItems;
+      const int h = active ? item / kItems : 0, ch = item % kItems;
       const int64_t row0 = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits;
       const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row0;
       const float4* po = reinterpret_cast<const float4*>(p.part_o + row0 * D) + ch;
@@ -1221,23 +1355,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       float M = -INFINITY;
       float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float den = 0.0f;
-      for (int sp0 = part; sp0 < nt; sp0 += 4 * kMaxSplitsPerThread) {
+      for (int sp0 = part; sp0 < ns; sp0 += 4 * kMaxSplitsPerThread) {
         float2 v[kMaxSplitsPerThread];
         float4 o[kMaxSplitsPerThread];
 #pragma unroll
         for (int u = 0; u < kMaxSplitsPerThread; ++u) {
           const int sp = sp0 + 4 * u;
           const bool mine = sp == split;
-          if constexpr (SHARED) {
-            if (sp >= ns) {
-              const bool in = active && sp < nt;
-              const int row = pre_row + h;
-              v[u] = in ? __ldcg(pre_ml + int64_t(sp - ns) * kPrefixRows + row) : make_float2(-INFINITY, 0.0f);
-              o[u] = in ? __ldcg(pre_o + prefix_part_index(sp - ns) + ch * kPrefixRows + row)
-                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              continue;
-            }
-          }
           const bool in = active && sp < ns && (mine || merge_ok);
           v[u] = !in ? make_float2(-INFINITY, 0.0f)
                      : mine ? make_float2(tot[2 * kMaxGroup + h], tot[h]) : __ldcg(&ml[sp]);
@@ -1296,7 +1420,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   for (int idx = tid; idx < G * kOutD; idx += kThreads) {
     const int h = idx / kOutD, dd = idx - h * kOutD;
     const float o = PAIR ? qs[h * D + (h >> 2) * kOutD + dd] : qs[idx];
-    store_out(idx, o * post);
+    p.out[(int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx] = o * post;
   }
 }
 

@@ -346,7 +346,7 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Seg
     bool bad = false;  // (reported by the decode kernel)
     uint32_t total;
     const uint32_t at = w.at;
-    w.g = prefix_scan(p.prefix, p.page_size, p.group, p.num_kv_heads, p.num_seqs, lane,
+    w.g = prefix_scan<true>(p.prefix, p.page_size, p.group, p.num_kv_heads, p.num_seqs, lane,
                       [&](const PrefixGroup& r, uint32_t t) { return r.tile0 <= at && at < r.tile0 + t; }, &bad, &total);
     if (!w.placed) {  // the first look only brings the total
       const uint32_t chunk = prefix_chunk(total, p.prefix.ctas);

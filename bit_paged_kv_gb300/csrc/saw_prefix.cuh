@@ -42,7 +42,8 @@ __device__ __forceinline__ uint32_t warp_scan_u32(uint32_t v, int lane) {  // in
 // -- out of range, descending, or reaching back over an earlier one, so that
 // the others stay disjoint and their units within the workspace -- shares
 // nothing; *bad is set in some lane.
-template <typename Pick>
+// PLACE false: only the group itself, without unit0, tile0 and *total.
+template <bool PLACE, typename Pick>
 __device__ __forceinline__ PrefixGroup prefix_scan(const PrefixSide& s, int page_size, int group,
                                                    int hkv, int num_seqs, int lane, Pick pick,
                                                    bool* bad, uint32_t* total) {
@@ -78,9 +79,13 @@ __device__ __forceinline__ PrefixGroup prefix_scan(const PrefixSide& s, int page
       r.blocks = r.tiles > 0 ? (hi - lo + per - 1) / per : 0;
     }
     const uint32_t u = uint32_t(r.blocks) * hkv, t = u * r.tiles;
-    const uint32_t ui = warp_scan_u32(u, lane), ti = warp_scan_u32(t, lane);
-    r.unit0 = units + ui - u;
-    r.tile0 = tiles + ti - t;
+    uint32_t ui = 0, ti = 0;
+    if constexpr (PLACE) {
+      ui = warp_scan_u32(u, lane);
+      ti = warp_scan_u32(t, lane);
+      r.unit0 = units + ui - u;
+      r.tile0 = tiles + ti - t;
+    }
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, pick(r, t));
     if (hit && !have) {
       const int at = __ffs(hit) - 1;
@@ -89,12 +94,16 @@ __device__ __forceinline__ PrefixGroup prefix_scan(const PrefixSide& s, int page
       found.tokens = __shfl_sync(0xFFFFFFFFu, r.tokens, at);
       found.tiles = __shfl_sync(0xFFFFFFFFu, r.tiles, at);
       found.blocks = __shfl_sync(0xFFFFFFFFu, r.blocks, at);
-      found.unit0 = __shfl_sync(0xFFFFFFFFu, r.unit0, at);
-      found.tile0 = __shfl_sync(0xFFFFFFFFu, r.tile0, at);
+      if constexpr (PLACE) {
+        found.unit0 = __shfl_sync(0xFFFFFFFFu, r.unit0, at);
+        found.tile0 = __shfl_sync(0xFFFFFFFFu, r.tile0, at);
+      }
       have = true;
     }
-    units += __shfl_sync(0xFFFFFFFFu, ui, 31);
-    tiles += __shfl_sync(0xFFFFFFFFu, ti, 31);
+    if constexpr (PLACE) {
+      units += __shfl_sync(0xFFFFFFFFu, ui, 31);
+      tiles += __shfl_sync(0xFFFFFFFFu, ti, 31);
+    }
     top = max(top, __shfl_sync(0xFFFFFFFFu, reach, 31));
   }
   *total = tiles;
