@@ -263,22 +263,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   const int hq0 = kvh * G;
   constexpr int kOutD = PAIR ? D / 2 : D;     // dims of an output row
   const int kv0 = PAIR ? 2 * kvh : kvh;       // (first) kv-head of this CTA
+  constexpr int kQHeads = (kMaxGroup + kWarps - 1) / kWarps;  // q heads per warp
+  uint2 qpre[kQHeads];  // SHARED behind a prefix kernel: this lane's q, under way from here
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int i = 0; i < kQHeads; ++i) {
+      const int h = warp + i * kWarps;
+      qpre[i] = make_uint2(0u, 0u);
+      if (behind && h < G)
+        qpre[i] = reinterpret_cast<const uint2*>(p.q + (int64_t(seq) * p.num_q_heads + hq0 + h) * D)[lane];
+    }
+  }
 
   int L = p.seq_lens[seq];
   if (L < 0 || L > p.max_seq_len) {
     if (split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     L = 0;
   }
-  PrefixGroup pg{0, 0, 0, 0, 0, 0, 0};
+  PrefixGroup pg{0, 0, 0, 0, 0, 0};
   int skip_pages = 0;
   if constexpr (SHARED) {
     // max_seq_len bounds the whole sequence here, max_own_len what follows
     // the prefix.  A length inside the prefix is an error (0: an idle row).
     bool bad = false;
-    uint32_t total;
-    pg = prefix_scan<false>(p.prefix, P, p.group, p.num_kv_heads, p.num_seqs, lane,
-                            [&](const PrefixGroup& r, uint32_t) { return r.first <= seq && seq < r.end; }, &bad,
-                            &total);
+    pg = prefix_of_seq(p.prefix, seq, P, p.group, p.num_seqs, lane, &bad);
     if (bad && seq == 0 && split == 0 && kvh == 0 && warp == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     if (L < pg.tokens || L - pg.tokens > p.max_own_len) {
       if (L != 0 && split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
@@ -502,7 +510,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // sits at k-step 2 (o / 8) + ((j >> 1) & 1), thread-in-group c, register
   // j & 1, half (j >> 2) & 1: the nibble the K codes put there.
   constexpr int kE = DM::kE;
-  for (int h = warp; h < kMaxGroup; h += kWarps) {  // (4-warp CTAs: two heads per warp)
+#pragma unroll
+  for (int qi = 0; qi < kQHeads; ++qi) {  // (4-warp CTAs: two heads per warp)
+    const int h = warp + qi * kWarps;
+    if (h >= kMaxGroup) break;
     float x[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) x[e] = 0.0f;
@@ -514,7 +525,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
                                kE * (PAIR ? (lane & 15) : lane);
         const bool f16 = p.in_f16 != 0;
         uint32_t raw[kE / 2];
-        if (kE == 2) {
+        if (SHARED && behind) {
+          raw[0] = qpre[qi].x;
+          raw[kE / 2 - 1] = qpre[qi].y;
+        } else if (kE == 2) {
           raw[0] = *reinterpret_cast<const uint32_t*>(qrow);
         } else {
 #pragma unroll
@@ -564,15 +578,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     for (int e = 0; e < kE; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
     for (int x2 = 16; x2 >= 1; x2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, x2));
-    int ex;
-    frexpf(amax, &ex);                       // amax < 2^ex (ex = 0 for amax = 0)
+    // amax < 2^ex (a zero or subnormal amax gives S = 100)
+    const int ex = int(__float_as_uint(amax) >> 23) - 126;
     const int S = min(max(14 - ex, -100), 100);
+    auto pow2 = [](int e) { return __uint_as_float(uint32_t(127 + e) << 23); };  // |e| <= 126
     float part = 0.0f;
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       const int d = kE * lane + e;
       const int se = (d & 1) ? S - 4 : S;
-      const float y = ldexpf(x[e], se);
+      const float y = x[e] * pow2(se);
       const __half hi = __float2half_rn(y);
       const __half lo = __float2half_rn(y - __half2float(hi));
       const int c_ = d / (D / 4);
@@ -590,13 +605,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         qh[(t * 32 + h * 4 + c_) * 4 + w2] = hi;
         qh[kLo + (t * 32 + h * 4 + c_) * 4 + w2] = lo;
       }
-      part += ldexpf(__half2float(hi) + __half2float(lo), -se);
+      part += (__half2float(hi) + __half2float(lo)) * pow2(-se);
     }
 #pragma unroll
     for (int x2 = 16; x2 >= 1; x2 >>= 1) part += __shfl_xor_sync(kFull, part, x2);
     if (lane == 0) {
       qsum[h] = part;
-      qsum[kMaxGroup + h] = ldexpf(1.0f, 24 - S);
+      qsum[kMaxGroup + h] = pow2(24 - S);
     }
   }
   __syncthreads();
@@ -1170,30 +1185,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       merge_ok = flag[1] != 0;
     }
-    // the prefix pass's partials of these rows: np of them from slot `slot` on
+    if (behind) pdl_wait_then_release();  // the prefix kernel is complete
+    // its partials of these rows: np of them from part `slot` on
     int np = 0, row0 = 0;
     int64_t slot = 0;
     if (pg.tokens > 0) {
-      bool bad = false;
-      uint32_t total;
-      const PrefixGroup at = prefix_scan<true>(
-          p.prefix, P, p.group, p.num_kv_heads, p.num_seqs, lane,
-          [&](const PrefixGroup& r, uint32_t) { return r.first <= seq && seq < r.end; }, &bad, &total);
-      const uint32_t chunk = prefix_chunk(total, p.prefix.ctas);
+      const int chunk = __ldcg(p.prefix.plan);
+      const int part0 = __ldcg(p.prefix.plan + 1 + pg.index);
       const int per = prefix_seqs_per_block(p.group);
-      const int blk = (seq - at.first) / per;
-      const uint32_t u = uint32_t(kvh) * at.blocks + blk;
-      const uint32_t t0 = at.tile0 + u * at.tiles;
-      const uint32_t c0 = t0 / chunk, c1 = (t0 + at.tiles - 1) / chunk;
-      np = int(c1 - c0) + 1;
-      row0 = (seq - at.first - blk * per) * p.group;
-      slot = int64_t(at.unit0) + u + c0;
+      const int blk = (seq - pg.first) / per;
+      np = (pg.tiles + chunk - 1) / chunk;
+      row0 = (seq - pg.first - blk * per) * p.group;
+      slot = int64_t(part0) + int64_t(kvh * pg.blocks + blk) * np;
     }
-    if (behind) pdl_wait_then_release();  // the prefix kernel is complete
     const float4* po = reinterpret_cast<const float4*>(p.prefix.part) + prefix_part_index(slot) + row0 + lane * kPrefixRows;
     const float2* pm = reinterpret_cast<const float2*>(p.prefix.part_ml) + slot * kPrefixRows + row0;
     const int others = merge_ok && !direct ? ns : 0;  // splits, this one among them
     const int nt = others + np;
+    // partial j of nt: a split's, or the prefix's
+    auto load_ml = [&](int h, int64_t srow, int j) {
+      if (j < others) return j != split ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + srow + j)
+                                        : make_float2(-INFINITY, 0.0f);
+      return j < nt ? __ldcg(pm + int64_t(j - others) * kPrefixRows + h) : make_float2(-INFINITY, 0.0f);
+    };
+    auto load_o = [&](int h, int64_t srow, int j) {
+      if (j < others) return j != split ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (srow + j) * D) + lane)
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      return j < nt ? __ldcg(po + prefix_part_index(j - others) + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    constexpr int kBatch = 12 / kHeads;  // loads in flight per head
+    float2 ml[kHeads];
+    float4 v[kHeads][kBatch];  // every head's first loads before any is used
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = warp + i * kWarps;
+      const int64_t srow = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits;
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      if (h < G) {
+        ml[i] = load_ml(h, srow, lane);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) v[i][b] = load_o(h, srow, b);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       const int h = warp + i * kWarps;
@@ -1201,47 +1234,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const int64_t srow = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits;
       float M = tot[2 * kMaxGroup + h], den = tot[h];
       float4 o = num[i];
-      // partial j of nt: a split's, or the prefix's
       for (int j0 = 0; j0 < nt; j0 += 32) {
-        const int j = j0 + lane;
-        float2 x = make_float2(-INFINITY, 0.0f);
-        if (j < others) {
-          if (j != split) x = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + srow + j);
-        } else if (j < nt) {
-          x = __ldcg(pm + int64_t(j - others) * kPrefixRows + h);
-        }
-        float Mn = fmaxf(M, x.x);
+        if (j0 > 0) ml[i] = load_ml(h, srow, j0 + lane);
+        float Mn = fmaxf(M, ml[i].x);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(kFull, Mn, d));
         const float Mu = (Mn == -INFINITY) ? 0.0f : Mn;
-        const float f = ex2(x.x - Mu), keep = ex2(M - Mu);
-        float dl = x.y * f;
+        const float f = ex2(ml[i].x - Mu), keep = ex2(M - Mu);
+        float dl = ml[i].y * f;
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) dl += __shfl_xor_sync(kFull, dl, d);
         den = den * keep + dl;
         o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
         M = Mn;
         const int n = min(32, nt - j0);
-        constexpr int kBatch = 8;  // loads in flight
         for (int b0 = 0; b0 < n; b0 += kBatch) {
-          float4 v[kBatch];
+          if (j0 + b0 > 0) {
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int jj = j0 + b0 + b;
-            v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (jj < others) {
-              if (jj != split) v[b] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (srow + jj) * D) + lane);
-            } else if (jj < nt && b0 + b < n) {
-              v[b] = __ldcg(po + prefix_part_index(jj - others) + h);
-            }
+            for (int b = 0; b < kBatch; ++b) v[i][b] = load_o(h, srow, j0 + b0 + b);
           }
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
-            const float wj = __shfl_sync(kFull, f, (b0 + b) & 31);
-            o.x = fmaf(v[b].x, wj, o.x);
-            o.y = fmaf(v[b].y, wj, o.y);
-            o.z = fmaf(v[b].z, wj, o.z);
-            o.w = fmaf(v[b].w, wj, o.w);
+            const float wj = b0 + b < n ? __shfl_sync(kFull, f, (b0 + b) & 31) : 0.0f;
+            o.x = fmaf(v[i][b].x, wj, o.x);
+            o.y = fmaf(v[i][b].y, wj, o.y);
+            o.z = fmaf(v[i][b].z, wj, o.z);
+            o.w = fmaf(v[i][b].w, wj, o.w);
           }
         }
       }

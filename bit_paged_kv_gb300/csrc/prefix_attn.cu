@@ -329,51 +329,130 @@ struct __align__(16) Segment {
 };
 static_assert(sizeof(Segment) == 48, "kOffSeg");
 
-// Walks this CTA's tiles segment by segment.  The producer warp does, and
-// announces each segment to the other warps through a ring in shared memory:
-// one copy of this code (in every role it was half of a kernel of 137 KB, and
-// instruction fetches were a fifth of all stalls).
-struct Walk {
-  PrefixGroup g;     // holds tile `at` once found
-  uint32_t at, end;
-  bool placed, found;
+// The producer warp finds this CTA's parts and announces them to the other
+// warps through a ring in shared memory: one copy of this code (in every role
+// it was half of a kernel of 137 KB, and instruction fetches were a fifth of
+// all stalls).  With up to 32 groups a lane keeps its group in registers.
+struct Work {
+  PrefixGroup mine;   // group base + lane
+  int base;
+  uint32_t chunk;     // tiles per part
+  uint32_t next;      // this CTA's next part
+  uint32_t before;    // parts of the groups before `base`
+  int top;            // furthest end of the groups up to base + 31
 };
 
-// Whole warp: the next segment, or false at the end of this CTA's piece.
-__device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Segment& s, int lane) {
-#pragma unroll 1
-  while (!w.placed || (w.at < w.end && !w.found)) {
-    bool bad = false;  // (reported by the decode kernel)
-    uint32_t total;
-    const uint32_t at = w.at;
-    w.g = prefix_scan<true>(p.prefix, p.page_size, p.group, p.num_kv_heads, p.num_seqs, lane,
-                      [&](const PrefixGroup& r, uint32_t t) { return r.tile0 <= at && at < r.tile0 + t; }, &bad, &total);
-    if (!w.placed) {  // the first look only brings the total
-      const uint32_t chunk = prefix_chunk(total, p.prefix.ctas);
-      const uint64_t lo = uint64_t(blockIdx.x) * chunk;
-      w.at = uint32_t(min(lo, uint64_t(total)));
-      w.end = uint32_t(min(lo + chunk, uint64_t(total)));
-      w.placed = true;
-    } else {
-      w.found = true;
+__device__ __forceinline__ uint32_t group_parts(const PrefixGroup& g, int hkv, uint32_t chunk) {
+  return uint32_t(g.blocks) * hkv * ((uint32_t(g.tiles) + chunk - 1) / chunk);
+}
+
+// Whole warp: the groups' first 32, and the chunk.  Lanes weigh chunks
+// ceil(Tmax / n) for n = 1 .. 64 parts of the longest prefix, two each: rounds
+// of the fullest CTA times the cost of a part.  More parts than max(units, 2
+// CTAs) are not considered (the workspace holds no more).
+__device__ __forceinline__ Work plan_work(const PrefixParams& p, int lane) {
+  Work w;
+  bool bad = false;  // (reported by the decode kernel)
+  int top = 0, tmax = 0;
+  w.base = 0;
+  w.before = 0;
+  for (int g0 = 0; g0 < max(p.prefix.num_groups, 1); g0 += 32) {
+    const PrefixGroup r = prefix_load(p.prefix, g0, p.page_size, p.group, p.num_seqs, lane, &top, &bad);
+    if (g0 == 0) {
+      w.mine = r;
+      w.top = top;
+    }
+    tmax = max(tmax, r.blocks > 0 ? r.tiles : 0);
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) tmax = max(tmax, __shfl_xor_sync(kAll, tmax, d));
+  tmax = max(tmax, 1);
+  uint32_t c[2], parts[2] = {0, 0}, units = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) c[k] = (uint32_t(tmax) + 2 * lane + k) / (2 * lane + k + 1);
+  top = w.top;
+  for (int g0 = 0; g0 < p.prefix.num_groups; g0 += 32) {
+    PrefixGroup r = w.mine;
+    if (g0 > 0) r = prefix_load(p.prefix, g0, p.page_size, p.group, p.num_seqs, lane, &top, &bad);
+    const int n = min(32, p.prefix.num_groups - g0);
+    for (int g = 0; g < n; ++g) {
+      const uint32_t u = uint32_t(__shfl_sync(kAll, r.blocks, g)) * p.num_kv_heads;
+      const uint32_t t = uint32_t(__shfl_sync(kAll, r.tiles, g));
+      units += u;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) parts[k] += u * ((t + c[k] - 1) / c[k]);
     }
   }
-  if (w.at >= w.end || w.g.tiles <= 0) return false;
-  const uint32_t in = w.at - w.g.tile0;
-  const uint32_t u = in / uint32_t(w.g.tiles);
-  const int per = prefix_seqs_per_block(p.group);
-  s.kvh = int(u / uint32_t(w.g.blocks));
-  const int blk = int(u - uint32_t(s.kvh) * w.g.blocks);
-  s.leader = w.g.first;
-  s.seq0 = w.g.first + blk * per;
-  s.rows = min(per, w.g.end - s.seq0) * p.group;
-  s.tile = int(in - u * uint32_t(w.g.tiles));
-  s.tiles = min(w.g.tiles - s.tile, int(w.end - w.at));
-  s.tokens = w.g.tokens;
-  s.slot = int64_t(w.g.unit0) + u + blockIdx.x;
-  w.at += s.tiles;
-  w.found = w.at < w.g.tile0 + uint32_t(w.g.blocks) * p.num_kv_heads * w.g.tiles;
-  return true;
+  uint32_t best = 0xFFFFFFFFu, cost = 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t x = ((parts[k] + p.prefix.ctas - 1) / p.prefix.ctas) * (c[k] + kPartCost);
+    const bool fits = parts[k] <= max(units, 2u * p.prefix.ctas);
+    if (fits && x < cost) {
+      cost = x;
+      best = c[k];
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    const uint32_t oc = __shfl_xor_sync(kAll, cost, d), ob = __shfl_xor_sync(kAll, best, d);
+    if (oc < cost || (oc == cost && ob > best)) {
+      cost = oc;
+      best = ob;
+    }
+  }
+  w.chunk = best;
+  w.next = blockIdx.x;
+  return w;
+}
+
+// Whole warp: the next part of this CTA, or false after the last.  CTA 0 also
+// leaves the plan for the decode kernel on its way.
+__device__ __forceinline__ bool next_segment(const PrefixParams& p, Work& w, Segment& s, int lane) {
+  for (;;) {
+    const uint32_t n = group_parts(w.mine, p.num_kv_heads, w.chunk);
+    const uint32_t upto = w.before + warp_scan_u32(n, lane);
+    const uint32_t hit = __ballot_sync(kAll, w.next < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const PrefixGroup g = prefix_from(w.mine, src);
+      const uint32_t part = w.next - __shfl_sync(kAll, upto - n, src);
+      const uint32_t per_unit = (uint32_t(g.tiles) + w.chunk - 1) / w.chunk;
+      const uint32_t u = part / per_unit, j = part - u * per_unit;
+      const int per = prefix_seqs_per_block(p.group);
+      s.kvh = int(u / uint32_t(g.blocks));
+      const int blk = int(u - uint32_t(s.kvh) * g.blocks);
+      s.leader = g.first;
+      s.seq0 = g.first + blk * per;
+      s.rows = min(per, g.end - s.seq0) * p.group;
+      s.tile = int(j * uint32_t(g.tiles) / per_unit);
+      s.tiles = int((j + 1) * uint32_t(g.tiles) / per_unit) - s.tile;
+      s.tokens = g.tokens;
+      s.slot = int64_t(w.next);
+      w.next += gridDim.x;
+      return true;
+    }
+    // beyond these 32 groups
+    w.before = __shfl_sync(kAll, upto, 31);
+    w.base += 32;
+    if (w.base >= p.prefix.num_groups) return false;
+    bool bad = false;
+    w.mine = prefix_load(p.prefix, w.base, p.page_size, p.group, p.num_seqs, lane, &w.top, &bad);
+  }
+}
+
+// CTA 0's producer warp, when its own work is done: the plan.
+__device__ __forceinline__ void publish_plan(const PrefixParams& p, uint32_t chunk, int lane) {
+  int top = 0;
+  bool bad = false;
+  uint32_t before = 0;
+  if (lane == 0) p.prefix.plan[0] = int(chunk);
+  for (int g0 = 0; g0 < p.prefix.num_groups; g0 += 32) {
+    const PrefixGroup r = prefix_load(p.prefix, g0, p.page_size, p.group, p.num_seqs, lane, &top, &bad);
+    const uint32_t n = group_parts(r, p.num_kv_heads, chunk), upto = before + warp_scan_u32(n, lane);
+    if (g0 + lane < p.prefix.num_groups) p.prefix.plan[1 + g0 + lane] = int(upto - n);
+    before = __shfl_sync(kAll, upto, 31);
+  }
 }
 
 // ------------------------------------------------------------ expanders
@@ -764,10 +843,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
     constexpr int kChunk = P * 68;
     constexpr int kPages = kKeys / P;               // pages per tile
     constexpr int kAhead = 32 / kPages;             // tiles whose page ids a warp holds
-    Walk walk{{}, 0u, 0u, false, false};
+    Work work = plan_work(p, lane);
+    const uint32_t chunk = work.chunk;
     for (bool more = true; more && !failed; ++segs) {
       Segment sg{};
-      more = next_segment(p, walk, sg, lane);
+      more = next_segment(p, work, sg, lane);
       sg.more = more;
       const int e = segs % kSegs;
       if (segs >= kSegs && !wait_parked(&bars[kSegEmpty + e], ((segs / kSegs) - 1) & 1, failed)) break;
@@ -823,6 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
         __syncwarp();
       }
     }
+    if (blockIdx.x == 0) publish_plan(p, chunk, lane);
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------- MMA issue
     constexpr uint32_t id_s = umma_idesc_f16(128, kKeys);
@@ -865,13 +946,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
   } else {
     // ---------------------------------------------------------- expanders
     const bool is_v = warp < kWarpK;
+    if (is_v) {
+      write_hadamard<F16IN>(smem + kOffV + kOpBytes, tid - 32 * kWarpV, p.rotate_k ? p.block_h : 1);
+      fence_async_smem();
+      __syncwarp();
+    }
     for (Segment sg; take(sg); ++segs) {
       if (is_v) {
         // the rotation matrix, once the last segment is done with the buffers
-        if (it > 0 && !wait_parked(&bars[kPvDone + ((it - 1) & 1)], ((it - 1) >> 1) & 1, failed)) break;
-        write_hadamard<F16IN>(smem + kOffV + kOpBytes, tid - 32 * kWarpV, p.rotate_k ? p.block_h : 1);
-        fence_async_smem();
-        __syncwarp();
+        // (the first one's was written before it was known)
+        if (segs > 0) {
+          if (!wait_parked(&bars[kPvDone + ((it - 1) & 1)], ((it - 1) >> 1) & 1, failed)) break;
+          write_hadamard<F16IN>(smem + kOffV + kOpBytes, tid - 32 * kWarpV, p.rotate_k ? p.block_h : 1);
+          fence_async_smem();
+          __syncwarp();
+        }
         arrive_elect(&bars[kQIn]);
         if (!wait_parked(&bars[kQFull], segs & 1, failed)) break;
       }

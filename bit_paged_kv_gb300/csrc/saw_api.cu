@@ -551,8 +551,8 @@ constexpr size_t kTicketRegion = size_t(1) << 20;
 struct PrefixPlan {
   int32_t ctas;         // 0: no prefix pass, every sequence reads its own pages
   int32_t plan_len;
-  size_t ticket_bytes, split_bytes, part_bytes, ml_bytes;
-  size_t total() const { return ticket_bytes + split_bytes + part_bytes + ml_bytes; }
+  size_t ticket_bytes, split_bytes, part_bytes, ml_bytes, plan_bytes;
+  size_t total() const { return ticket_bytes + split_bytes + part_bytes + ml_bytes + plan_bytes; }
 };
 
 int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
@@ -576,8 +576,10 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
   if (shared) {
     p.ctas = int32_t(sms);
     p.plan_len = max_own_len;
-    p.part_bytes = size_t(units + sms) * saw::kPrefixRows * kHeadDim * 4;
-    p.ml_bytes = size_t(units + sms) * saw::kPrefixRows * 8;
+    const int64_t parts = std::max(units, 2 * sms);
+    p.part_bytes = size_t(parts) * saw::kPrefixRows * kHeadDim * 4;
+    p.ml_bytes = size_t(parts) * saw::kPrefixRows * 8;
+    p.plan_bytes = (size_t(num_groups) * 4 + 4 + 15) / 16 * 16;
   } else {
     p.plan_len = max_prefix_len + max_own_len;
   }
@@ -637,6 +639,10 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
                       workspace, workspace_bytes, 0, formats, dev_status);
   if (rc != SAW_OK || num_seqs == 0) return rc;
   if (out16) p.out16 = static_cast<uint16_t*>(out);
+  // short own parts, one split: four 4-warp CTAs per SM already when that saves
+  // a wave
+  const int sms_now = sm_count();
+  if (p.num_splits == 1 && int64_t(num_seqs) * num_kv_heads > 2 * int64_t(sms_now)) p.warps = 4;
   p.max_blocks = max_blocks_per_seq;
   p.max_seq_len = int32_t(std::min<int64_t>(int64_t(max_prefix_len) + max_own_len,
                                             int64_t(max_blocks_per_seq) * page_size));
@@ -655,6 +661,7 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
     ws += plan.split_bytes;
     p.prefix.part = reinterpret_cast<float*>(ws);
     p.prefix.part_ml = reinterpret_cast<float*>(ws + plan.part_bytes);
+    p.prefix.plan = reinterpret_cast<int32_t*>(ws + plan.part_bytes + plan.ml_bytes);
     saw::PrefixParams x{};
     x.q = p.q;
     x.k_cache = p.k_cache;

@@ -133,8 +133,9 @@ struct PrefixSide {
   int32_t num_groups;
   int32_t max_prefix_len;
   int32_t ctas;                 // CTAs of the prefix pass; 0: none ran, nothing is shared
-  float* part;                  // numerators, 64 KB per slot
+  float* part;                  // numerators, 64 KB per part
   float* part_ml;               // (m, l) per row
+  int32_t* plan;                // [1 + num_groups]: tiles per part, first part of each group
 };
 
 struct PrefixParams {

@@ -1,15 +1,14 @@
-// saw_prefix.cuh -- how the shared-prefix pass is cut into work, computed the
-// same way by the kernel that writes its partial results and by the decode
-// kernel that reads them.
+// saw_prefix.cuh -- how the shared-prefix pass is cut into work.
 //
 // A group's rows are (sequence, q-head of a kv-head) pairs.  A unit is one
 // kv-head and one block of seqs_per_block(G) neighbouring sequences of a group
-// (at most kPrefixRows rows, one tensor-core tile).  Its keys are tiles of
-// kPrefixKeys tokens, T of them; units of a group follow one another kv-head
-// by kv-head, groups in order, and all tiles form one line that is cut into
-// equal pieces of `chunk` tiles, one per CTA.  Unit u meeting CTA c leaves a
-// partial result in slot u + c: walking along the line, u or c grows at every
-// cut, so slots never collide, and a unit's slots are consecutive.
+// (at most kPrefixRows rows, one tensor-core tile).  Its keys are T tiles of
+// kPrefixKeys tokens, cut into n = ceil(T / chunk) equal parts; part j of unit
+// u (units of a group kv-head by kv-head) is number part0 + u n + j, and parts
+// go round the CTAs.  `chunk` is the one for which the fullest CTA has least to
+// do, a part costing its tiles and kPartCost more: CTAs that took equal pieces
+// of one line of tiles had two units to start more often than one.  The prefix
+// kernel leaves chunk and every group's part0 for the decode kernel's merge.
 #pragma once
 
 #include "saw_device.cuh"
@@ -19,14 +18,16 @@ namespace saw {
 
 __host__ __device__ constexpr int prefix_seqs_per_block(int group) { return kPrefixRows / group; }
 
-// One group (unit0, tile0: units and tiles of the groups before).
+// One group.
 struct PrefixGroup {
   int first, end;      // sequences
   int tokens;          // whole pages of the prefix, in tokens
   int tiles;           // key tiles of a unit
   int blocks;          // blocks of sequences (0 with nothing shared)
-  uint32_t unit0, tile0;
+  int index;
 };
+
+constexpr int kPartCost = 5;  // starting and ending a part, in tiles
 
 __device__ __forceinline__ uint32_t warp_scan_u32(uint32_t v, int lane) {  // inclusive
 #pragma unroll
@@ -37,82 +38,66 @@ __device__ __forceinline__ uint32_t warp_scan_u32(uint32_t v, int lane) {  // in
   return v;
 }
 
-// Whole warp: the first group for which pick(group) holds (zero sizes if none
-// does), and the tiles of all groups.  A group whose entries are inconsistent
-// -- out of range, descending, or reaching back over an earlier one, so that
-// the others stay disjoint and their units within the workspace -- shares
-// nothing; *bad is set in some lane.
-// PLACE false: only the group itself, without unit0, tile0 and *total.
-template <bool PLACE, typename Pick>
-__device__ __forceinline__ PrefixGroup prefix_scan(const PrefixSide& s, int page_size, int group,
-                                                   int hkv, int num_seqs, int lane, Pick pick,
-                                                   bool* bad, uint32_t* total) {
-  PrefixGroup found{0, 0, 0, 0, 0, 0, 0};
-  uint32_t units = 0, tiles = 0;
-  int top = 0;  // end of the groups so far
-  bool have = false;
-  const int per = prefix_seqs_per_block(group);
-  for (int g0 = 0; g0 < s.num_groups; g0 += 32) {
-    const int g = g0 + lane;
-    PrefixGroup r{0, 0, 0, 0, 0, 0, 0};
-    int lo = 0, hi = 0, pre = 0;
-    if (g < s.num_groups) {
-      lo = s.cu_groups[g];
-      hi = s.cu_groups[g + 1];
-      pre = s.prefix_lens[g];
-    }
-    int reach = hi;  // furthest end up to this group
+// Whole warp: group g0 + lane (nothing shared beyond the last).  *top, the
+// furthest end of the groups before g0, moves on.  A group whose entries are
+// inconsistent -- out of range, descending, or reaching back over an earlier
+// one, so that the others stay disjoint and their units within the workspace --
+// shares nothing; *bad is set in its lane.
+__device__ __forceinline__ PrefixGroup prefix_load(const PrefixSide& s, int g0, int page_size, int group,
+                                                   int num_seqs, int lane, int* top, bool* bad) {
+  const int g = g0 + lane;
+  PrefixGroup r{0, 0, 0, 0, 0, g};
+  int lo = 0, hi = 0, pre = 0;
+  if (g < s.num_groups) {
+    lo = s.cu_groups[g];
+    hi = s.cu_groups[g + 1];
+    pre = s.prefix_lens[g];
+  }
+  int reach = hi;  // furthest end up to this group
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, reach, d);
-      if (lane >= d) reach = max(reach, o);
-    }
-    int before = __shfl_up_sync(0xFFFFFFFFu, reach, 1);
-    before = lane == 0 ? top : max(top, before);
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, reach, d);
+    if (lane >= d) reach = max(reach, o);
+  }
+  int before = __shfl_up_sync(0xFFFFFFFFu, reach, 1);
+  before = lane == 0 ? *top : max(*top, before);
+  if (g < s.num_groups) {
     if (lo < before || hi < lo || hi > num_seqs || pre < 0 || pre > s.max_prefix_len) {
-      if (g < s.num_groups) *bad = true;
+      *bad = true;
     } else {
+      const int per = prefix_seqs_per_block(group);
       r.first = lo;
       r.end = hi;
-      r.tokens = pre / page_size * page_size;
+      r.tokens = pre & -page_size;  // (page sizes are powers of two)
       r.tiles = (r.tokens + kPrefixKeys - 1) / kPrefixKeys;
       r.blocks = r.tiles > 0 ? (hi - lo + per - 1) / per : 0;
     }
-    const uint32_t u = uint32_t(r.blocks) * hkv, t = u * r.tiles;
-    uint32_t ui = 0, ti = 0;
-    if constexpr (PLACE) {
-      ui = warp_scan_u32(u, lane);
-      ti = warp_scan_u32(t, lane);
-      r.unit0 = units + ui - u;
-      r.tile0 = tiles + ti - t;
-    }
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, pick(r, t));
-    if (hit && !have) {
-      const int at = __ffs(hit) - 1;
-      found.first = __shfl_sync(0xFFFFFFFFu, r.first, at);
-      found.end = __shfl_sync(0xFFFFFFFFu, r.end, at);
-      found.tokens = __shfl_sync(0xFFFFFFFFu, r.tokens, at);
-      found.tiles = __shfl_sync(0xFFFFFFFFu, r.tiles, at);
-      found.blocks = __shfl_sync(0xFFFFFFFFu, r.blocks, at);
-      if constexpr (PLACE) {
-        found.unit0 = __shfl_sync(0xFFFFFFFFu, r.unit0, at);
-        found.tile0 = __shfl_sync(0xFFFFFFFFu, r.tile0, at);
-      }
-      have = true;
-    }
-    if constexpr (PLACE) {
-      units += __shfl_sync(0xFFFFFFFFu, ui, 31);
-      tiles += __shfl_sync(0xFFFFFFFFu, ti, 31);
-    }
-    top = max(top, __shfl_sync(0xFFFFFFFFu, reach, 31));
   }
-  *total = tiles;
-  return found;
+  *top = max(*top, __shfl_sync(0xFFFFFFFFu, reach, 31));
+  return r;
 }
 
-// Tiles per CTA when `total` tiles are shared by `ctas` CTAs.
-__device__ __forceinline__ uint32_t prefix_chunk(uint32_t total, int ctas) {
-  return (total + uint32_t(ctas) - 1) / uint32_t(ctas);
+__device__ __forceinline__ PrefixGroup prefix_from(const PrefixGroup& r, int lane) {
+  PrefixGroup o;
+  o.first = __shfl_sync(0xFFFFFFFFu, r.first, lane);
+  o.end = __shfl_sync(0xFFFFFFFFu, r.end, lane);
+  o.tokens = __shfl_sync(0xFFFFFFFFu, r.tokens, lane);
+  o.tiles = __shfl_sync(0xFFFFFFFFu, r.tiles, lane);
+  o.blocks = __shfl_sync(0xFFFFFFFFu, r.blocks, lane);
+  o.index = __shfl_sync(0xFFFFFFFFu, r.index, lane);
+  return o;
+}
+
+// Whole warp: the group that holds sequence `seq` (nothing shared if none does).
+__device__ __forceinline__ PrefixGroup prefix_of_seq(const PrefixSide& s, int seq, int page_size, int group,
+                                                     int num_seqs, int lane, bool* bad) {
+  int top = 0;
+  for (int g0 = 0; g0 < s.num_groups; g0 += 32) {
+    const PrefixGroup r = prefix_load(s, g0, page_size, group, num_seqs, lane, &top, bad);
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, r.first <= seq && seq < r.end);
+    if (hit) return prefix_from(r, __ffs(hit) - 1);
+  }
+  return PrefixGroup{0, 0, 0, 0, 0, 0};
 }
 
 // Partial results: slot s holds numerators as [32 groups of 4 dims][128
