@@ -26,6 +26,7 @@ SAW_STEP_EARLY_PAGES = 1
 SAW_FMT_F16_INPUT = 1
 SAW_FMT_BF16_META = 2
 SAW_FMT_OUT_INPUT = 4
+SAW_PREFIX_AUTO, SAW_PREFIX_SHARE, SAW_PREFIX_SEPARATE = range(3)
 SAW_ROPE_NONE, SAW_ROPE_LINEAR, SAW_ROPE_NTK, SAW_ROPE_YARN, SAW_ROPE_BANDS = range(5)
 
 EXPORTS = ("saw_status_string", "saw_cache_bytes", "saw_quantize_append", "saw_decode_plan",
@@ -100,10 +101,10 @@ def lib() -> C.CDLL:
     L.saw_rope_append.argtypes = [P, i64, P, i64, P, i64, P, P, i32, i32, i32, P, i32, i32, i32,
                                   i32, P, i64, P, P, i32, i32, i32, i32, i32, i32, P, P]
     L.saw_prefix_decode_workspace_bytes.restype = sz
-    L.saw_prefix_decode_workspace_bytes.argtypes = [i32] * 8
+    L.saw_prefix_decode_workspace_bytes.argtypes = [i32] * 9
     L.saw_prefix_decode_int4.restype = i32
     L.saw_prefix_decode_int4.argtypes = [P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
-                                         i32, i32, i32, i32, i32, i32, f32, P, P, sz, i32, P, P]
+                                         i32, i32, i32, i32, i32, i32, f32, P, P, sz, i32, i32, P, P]
     # the *_ex calls: the same arguments plus `formats` before dev_status
     for name in ("saw_quantize_append", "saw_paged_decode_int4", "saw_decode_step",
                  "saw_prefill_attn_int4", "saw_paged_decode_int4_noalloc"):
@@ -462,10 +463,11 @@ def saw_rope_append(q, k: torch.Tensor, v, positions: torch.Tensor, cos_sin: tor
 
 def saw_prefix_decode_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int,
                                       num_kv_heads: int, head_dim: int, page_size: int,
-                                      max_prefix_len: int, max_own_len: int) -> int:
+                                      max_prefix_len: int, max_own_len: int,
+                                      mode: int = SAW_PREFIX_AUTO) -> int:
     return int(lib().saw_prefix_decode_workspace_bytes(num_seqs, num_groups, num_q_heads,
                                                        num_kv_heads, head_dim, page_size,
-                                                       max_prefix_len, max_own_len))
+                                                       max_prefix_len, max_own_len, mode))
 
 
 def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -474,7 +476,8 @@ def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                            max_prefix_len: int, max_own_len: int, num_kv_heads: int,
                            num_pages: int, page_size: int, rotate_k: bool, rotate_v: bool,
                            block_h: int, out: torch.Tensor, workspace=None, sm_scale: float = 0.0,
-                           dev_status=None, stream=None, meta_bf16: bool = False) -> None:
+                           dev_status=None, stream=None, meta_bf16: bool = False,
+                           mode: int = SAW_PREFIX_AUTO) -> None:
     """Decode of groups of sequences that share their first pages.  q:
     bfloat16 or float16 [B, Hq, 128] contiguous; out: the same shape, float32
     or q's type; cu_group_seqs: int32 [groups + 1], prefix_lens: int32
@@ -499,7 +502,7 @@ def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
         _i32(cu_group_seqs, "cu_group_seqs", groups + 1), _i32(prefix_lens, "prefix_lens"),
         groups, B, max_prefix_len, max_own_len, hq, num_kv_heads, d, num_pages, page_size,
         int(rotate_k), int(rotate_v), block_h, sm_scale, out.data_ptr(), _at(workspace), ws_bytes,
-        fmt, _i32(dev_status, "dev_status"), _raw_stream(q, stream))
+        mode, fmt, _i32(dev_status, "dev_status"), _raw_stream(q, stream))
     _raise(rc, "saw_prefix_decode_int4")
 
 

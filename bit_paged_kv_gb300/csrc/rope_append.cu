@@ -9,6 +9,8 @@
 // k goes on in binary32 into the append's butterfly and quantizer (the rule
 // of saw_quantize_append from "widen to binary32" on); q is rounded once, to
 // the input type.
+#include <type_traits>
+
 #include "saw_device.cuh"
 #include "saw_int4.h"
 #include "saw_quant_row.cuh"
@@ -259,6 +261,331 @@ cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, rope_append_row_kernel<D>, p);
 }
 
+// ------------------------------------------------------------ bulk
+//
+// Large batches.  Item = (token, part): up to kQPart q-heads, or the token's K
+// rows, or its V rows; every warp walks items on its own, so that the q parts
+// (pure traffic) and the K and V parts (150 or so instructions a row, which
+// alone would be bound by issue) of different warps share an SM.  Lane a of
+// the D / 16 that share a row holds its 16-byte chunks a and a + D / 16, dims 8
+// a .. + 7 and the same + D / 2: the (i, i + D/2) pairs of a whole-head rotary
+// sit in one lane, the butterfly's strides 1, 2, 4 and D / 2 too, and only 8 ..
+// D / 4 cross lanes.  The lane's cosines and sines serve all heads of the
+// token.
+//
+// Bound: HBM.  131072 tokens, Hq 32, Hkv 8, D 128: 2.90 GB, 426 us at the
+// measured copy rate.
+constexpr int kBulkWarps = 8, kBulkCtasPerSm = 2;
+constexpr int64_t kBulkMinElems = int64_t(1) << 21;  // smaller batches: a warp per row
+constexpr int kQPart = 16;  // q-heads per item
+
+enum { kHalfWhole = 0, kHalfPart = 1, kInter = 2 };
+
+template <bool F16IN>
+__device__ __forceinline__ void widen8(const uint4& w, float* x) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = in_lo(ws[j], F16IN);
+    x[2 * j + 1] = in_hi(ws[j], F16IN);
+  }
+}
+template <bool F16IN>
+__device__ __forceinline__ uint4 narrow8(const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = F16IN ? pack_half2(x[2 * j], x[2 * j + 1]) : pack_bf162(x[2 * j], x[2 * j + 1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A lane's cosines and sines: of its pairs (kHalfWhole, 8), of its chunks' 2 x
+// 4 pairs (kInter), or of its chunks' 2 x 8 elements (kHalfPart).
+template <int LAYOUT>
+struct Angles {
+  static constexpr int kN = LAYOUT == kHalfPart ? 16 : 8;
+  float c[kN], s[kN];
+};
+
+template <int D, int LAYOUT>
+__device__ __forceinline__ void load_angles(Angles<LAYOUT>& t, const float* cs, int r, int a) {
+  const int half = r >> 1;
+  auto run = [&](int at, int i, auto count) {  // c, s [at ..] from pairs i ..
+    constexpr int n = decltype(count)::value;
+#pragma unroll
+    for (int k = 0; k < n; k += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(cs + i + k));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + i + k));
+      t.c[at + k] = x.x; t.c[at + k + 1] = x.y; t.c[at + k + 2] = x.z; t.c[at + k + 3] = x.w;
+      t.s[at + k] = y.x; t.s[at + k + 1] = y.y; t.s[at + k + 2] = y.z; t.s[at + k + 3] = y.w;
+    }
+  };
+  using N4 = std::integral_constant<int, 4>;
+  using N8 = std::integral_constant<int, 8>;
+  if constexpr (LAYOUT == kHalfWhole) {
+    run(0, 8 * a, N8{});
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int ch = a + u * (D / 16);
+      if (8 * ch < r) {
+        if constexpr (LAYOUT == kInter) run(4 * u, 4 * ch, N4{});
+        else run(8 * u, 8 * (8 * ch < half ? ch : ch - half / 8), N8{});
+      }
+    }
+  }
+}
+
+// Turns a lane's 16 values.  Each product and each sum is rounded once
+// (scalar sums: packed products and packed sums were fused by the assembler).
+template <int D, int LAYOUT>
+__device__ __forceinline__ void turn16(float (&x)[16], const Angles<LAYOUT>& t, int r, int a, int lane) {
+  if constexpr (LAYOUT == kHalfWhole) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = x[e], v = x[8 + e];
+      x[e] = __fsub_rn(__fmul_rn(u, t.c[e]), __fmul_rn(v, t.s[e]));
+      x[8 + e] = __fadd_rn(__fmul_rn(v, t.c[e]), __fmul_rn(u, t.s[e]));
+    }
+  } else if constexpr (LAYOUT == kInter) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (8 * (a + u * (D / 16)) < r) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = x[8 * u + 2 * e], q = x[8 * u + 2 * e + 1];
+          x[8 * u + 2 * e] = __fsub_rn(__fmul_rn(p, t.c[4 * u + e]), __fmul_rn(q, t.s[4 * u + e]));
+          x[8 * u + 2 * e + 1] = __fadd_rn(__fmul_rn(q, t.c[4 * u + e]), __fmul_rn(p, t.s[4 * u + e]));
+        }
+      }
+  } else {
+    // the partner of chunk ch is `half` elements away: chunk pc, in lane pc %
+    // (D / 16) of this row as its first or second chunk
+    constexpr int LPR = D / 16;
+    const int hc = r >> 4;  // chunks of half the turned part
+    float o[16];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int ch = a + u * LPR;
+      const int pc = ch < hc ? ch + hc : (ch < 2 * hc ? ch - hc : ch);
+      const int from = (lane & ~(LPR - 1)) | (pc & (LPR - 1));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f0 = __shfl_sync(kAll, x[e], from), f1 = __shfl_sync(kAll, x[8 + e], from);
+        o[8 * u + e] = pc >= LPR ? f1 : f0;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int ch = a + u * LPR;
+      if (ch < 2 * hc) {
+        const bool low = ch < hc;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float m = __fmul_rn(x[8 * u + e], t.c[8 * u + e]), n = __fmul_rn(o[8 * u + e], t.s[8 * u + e]);
+          x[8 * u + e] = low ? __fsub_rn(m, n) : __fadd_rn(m, n);
+        }
+      }
+    }
+  }
+}
+
+// The row's butterfly (blocks of h, ascending strides), then the factor.
+// Sums with a partner lane as RN(+-x + o), the +-1 product exact.
+template <int D>
+__device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int lane) {
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) {  // (h >= 16)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(i & s)) {
+        const float a = x[i], b = x[i + s];
+        x[i] = __fadd_rn(a, b);
+        x[i + s] = __fsub_rn(a, b);
+      }
+  }
+#pragma unroll
+  for (int s = 8; s < D / 2; s <<= 1) {
+    if (s < h) {
+      const float sign = (lane & (s >> 3)) ? -1.0f : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(x[i], sign, __shfl_xor_sync(kAll, x[i], s >> 3));
+    }
+  }
+  if (h == D) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[i], b = x[i + 8];
+      x[i] = __fadd_rn(a, b);
+      x[i + 8] = __fsub_rn(a, b);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], c_h);
+}
+
+// Eight codes as a word.  fast (no clamp can bite): (y - z) r 2^-24 converts
+// to a binary16 whose bits are the round-half-even code.
+__device__ __forceinline__ uint32_t codes8(const float* x, const RowMeta& m) {
+  if (m.fast) {
+    const float r24 = __fmul_rn(m.rcp, 5.9604644775390625e-08f);
+    uint32_t d[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int a = (k & 1) + 4 * (k >> 1);
+      d[k] = pack_half2(__fmul_rn(__fsub_rn(x[a], m.z), r24), __fmul_rn(__fsub_rn(x[a + 2], m.z), r24));
+    }
+    // bytes 0 and 2: (c0 c1), (c2 c3); (c4 c5), (c6 c7); a -0 leaves its sign
+    // in a byte that is dropped or masked
+    const uint32_t lo = d[0] | ((d[1] << 4) & 0x00F000F0u), hi = d[2] | ((d[3] << 4) & 0x00F000F0u);
+    return prmt(lo, hi, 0x6420u);
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    int q = __float2int_rn(__fmul_rn(__fsub_rn(x[k], m.z), m.rcp));
+    q = min(max(q, 0), 15);
+    w |= uint32_t(q) << (4 * k);
+  }
+  return w;
+}
+
+template <int D, bool F16IN, int LAYOUT>
+__global__ void __launch_bounds__(32 * kBulkWarps, kBulkCtasPerSm) rope_append_bulk_kernel(const RopeParams p) {
+  pdl_wait_then_release();
+  constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp
+  const int lane = threadIdx.x & 31;
+  const int a = lane & (LPR - 1), sub = lane / LPR;
+  const int nq = (p.num_q_heads + kQPart - 1) / kQPart;
+  const uint32_t parts = uint32_t(nq + p.num_tensors);
+  const uint32_t items = uint32_t(p.num_tokens) * parts;
+  const uint32_t warps = gridDim.x * kBulkWarps;
+  const int hkv = p.num_kv_heads;
+  for (uint32_t it = blockIdx.x * kBulkWarps + (threadIdx.x >> 5); it < items; it += warps) {
+    const int t = int(it / parts), part = int(it - uint32_t(t) * parts);
+    const int pos = p.positions[t];
+    const bool pos_ok = pos >= 0 && pos < p.max_pos;
+    if (part < nq) {
+      // ---- q-heads, four rounds of loads in flight
+      if (!pos_ok) continue;  // (reported with the K rows)
+      Angles<LAYOUT> ang;
+      load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
+      const int h0 = part * kQPart, h1 = min(p.num_q_heads, h0 + kQPart);
+      const uint16_t* src = p.q + int64_t(t) * p.q_stride + 8 * a;
+      uint16_t* dst = p.q_out + int64_t(t) * p.q_out_stride + 8 * a;
+      constexpr int kRounds = 4;
+      for (int hb = h0; hb < h1; hb += RPW * kRounds) {
+        uint4 w[kRounds][2];
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+          const int h = hb + k * RPW + sub;
+          w[k][0] = w[k][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < h1) {
+            w[k][0] = *reinterpret_cast<const uint4*>(src + h * D);
+            w[k][1] = *reinterpret_cast<const uint4*>(src + h * D + D / 2);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+          if (hb + k * RPW >= h1) break;
+          const int h = hb + k * RPW + sub;
+          float x[16];
+          widen8<F16IN>(w[k][0], x);
+          widen8<F16IN>(w[k][1], x + 8);
+          turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
+          if (h < h1) {
+            *reinterpret_cast<uint4*>(dst + h * D) = narrow8<F16IN>(x);
+            *reinterpret_cast<uint4*>(dst + h * D + D / 2) = narrow8<F16IN>(x + 8);
+          }
+        }
+      }
+      continue;
+    }
+    // ---- K or V rows
+    const int tensor = part - nq;
+    const int32_t slot = p.slot_mapping[t];
+    if (!pos_ok && tensor == 0 && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+    if (slot == -1 || !pos_ok) continue;
+    if (slot < 0 || int64_t(slot) >= p.num_slots) {
+      if (lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+      continue;
+    }
+    const uint16_t* src = (tensor ? p.v + int64_t(t) * p.v_stride : p.k + int64_t(t) * p.k_stride) + 8 * a;
+    const int P = p.page_size;
+    const int page = slot >> p.page_shift, off = slot & (P - 1);
+    uint8_t* chunk0 = (tensor ? p.v_cache : p.k_cache) + int64_t(page) * hkv * int64_t(P * (D / 2 + 4));
+    const bool rot = (tensor ? p.rotate_v : p.rotate_k) != 0;
+    Angles<LAYOUT> ang;
+    if (tensor == 0) load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
+    uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
+    if (sub < hkv) {
+      w0 = *reinterpret_cast<const uint4*>(src + sub * D);
+      w1 = *reinterpret_cast<const uint4*>(src + sub * D + D / 2);
+    }
+    for (int hb = 0; hb < hkv; hb += RPW) {
+      const int h = hb + sub;
+      float x[16];
+      widen8<F16IN>(w0, x);
+      widen8<F16IN>(w1, x + 8);
+      if (h + RPW < hkv) {  // the next rows, under way while these are worked on
+        w0 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D);
+        w1 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D + D / 2);
+      }
+      if (tensor == 0) turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
+      if (rot) rotate16<D>(x, p.block_h, p.c_h, lane);
+      float mn = fminf(x[0], x[1]), mx = fmaxf(x[0], x[1]);
+#pragma unroll
+      for (int i = 2; i < 16; ++i) {
+        mn = fminf(mn, x[i]);
+        mx = fmaxf(mx, x[i]);
+      }
+#pragma unroll
+      for (int d = 1; d < LPR; d <<= 1) {
+        mn = fminf(mn, __shfl_xor_sync(kAll, mn, d));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
+      }
+      const RowMeta m = row_meta(mn, mx, p.meta_bf16 != 0);
+      const uint32_t c0 = codes8(x, m), c1 = codes8(x + 8, m);
+      if (h < hkv) {
+        uint8_t* chunk = chunk0 + int64_t(h) * (P * (D / 2 + 4));
+        uint32_t* codes = reinterpret_cast<uint32_t*>(chunk + off * (D / 2));
+        codes[a] = c0;
+        codes[a + LPR] = c1;
+        if (a == 0)
+          *reinterpret_cast<uint32_t*>(chunk + P * (D / 2) + 4 * off) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
+      }
+    }
+  }
+}
+
+template <int D, bool F16IN, int LAYOUT>
+cudaError_t launch_bulk_l(const RopeParams& p, int sms, cudaStream_t stream) {
+  const int64_t items = int64_t(p.num_tokens) * ((p.num_q_heads + kQPart - 1) / kQPart + p.num_tensors);
+  const int64_t want = (items + kBulkWarps - 1) / kBulkWarps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(want < int64_t(kBulkCtasPerSm) * sms ? want : int64_t(kBulkCtasPerSm) * sms));
+  cfg.blockDim = dim3(32 * kBulkWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_append_bulk_kernel<D, F16IN, LAYOUT>, p);
+}
+
+template <int D>
+cudaError_t launch_bulk(const RopeParams& p, int sms, cudaStream_t stream) {
+  const int layout = p.interleaved ? kInter : p.rope_dim == D ? kHalfWhole : kHalfPart;
+  if (p.in_f16)
+    return layout == kInter        ? launch_bulk_l<D, true, kInter>(p, sms, stream)
+           : layout == kHalfWhole  ? launch_bulk_l<D, true, kHalfWhole>(p, sms, stream)
+                                   : launch_bulk_l<D, true, kHalfPart>(p, sms, stream);
+  return layout == kInter       ? launch_bulk_l<D, false, kInter>(p, sms, stream)
+         : layout == kHalfWhole ? launch_bulk_l<D, false, kHalfWhole>(p, sms, stream)
+                                : launch_bulk_l<D, false, kHalfPart>(p, sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t stream) {
@@ -277,11 +604,11 @@ cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t st
 }
 
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream) {
-  (void)sms;
+  const bool bulk = int64_t(p.num_tokens) * (p.num_q_heads + 2 * p.num_kv_heads) * p.head_dim >= kBulkMinElems;
   switch (p.head_dim) {
-    case 64: return launch_rows<64>(p, stream);
-    case 128: return launch_rows<128>(p, stream);
-    case 256: return launch_rows<256>(p, stream);
+    case 64: return bulk ? launch_bulk<64>(p, sms, stream) : launch_rows<64>(p, stream);
+    case 128: return bulk ? launch_bulk<128>(p, sms, stream) : launch_rows<128>(p, stream);
+    case 256: return bulk ? launch_bulk<256>(p, sms, stream) : launch_rows<256>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -557,7 +557,8 @@ struct PrefixPlan {
 
 int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
                     int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
-                    int32_t max_prefix_len, int32_t max_own_len, PrefixPlan* out) {
+                    int32_t max_prefix_len, int32_t max_own_len, int32_t mode, PrefixPlan* out) {
+  if (mode < SAW_PREFIX_AUTO || mode > SAW_PREFIX_SEPARATE) return SAW_ERR_INVALID_ARG;
   if (num_seqs < 0 || num_groups < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
       max_prefix_len < 0 || max_own_len < 0 || int64_t(max_prefix_len) + max_own_len > INT32_MAX)
     return SAW_ERR_INVALID_ARG;
@@ -572,8 +573,17 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
   const int64_t units = (num_groups + num_seqs / per) * num_kv_heads;  // at most
   const int64_t tiles = ceil_div(max_prefix_len, saw::kPrefixKeys);
   if (units * tiles > INT32_MAX) return SAW_ERR_UNSUPPORTED;
-  const bool shared = num_groups > 0 && num_seqs > 1 && max_prefix_len >= page_size;
-  if (shared) {
+  // The prefix pass costs its launch, a part's start and end and the merge
+  // (10 us more than the decode alone) and 1.6 us per key tile of the fullest
+  // SM; without it the decode reads every sequence's copy, 32768 (token,
+  // kv-head) rows of K and V per us.  Both sides on GB300, Hq 32, Hkv 8, short
+  // own parts: 64 x 1024 tokens 23.0 against 22.0 us, 32 x 1024 20.6 / 11.6,
+  // 8 x 4096 20.6 / 13.6, 32 x 4096 24.1 / 27.7, 16 x 8192 24.2 / 39.7, 4 x
+  // 32768 35.6 / 35.6, 128 x 1024 in 40 groups 48.3 / 27.3.
+  const double apart = double(num_seqs) * max_prefix_len * num_kv_heads / 32768.0;
+  const double together = 10.0 + 1.6 * double(ceil_div(units * tiles, sms));
+  const bool can_share = num_groups > 0 && num_seqs > 0 && max_prefix_len >= page_size;
+  if (can_share && (mode == SAW_PREFIX_SHARE || (mode == SAW_PREFIX_AUTO && apart > together))) {
     p.ctas = int32_t(sms);
     p.plan_len = max_own_len;
     const int64_t parts = std::max(units, 2 * sms);
@@ -598,10 +608,11 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
 size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
                                          int32_t num_q_heads, int32_t num_kv_heads,
                                          int32_t head_dim, int32_t page_size,
-                                         int32_t max_prefix_len, int32_t max_own_len) {
+                                         int32_t max_prefix_len, int32_t max_own_len,
+                                         int32_t mode) {
   PrefixPlan plan;
   if (plan_prefix(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, page_size,
-                  max_prefix_len, max_own_len, &plan) != SAW_OK)
+                  max_prefix_len, max_own_len, mode, &plan) != SAW_OK)
     return 0;
   return plan.total();
 }
@@ -614,13 +625,13 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
                                int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
                                int32_t page_size, int32_t rotate_k, int32_t rotate_v,
                                int32_t block_h, float sm_scale, void* out, void* workspace,
-                               size_t workspace_bytes, int32_t formats, int32_t* dev_status,
-                               void* stream) {
+                               size_t workspace_bytes, int32_t mode, int32_t formats,
+                               int32_t* dev_status, void* stream) {
   const bool out16 = (formats & SAW_FMT_OUT_INPUT) != 0;
   formats &= ~int32_t(SAW_FMT_OUT_INPUT);
   PrefixPlan plan;
   int32_t rc = plan_prefix(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, page_size,
-                           max_prefix_len, max_own_len, &plan);
+                           max_prefix_len, max_own_len, mode, &plan);
   if (rc != SAW_OK) return rc;
   if (num_seqs > 0 && num_groups > 0 && (!cu_group_seqs || !prefix_lens))
     return SAW_ERR_INVALID_ARG;

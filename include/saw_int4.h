@@ -513,8 +513,8 @@ int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
                         void* stream);
 
 /*
- * Workspace bytes of saw_prefix_decode_int4 for these sizes on the current
- * device; 0 when it needs none or the sizes are bad.  Zero-fill a workspace
+ * Workspace bytes of saw_prefix_decode_int4 for these sizes and `mode` on the
+ * current device; 0 when it needs none or the sizes are bad.  Zero-fill a workspace
  * before its first use; each call leaves it ready for the next, of whatever
  * sizes (up to 131072 (sequence, kv-head) pairs; a larger batch wants one of
  * its own).
@@ -522,7 +522,8 @@ int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
 size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
                                          int32_t num_q_heads, int32_t num_kv_heads,
                                          int32_t head_dim, int32_t page_size,
-                                         int32_t max_prefix_len, int32_t max_own_len);
+                                         int32_t max_prefix_len, int32_t max_own_len,
+                                         int32_t mode);
 
 /*
  * saw_prefix_decode_int4 -- saw_paged_decode_int4 for a batch in which groups
@@ -551,13 +552,24 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  * workspace     saw_prefix_decode_workspace_bytes(...) bytes, 16-byte
  *               aligned, zero-filled before its first use.  Calls sharing one
  *               must be ordered (one stream).
+ * mode          SAW_PREFIX_AUTO: by size, whichever is faster (short prefixes
+ *               and few sequences are not worth a pass of their own);
+ *               SAW_PREFIX_SHARE, SAW_PREFIX_SEPARATE: always, never (tests).
  * formats       SAW_FMT_F16_INPUT, SAW_FMT_BF16_META, SAW_FMT_OUT_INPUT.
+ *
+ * Arithmetic of the prefix pass: scores to about 2^-22 of their terms (codes
+ * exact, q' in two binary16 parts; a |q'| whose product with the softmax scale
+ * and log2 e exceeds 4094 saturates), dequantized V and p rounded once to
+ * binary16 (V beyond +-65504 saturates), sums and softmax in binary32.
  *
  * A group with inconsistent entries is reported as SAW_ERR_DEVICE_INDEX and
  * shares nothing.  Other arguments and errors as saw_paged_decode_int4;
  * head_dim 128 and at most 8 q-heads per kv-head (else SAW_ERR_UNSUPPORTED).
  */
 #define SAW_FMT_OUT_INPUT 4
+#define SAW_PREFIX_AUTO 0
+#define SAW_PREFIX_SHARE 1
+#define SAW_PREFIX_SEPARATE 2
 int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v_cache,
                                const int32_t* block_tables, int32_t max_blocks_per_seq,
                                const int32_t* seq_lens, const int32_t* cu_group_seqs,
@@ -566,8 +578,8 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
                                int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
                                int32_t page_size, int32_t rotate_k, int32_t rotate_v,
                                int32_t block_h, float sm_scale, void* out, void* workspace,
-                               size_t workspace_bytes, int32_t formats, int32_t* dev_status,
-                               void* stream);
+                               size_t workspace_bytes, int32_t mode, int32_t formats,
+                               int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------
  * BF16 baseline.  gist.science "SAW-INT4: System-Aware 4-Bit KV-Cache

@@ -52,14 +52,17 @@ def setup(seed, sizes, pre, own, hq=8, hkv=2, P=16, rk=True, rv=True, h=128, dt=
                 max_pre=int(max(pre)), max_own=int(max(list(own) + [0])))
 
 
-def run(s, out_dtype=torch.float32, sm_scale=0.0, ws=None, stream=None, **kw):
+SHARE, SEPARATE, AUTO = saw.SAW_PREFIX_SHARE, saw.SAW_PREFIX_SEPARATE, saw.SAW_PREFIX_AUTO
+
+
+def run(s, out_dtype=torch.float32, sm_scale=0.0, ws=None, stream=None, mode=SHARE, **kw):
     s = dict(s, **kw)
     wl, q = s["wl"], s["q"]
     i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
     B, G = q.shape[0], len(s["pre"])
     out = torch.full(q.shape, float("nan"), dtype=out_dtype, device="cuda")
     need = saw.saw_prefix_decode_workspace_bytes(B, G, wl.num_q_heads, wl.num_kv_heads, 128, wl.page_size,
-                                                 s["max_pre"], s["max_own"])
+                                                 s["max_pre"], s["max_own"], mode)
     if ws is None:
         ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
     assert ws.numel() >= need
@@ -68,7 +71,7 @@ def run(s, out_dtype=torch.float32, sm_scale=0.0, ws=None, stream=None, **kw):
     torch.cuda.synchronize()
     saw.saw_prefix_decode_int4(q, s["kc"], s["vc"], *args, s["max_pre"], s["max_own"], wl.num_kv_heads, s["pages"],
                                wl.page_size, wl.rotate_k, wl.rotate_v, wl.block_h, out, ws, sm_scale=sm_scale,
-                               dev_status=st, meta_bf16=s["meta"], stream=stream)
+                               dev_status=st, meta_bf16=s["meta"], stream=stream, mode=mode)
     torch.cuda.synchronize()
     return out, int(st.item())
 
@@ -83,14 +86,15 @@ def reference(s, sm_scale=None, bt=None, lens=None):
 
 
 def check(s, label, out_dtype=torch.float32, sm_scale=0.0):
-    out, st = run(s, out_dtype, sm_scale)
-    assert st == 0
     ref = reference(s, sm_scale or None)
-    got = out.float().cpu().numpy().reshape(-1, 128)
-    assert np.isfinite(got).all()
     tol = ATTN_TOL + (0 if out_dtype is torch.float32 else torch.finfo(out_dtype).eps / 2)
-    err = rel_err(got, ref, f"prefix-{label}")
-    assert err <= tol, f"relative error {err:.3e}"
+    for mode in (SEPARATE, AUTO, SHARE):
+        out, st = run(s, out_dtype, sm_scale, mode=mode)
+        assert st == 0
+        got = out.float().cpu().numpy().reshape(-1, 128)
+        assert np.isfinite(got).all()
+        err = rel_err(got, ref, f"prefix-{label}")
+        assert err <= tol, f"mode {mode}: relative error {err:.3e}"
     return out
 
 
@@ -200,12 +204,13 @@ def test_bad_lengths_and_groups_are_reported():
             t["pre"][1], t["max_own"] = 257, 300
         else:
             t["pre"][0], t["max_own"] = -1, 300
-        out, st = run(t)
-        assert st == saw.SAW_ERR_DEVICE_INDEX, what
-        got = out.cpu().numpy()
-        ok = [b for b in range(40) if b not in bad]
-        assert rel_err(got[ok], want[ok], f"prefix-bad-{what}") <= ATTN_TOL
-        assert all((got[b] == 0).all() for b in bad)
+        for mode in (SHARE, SEPARATE):
+            out, st = run(t, mode=mode)
+            assert st == saw.SAW_ERR_DEVICE_INDEX, what
+            got = out.cpu().numpy()
+            ok = [b for b in range(40) if b not in bad]
+            assert rel_err(got[ok], want[ok], f"prefix-bad-{what}") <= ATTN_TOL
+            assert all((got[b] == 0).all() for b in bad)
 
 
 def test_bad_pages_are_skipped():
@@ -252,7 +257,7 @@ def test_keys_outside_the_sequences_do_not_matter():
 def test_repeated_calls_share_a_workspace():
     """A workspace serves call after call, of this shape and of smaller ones, and the answer does not change."""
     s = setup(15, [64], [2048], np.arange(1, 65) * 20, hq=32, hkv=8)
-    need = saw.saw_prefix_decode_workspace_bytes(64, 1, 32, 8, 128, 16, s["max_pre"], s["max_own"])
+    need = saw.saw_prefix_decode_workspace_bytes(64, 1, 32, 8, 128, 16, s["max_pre"], s["max_own"], SHARE)
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     first, _ = run(s, ws=ws)
     small = setup(16, [8], [512], np.arange(1, 9), hq=32, hkv=8)
@@ -263,7 +268,7 @@ def test_repeated_calls_share_a_workspace():
         other, st = run(small, ws=ws)
         assert st == 0 and torch.equal(other, alone)
     many = setup(19, [100] * 3, [160] * 3, np.arange(1, 301) * 8, hq=32, hkv=8)
-    need = max(need, saw.saw_prefix_decode_workspace_bytes(300, 3, 32, 8, 128, 16, 160, many["max_own"]))
+    need = max(need, saw.saw_prefix_decode_workspace_bytes(300, 3, 32, 8, 128, 16, 160, many["max_own"], SHARE))
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     alone, _ = run(many)
     for _ in range(2):
@@ -280,7 +285,7 @@ def test_graph_replay_with_new_inputs_and_other_stream():
     wl = s["wl"]
     i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()
     args = [i32(s[k]) for k in ("bt", "lens", "cu", "pre")]
-    need = saw.saw_prefix_decode_workspace_bytes(48, 1, 32, 8, 128, 16, s["max_pre"], s["max_own"])
+    need = saw.saw_prefix_decode_workspace_bytes(48, 1, 32, 8, 128, 16, s["max_pre"], s["max_own"], SHARE)
     ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
     out = torch.empty(s["q"].shape, device="cuda")
     q = s["q"].clone()
@@ -288,7 +293,7 @@ def test_graph_replay_with_new_inputs_and_other_stream():
     with torch.cuda.graph(graph):
         for _ in range(2):
             saw.saw_prefix_decode_int4(q, s["kc"], s["vc"], *args, s["max_pre"], s["max_own"], 8, s["pages"], 16, True,
-                                       True, 128, out, ws)
+                                       True, 128, out, ws, mode=SHARE)
     q.copy_(s["q"].flip(0))
     lens = s["lens"].copy()
     lens[::3] = 1024 + 1

@@ -91,12 +91,12 @@ def test_rope_append_refused(L, kw, expect):
 
 def _prefix(L, **kw):
     a = dict(q=A, kc=A, vc=B, bt=A, mb=8, sl=B, cu=A, pre=B, groups=1, B=2, maxp=64, maxo=64, hq=32, hkv=8,
-             d=128, pages=8, P=16, rk=1, rv=1, h=128, scale=0.0, out=A, ws=B, wsb=1 << 40, fmt=4)
+             d=128, pages=8, P=16, rk=1, rv=1, h=128, scale=0.0, out=A, ws=B, wsb=1 << 40, mode=0, fmt=4)
     a.update(kw)
     return L.saw_prefix_decode_int4(a["q"], a["kc"], a["vc"], a["bt"], a["mb"], a["sl"], a["cu"], a["pre"],
                                     a["groups"], a["B"], a["maxp"], a["maxo"], a["hq"], a["hkv"], a["d"],
                                     a["pages"], a["P"], a["rk"], a["rv"], a["h"], a["scale"], a["out"],
-                                    a["ws"], a["wsb"], a["fmt"], None, None)
+                                    a["ws"], a["wsb"], a["mode"], a["fmt"], None, None)
 
 
 @pytest.mark.parametrize("kw,expect", [
@@ -106,7 +106,7 @@ def _prefix(L, **kw):
     (dict(mb=-1), INV), (dict(cu=None), INV), (dict(pre=None), INV), (dict(q=None), INV), (dict(kc=None), INV),
     (dict(bt=None), INV), (dict(sl=None), INV), (dict(out=None), INV), (dict(out=MIS), INV), (dict(q=MIS), INV),
     (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV), (dict(fmt=8), INV), (dict(h=48), INV),
-    (dict(rk=2), INV), (dict(hkv=0), INV),
+    (dict(rk=2), INV), (dict(hkv=0), INV), (dict(mode=3), INV), (dict(mode=-1), INV),
     (dict(B=0), saw.SAW_OK),
 ])
 def test_prefix_refused(L, kw, expect):
@@ -121,6 +121,12 @@ def test_prefix_workspace_refused(L):
     assert _prefix(L, **big, ws=None) == INV
     assert _prefix(L, **big, ws=MIS) == INV
     assert _prefix(L, **big, wsb=need - 1) == INV
+    # small sizes read every table apart: no more than the decode's own workspace
+    small = (4, 1, 32, 8, 128, 16, 64, 64)
+    assert saw.saw_prefix_decode_workspace_bytes(*small) == 0
+    assert saw.saw_prefix_decode_workspace_bytes(*small, saw.SAW_PREFIX_SHARE) > 0
+    assert saw.saw_prefix_decode_workspace_bytes(*small, 7) == 0
+    assert _prefix(L, mode=saw.SAW_PREFIX_SHARE, wsb=1 << 20) == INV
     assert saw.saw_prefix_decode_workspace_bytes(64, 1, 32, 8, 64, 16, 16384, 2048) == 0
     assert saw.saw_prefix_decode_workspace_bytes(-1, 1, 32, 8, 128, 16, 16384, 2048) == 0
 
