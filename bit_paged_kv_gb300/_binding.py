@@ -351,31 +351,41 @@ def saw_prefill_attn_int4(q: torch.Tensor, cu_q_lens: torch.Tensor, k_cache: tor
 # share of a call is what a user waits for: pointers are passed as plain
 # integers and every check is one comparison.
 
-def _dev(t: torch.Tensor) -> None:
+_INT32 = torch.int32
+# The current stream as an integer, without building a Stream object (2 us of
+# a 10 us call).
+_raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _dev(t: torch.Tensor) -> int:
     """The library launches on the current device: it has to be the tensors'."""
-    if t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _i32(t, what: str, n: int | None = None):
+def _on(stream, dev: int) -> int:
+    if stream is None:
+        if _raw_current is not None:
+            return _raw_current(dev)
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _i32(t, what: str, n: int = -1):
     if t is None:
         return None
-    if t.dtype is not torch.int32 or not t.is_contiguous():
+    if t.dtype is not _INT32 or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32")
-    if n is not None and t.numel() != n:
+    if n >= 0 and t.numel() != n:
         raise ValueError(f"{what} must have {n} entries, not {t.numel()}")
     return t.data_ptr()
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(t: torch.Tensor, stream):
-    if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def saw_build_tables(cached_lens, new_lens: torch.Tensor, free_pages: torch.Tensor, num_free,
@@ -388,21 +398,22 @@ def saw_build_tables(cached_lens, new_lens: torch.Tensor, free_pages: torch.Tens
     [B] and a list of free pages; num_free: int32 [1] or None (all of the
     list).  src_tables [R, blocks] with src_rows [B]: the requests' tables so
     far (None: nothing cached; block_tables itself: extended in place)."""
-    _dev(new_lens)
-    B = new_lens.numel()
+    dev = _dev(new_lens)
+    B, tokens = new_lens.numel(), slot_mapping.numel()
     rows, blocks = src_tables.shape if src_tables is not None else (0, 0)
-    if block_tables.shape[0] != B:
-        raise ValueError(f"block_tables must have {B} rows, not {block_tables.shape[0]}")
-    rc = lib().saw_build_tables(
+    b, width = block_tables.shape
+    if b != B:
+        raise ValueError(f"block_tables must have {B} rows, not {b}")
+    rc = (_lib or lib()).saw_build_tables(
         _i32(src_tables, "src_tables"), rows, blocks, _i32(src_rows, "src_rows", B),
         _i32(cached_lens, "cached_lens", B), _i32(new_lens, "new_lens"),
         _i32(free_pages, "free_pages"), free_pages.numel(), _i32(num_free, "num_free", 1), B,
-        slot_mapping.numel(), num_pages, page_size, _i32(block_tables, "block_tables"),
-        block_tables.shape[1], _i32(seq_lens, "seq_lens", B),
+        tokens, num_pages, page_size, _i32(block_tables, "block_tables"), width, _i32(seq_lens, "seq_lens", B),
         _i32(cu_q_lens, "cu_q_lens", B + 1), _i32(slot_mapping, "slot_mapping"),
-        _i32(positions, "positions", slot_mapping.numel()), _i32(pages_taken, "pages_taken", 1),
-        _i32(dev_status, "dev_status"), _raw_stream(new_lens, stream))
-    _raise(rc, "saw_build_tables")
+        _i32(positions, "positions", tokens), _i32(pages_taken, "pages_taken", 1),
+        _i32(dev_status, "dev_status"), _on(stream, dev))
+    if rc:
+        _raise(rc, "saw_build_tables")
 
 
 def saw_rope_table(cos_sin: torch.Tensor, base: float = 10000.0, scaling: int = SAW_ROPE_NONE,
@@ -410,23 +421,24 @@ def saw_rope_table(cos_sin: torch.Tensor, base: float = 10000.0, scaling: int = 
                    high: float = 0.0, att_scale: float = 0.0, stream=None) -> None:
     """Fill cos_sin (float32 [max_pos, rope_dim]): cosines of the rope_dim/2
     pairs, then sines.  scaling: one of SAW_ROPE_*; see include/saw_int4.h."""
-    _dev(cos_sin)
+    dev = _dev(cos_sin)
     if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be contiguous float32 [max_pos, rope_dim]")
-    rc = lib().saw_rope_table(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], base,
-                              scaling, factor, orig_max_pos, low, high, att_scale,
-                              _raw_stream(cos_sin, stream))
-    _raise(rc, "saw_rope_table")
+    n, r = cos_sin.shape
+    rc = (_lib or lib()).saw_rope_table(cos_sin.data_ptr(), n, r, base, scaling, factor,
+                                        orig_max_pos, low, high, att_scale, _on(stream, dev))
+    if rc:
+        _raise(rc, "saw_rope_table")
 
 
-def _rows(t: torch.Tensor, like: torch.Tensor, what: str) -> int:
-    """Checks rows [T, heads, D] with only the token dimension strided."""
-    s = t.stride()
-    if t.dtype is not like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2] \
-            or s[2] != 1 or (s[1] != t.shape[2] and t.shape[1] != 1):
-        raise ValueError(f"{what} must be [T, heads, D] rows like k's type, each token's contiguous")
+def _rows(t: torch.Tensor, dtype, T: int, D: int, what: str):
+    """(heads, token stride) of rows [T, heads, D] with only the token dimension strided."""
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if t.dtype is not dtype or n != T or d != D or s2 != 1 or (s1 != D and h != 1):
+        raise ValueError(f"{what} must be [{T}, heads, {D}] rows of k's type, each token's contiguous")
     # (a single token's stride is whatever the view says; it is never used)
-    return s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return h, (s0 if T > 1 else h * D)
 
 
 def saw_rope_append(q, k: torch.Tensor, v, positions: torch.Tensor, cos_sin: torch.Tensor,
@@ -438,27 +450,34 @@ def saw_rope_append(q, k: torch.Tensor, v, positions: torch.Tensor, cos_sin: tor
     [T, Hq, D], k, v: [T, Hkv, D], bfloat16 or float16, token dim strided;
     q (with q_out) and v may be None; q_out may be q.  positions,
     slot_mapping: int32 [T]; cos_sin: float32 [max_pos, rope_dim]."""
-    _dev(k)
-    T, hkv, d = k.shape
-    fmt = _formats(k, meta_bf16)
-    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
+    dev = _dev(k)
+    T, _, d = k.shape
+    dtype = k.dtype
+    hkv, ks = _rows(k, dtype, T, d, "k")
+    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous float32 [max_pos, rope_dim]")
-    qs = qos = hq = 0
+    max_pos, rope_dim = cos_sin.shape
+    pq = pqo = pv = pvc = None
+    qs = qos = hq = vs = 0
     if q is not None:
-        hq = q.shape[1]
-        qs, qos = _rows(q, k, "q"), _rows(q_out, k, "q_out")
-        if q_out.shape[1] != hq:
+        hq, qs = _rows(q, dtype, T, d, "q")
+        ho, qos = _rows(q_out, dtype, T, d, "q_out")
+        if ho != hq:
             raise ValueError("q_out must have q's heads")
-    if v is not None and v.shape[1] != hkv:
-        raise ValueError("v must have k's heads")
-    rc = lib().saw_rope_append(
-        _at(q), qs, k.data_ptr(), _rows(k, k, "k"), _at(v), _rows(v, k, "v") if v is not None else 0,
-        _i32(positions, "positions", T), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-        1 if interleaved else 0, _i32(slot_mapping, "slot_mapping", T), T, hq, hkv, d,
-        _at(q_out) if q is not None else None, qos, k_cache.data_ptr(),
-        _at(v_cache) if v is not None else None, num_pages, page_size, int(rotate_k),
-        int(rotate_v), block_h, fmt, _i32(dev_status, "dev_status"), _raw_stream(k, stream))
-    _raise(rc, "saw_rope_append")
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
+    if v is not None:
+        hv, vs = _rows(v, dtype, T, d, "v")
+        if hv != hkv:
+            raise ValueError("v must have k's heads")
+        pv, pvc = v.data_ptr(), v_cache.data_ptr()
+    rc = (_lib or lib()).saw_rope_append(
+        pq, qs, k.data_ptr(), ks, pv, vs, _i32(positions, "positions", T), cos_sin.data_ptr(),
+        max_pos, rope_dim, 1 if interleaved else 0, _i32(slot_mapping, "slot_mapping", T), T, hq,
+        hkv, d, pqo, qos, k_cache.data_ptr(), pvc, num_pages, page_size, 1 if rotate_k else 0,
+        1 if rotate_v else 0, block_h, _formats(k, meta_bf16), _i32(dev_status, "dev_status"),
+        _on(stream, dev))
+    if rc:
+        _raise(rc, "saw_rope_append")
 
 
 def saw_prefix_decode_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int,
@@ -483,7 +502,7 @@ def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     or q's type; cu_group_seqs: int32 [groups + 1], prefix_lens: int32
     [groups]; workspace: saw_prefix_decode_workspace_bytes() bytes,
     zero-filled before its first use."""
-    _dev(q)
+    dev = _dev(q)
     B, hq, d = q.shape
     fmt = _formats(q, meta_bf16)
     if out.dtype is q.dtype:
@@ -493,17 +512,21 @@ def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     if not (q.is_contiguous() and out.is_contiguous() and out.shape == q.shape):
         raise ValueError("q and out must be contiguous and of one shape")
     groups = prefix_lens.numel()
-    if block_tables.shape[0] != B:
-        raise ValueError(f"block_tables must have {B} rows, not {block_tables.shape[0]}")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    rc = lib().saw_prefix_decode_int4(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        _i32(block_tables, "block_tables"), block_tables.shape[1], _i32(seq_lens, "seq_lens", B),
-        _i32(cu_group_seqs, "cu_group_seqs", groups + 1), _i32(prefix_lens, "prefix_lens"),
-        groups, B, max_prefix_len, max_own_len, hq, num_kv_heads, d, num_pages, page_size,
-        int(rotate_k), int(rotate_v), block_h, sm_scale, out.data_ptr(), _at(workspace), ws_bytes,
-        mode, fmt, _i32(dev_status, "dev_status"), _raw_stream(q, stream))
-    _raise(rc, "saw_prefix_decode_int4")
+    b, width = block_tables.shape
+    if b != B:
+        raise ValueError(f"block_tables must have {B} rows, not {b}")
+    pw, ws_bytes = None, 0
+    if workspace is not None:
+        pw, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = (_lib or lib()).saw_prefix_decode_int4(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _i32(block_tables, "block_tables"),
+        width, _i32(seq_lens, "seq_lens", B), _i32(cu_group_seqs, "cu_group_seqs", groups + 1),
+        _i32(prefix_lens, "prefix_lens"), groups, B, max_prefix_len, max_own_len, hq,
+        num_kv_heads, d, num_pages, page_size, 1 if rotate_k else 0, 1 if rotate_v else 0,
+        block_h, sm_scale, out.data_ptr(), pw, ws_bytes, mode, fmt,
+        _i32(dev_status, "dev_status"), _on(stream, dev))
+    if rc:
+        _raise(rc, "saw_prefix_decode_int4")
 
 
 # ---------------------------------------------------------------- *_ex twins

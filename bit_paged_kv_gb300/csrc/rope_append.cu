@@ -9,6 +9,7 @@
 // k goes on in binary32 into the append's butterfly and quantizer (the rule
 // of saw_quantize_append from "widen to binary32" on); q is rounded once, to
 // the input type.
+#include <numeric>
 #include <type_traits>
 
 #include "saw_device.cuh"
@@ -275,9 +276,14 @@ cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
 //
 // Bound: HBM.  131072 tokens, Hq 32, Hkv 8, D 128: 2.90 GB, 426 us at the
 // measured copy rate.
-constexpr int kBulkWarps = 8, kBulkCtasPerSm = 2;
+constexpr int kBulkWarps = 8;
+constexpr int kRounds = 4;  // rounds of q-head loads in flight
 constexpr int64_t kBulkMinElems = int64_t(1) << 21;  // smaller batches: a warp per row
 constexpr int kQPart = 16;  // q-heads per item
+// CTAs per SM (85 or 128 registers a thread): 131072 tokens 484 us with three,
+// 527 with two; the layout that exchanges partners by shuffles keeps two (its
+// 2047-token case 14.4 us, 22.3 with three and spills).
+constexpr int bulk_ctas(int layout) { return layout == 1 ? 2 : 3; }
 
 enum { kHalfWhole = 0, kHalfPart = 1, kInter = 2 };
 
@@ -451,7 +457,8 @@ __device__ __forceinline__ uint32_t codes8(const float* x, const RowMeta& m) {
 }
 
 template <int D, bool F16IN, int LAYOUT>
-__global__ void __launch_bounds__(32 * kBulkWarps, kBulkCtasPerSm) rope_append_bulk_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
+    rope_append_bulk_kernel(const RopeParams p, uint32_t warps) {
   pdl_wait_then_release();
   constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp
   const int lane = threadIdx.x & 31;
@@ -459,21 +466,28 @@ __global__ void __launch_bounds__(32 * kBulkWarps, kBulkCtasPerSm) rope_append_b
   const int nq = (p.num_q_heads + kQPart - 1) / kQPart;
   const uint32_t parts = uint32_t(nq + p.num_tensors);
   const uint32_t items = uint32_t(p.num_tokens) * parts;
-  const uint32_t warps = gridDim.x * kBulkWarps;
   const int hkv = p.num_kv_heads;
-  for (uint32_t it = blockIdx.x * kBulkWarps + (threadIdx.x >> 5); it < items; it += warps) {
+  uint32_t it = blockIdx.x * kBulkWarps + (threadIdx.x >> 5);
+  if (it >= warps) return;
+  // the next item's position and slot are under way while one is worked on
+  int pos_next = it < items ? p.positions[it / parts] : 0;
+  int slot_next = it < items ? p.slot_mapping[it / parts] : 0;
+  for (; it < items; it += warps) {
     const int t = int(it / parts), part = int(it - uint32_t(t) * parts);
-    const int pos = p.positions[t];
+    const int pos = pos_next, slot = slot_next;
+    if (it + warps < items) {
+      pos_next = p.positions[(it + warps) / parts];
+      slot_next = p.slot_mapping[(it + warps) / parts];
+    }
     const bool pos_ok = pos >= 0 && pos < p.max_pos;
     if (part < nq) {
-      // ---- q-heads, four rounds of loads in flight
+      // ---- q-heads, kRounds rounds of loads in flight
       if (!pos_ok) continue;  // (reported with the K rows)
-      Angles<LAYOUT> ang;
-      load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
       const int h0 = part * kQPart, h1 = min(p.num_q_heads, h0 + kQPart);
       const uint16_t* src = p.q + int64_t(t) * p.q_stride + 8 * a;
       uint16_t* dst = p.q_out + int64_t(t) * p.q_out_stride + 8 * a;
-      constexpr int kRounds = 4;
+      Angles<LAYOUT> ang;
+      load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
       for (int hb = h0; hb < h1; hb += RPW * kRounds) {
         uint4 w[kRounds][2];
 #pragma unroll
@@ -503,7 +517,6 @@ __global__ void __launch_bounds__(32 * kBulkWarps, kBulkCtasPerSm) rope_append_b
     }
     // ---- K or V rows
     const int tensor = part - nq;
-    const int32_t slot = p.slot_mapping[t];
     if (!pos_ok && tensor == 0 && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     if (slot == -1 || !pos_ok) continue;
     if (slot < 0 || int64_t(slot) >= p.num_slots) {
@@ -515,13 +528,13 @@ __global__ void __launch_bounds__(32 * kBulkWarps, kBulkCtasPerSm) rope_append_b
     const int page = slot >> p.page_shift, off = slot & (P - 1);
     uint8_t* chunk0 = (tensor ? p.v_cache : p.k_cache) + int64_t(page) * hkv * int64_t(P * (D / 2 + 4));
     const bool rot = (tensor ? p.rotate_v : p.rotate_k) != 0;
-    Angles<LAYOUT> ang;
-    if (tensor == 0) load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
     uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
     if (sub < hkv) {
       w0 = *reinterpret_cast<const uint4*>(src + sub * D);
       w1 = *reinterpret_cast<const uint4*>(src + sub * D + D / 2);
     }
+    Angles<LAYOUT> ang;
+    if (tensor == 0) load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
     for (int hb = 0; hb < hkv; hb += RPW) {
       const int h = hb + sub;
       float x[16];
@@ -560,10 +573,12 @@ __global__ void __launch_bounds__(32 * kBulkWarps, kBulkCtasPerSm) rope_append_b
 
 template <int D, bool F16IN, int LAYOUT>
 cudaError_t launch_bulk_l(const RopeParams& p, int sms, cudaStream_t stream) {
-  const int64_t items = int64_t(p.num_tokens) * ((p.num_q_heads + kQPart - 1) / kQPart + p.num_tensors);
+  const int parts = (p.num_q_heads + kQPart - 1) / kQPart + p.num_tensors;
+  const int64_t items = int64_t(p.num_tokens) * parts;
   const int64_t want = (items + kBulkWarps - 1) / kBulkWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(want < int64_t(kBulkCtasPerSm) * sms ? want : int64_t(kBulkCtasPerSm) * sms));
+  const int64_t most = int64_t(bulk_ctas(LAYOUT)) * sms;
+  cfg.gridDim = dim3(unsigned(want < most ? want : most));
   cfg.blockDim = dim3(32 * kBulkWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -571,7 +586,11 @@ cudaError_t launch_bulk_l(const RopeParams& p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_append_bulk_kernel<D, F16IN, LAYOUT>, p);
+  // a stride coprime to the parts gives every warp all kinds of them in turn
+  // (a common divisor: some warps quantize, some only turn q; 525 -> 690 us)
+  uint32_t warps = cfg.gridDim.x * kBulkWarps;
+  while (warps > 1 && std::gcd(warps, uint32_t(parts)) != 1) --warps;
+  return cudaLaunchKernelEx(&cfg, rope_append_bulk_kernel<D, F16IN, LAYOUT>, p, warps);
 }
 
 template <int D>
