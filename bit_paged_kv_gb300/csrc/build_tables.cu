@@ -12,25 +12,28 @@
 // a prefix of the list, whatever the order in which CTAs run.
 //
 // One launch, and no CTA waits for another: every CTA computes the two
-// exclusive sums (tokens, pages) over all requests itself -- each warp a
-// contiguous run of requests with coalesced loads, then one scan over the 16
-// warps' totals -- and keeps them in shared memory, one entry per request (per
-// 32 requests above kDirect).  That is 8 bytes per request and CTA from L2,
-// against a second launch or a look-back between CTAs.  Then the grid shares
-// out (request, 256 entries) pieces of table rows to warps and the tokens to
-// threads, each token finding its request by bisection in shared memory.
-#include "saw_device.cuh"
-#include "saw_int4.h"
-#include "saw_quant_row.cuh"
-
+// exclusive sums (tokens, pages) over all requests itself -- coalesced loads
+// into shared memory, each thread the sum of a run of requests, one scan over
+// threads -- and keeps them with the requests' lengths and rows (above kDirect
+// requests, the sums of every 32nd only).  That is 12 bytes per request and
+// CTA from L2, against a second launch or a look-back between CTAs.  Then the
+// grid shares out (request, 512 entries) pieces of table rows and runs of 128
+// tokens to warps.  A warp's first and last token, found by bisection, bound
+// the search of the others; the four page words of a lane load together.
+//
+// Bound: 64 requests with tables of up to 16384 tokens (0.3 MB), 4.2 us, are
+// a launch and four dependent loads.  4096 requests of up to 32768 cached and
+// 256 new tokens, 13.1 us, move 42 MB (6.2 us at the measured copy rate); the
+// rest is issue: 17.6 us with 64-bit sums and the group size a variable, 33.9
+// with a scan per 32 requests in two CTAs per SM.
 namespace saw {
 namespace {
 
-constexpr int kTabThreads = 512;
-constexpr int kTabWarps = kTabThreads / 32;
+constexpr int kTabMaxThreads = 1024;
 constexpr int kDirect = 4096;   // up to this many requests: one prefix entry per request
 constexpr int kGroup = 32;      // above: one per 32
-constexpr int kPiece = 256;     // table entries per warp item
+constexpr int kPiece = 512;     // table entries per warp item
+constexpr int kAhead = 4;       // requests a thread loads at once
 constexpr int kTokPerLane = 4;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
@@ -42,23 +45,32 @@ struct Req {
   bool ok;
 };
 
-__device__ __forceinline__ Req load_req(const TablesParams& p, int b) {
+struct Raw {
+  int c, n, row;
+};
+__device__ __forceinline__ Raw load_raw(const TablesParams& p, int b) {
+  return Raw{p.cached_lens ? p.cached_lens[b] : 0, p.new_lens[b], p.src_rows ? p.src_rows[b] : b};
+}
+__device__ __forceinline__ Req make_req(const TablesParams& p, const Raw& x) {
   Req r;
-  const int c = p.cached_lens ? p.cached_lens[b] : 0;
-  const int n = p.new_lens[b];
-  r.row = p.src_rows ? p.src_rows[b] : b;
+  const int c = x.c, n = x.n;
+  r.row = x.row;
   r.tokens = max(n, 0);
-  const int64_t total = int64_t(c) + n;
-  r.ok = c >= 0 && n >= 0 && total <= (int64_t(p.max_blocks) << p.page_shift);
-  if (r.ok && c > 0)
-    r.ok = p.src_tables != nullptr && r.row >= 0 && r.row < p.num_src_rows &&
-           ((int64_t(c) + p.page_size - 1) >> p.page_shift) <= p.src_blocks;
+  // unsigned words hold c + n and c + page_size - 1 of any two counts
+  const uint32_t uc = uint32_t(c), total = uc + uint32_t(n), up = uint32_t(p.page_size) - 1;
+  const uint32_t old = (uc + up) >> p.page_shift;
+  r.ok = c >= 0 && n >= 0 && total <= uint32_t(p.max_blocks) << p.page_shift;
+  if (c > 0)
+    r.ok = r.ok && p.src_tables != nullptr && uint32_t(r.row) < uint32_t(p.num_src_rows) &&
+           old <= uint32_t(p.src_blocks);
   r.cached = r.ok ? c : 0;
   r.fresh = r.ok ? n : 0;
-  r.old = int((int64_t(r.cached) + p.page_size - 1) >> p.page_shift);
-  r.need = int((int64_t(r.cached) + r.fresh + p.page_size - 1) >> p.page_shift) - r.old;
+  r.old = r.ok ? int(old) : 0;
+  r.need = r.ok ? int(((total + up) >> p.page_shift) - old) : 0;
   return r;
 }
+
+__device__ __forceinline__ Req load_req(const TablesParams& p, int b) { return make_req(p, load_raw(p, b)); }
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
 #pragma unroll
@@ -71,9 +83,13 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusiv
 
 __device__ __forceinline__ int clamp32(int64_t v) { return int(min(v, int64_t(INT32_MAX))); }
 
-// The last entry u in [0, n) with pre[u] <= x (pre ascending, pre[0] = 0).
-__device__ __forceinline__ int find_last(const int* pre, int n, int x) {
-  int lo = 0, hi = n;
+// Whether `need` pages after `off` are within the list; off and need <= 2^31 - 1.
+__device__ __forceinline__ bool covered(int off, int need, int nfree) {
+  return need == 0 || uint32_t(off) + uint32_t(need) <= uint32_t(nfree);
+}
+
+// The last entry u in [lo, hi) with pre[u] <= x (pre ascending, pre[lo] <= x).
+__device__ __forceinline__ int find_last(const int* pre, int lo, int hi, int x) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pre[mid] <= x) lo = mid; else hi = mid;
@@ -81,74 +97,102 @@ __device__ __forceinline__ int find_last(const int* pre, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesParams p) {
+// Entry b of a shared array, one word skipped per 32: a thread's run of
+// consecutive requests starts in a bank of its own.
+__device__ __forceinline__ int pad(int b) { return b + (b >> 5); }
+
+// unit: requests per entry of the exclusive sums, 1 or kGroup.
+template <int unit>
+__global__ void __launch_bounds__(kTabMaxThreads) build_tables_kernel(const TablesParams p) {
   pdl_wait_then_release();
   extern __shared__ int sm[];
-  __shared__ int64_t base_tok[kTabWarps], base_page[kTabWarps];
+  __shared__ int64_t base_tok[kTabMaxThreads / 32], base_page[kTabMaxThreads / 32];
   __shared__ int64_t total_tok;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, cta_warps = threads >> 5;
   const int B = p.num_seqs;
-  const int unit = B <= kDirect ? 1 : kGroup;
   const int units = (B + unit - 1) / unit;
-  int* pre_tok = sm;            // [units + 1] tokens before unit u (clamped to int32)
-  int* pre_page = sm + units + 1;
+  int* pre_tok = sm;                      // [units + 1] tokens before unit u (clamped to int32)
+  int* pre_page = pre_tok + units + 1;    // [units + 1] pages before unit u
+  int* req_c = pre_page + units + 1;      // with unit 1, by pad(b): cached, new, row as given
+  int* req_n = req_c + pad(units) + 1;
+  int* req_row = req_n + pad(units) + 1;
+  const int nfree_raw = p.num_free ? *p.num_free : p.max_free;
 
-  // ---- exclusive sums: warp w takes requests [w run, (w + 1) run)
-  const int run = ((B + kTabWarps - 1) / kTabWarps + 31) / 32 * 32;
-  const int b_lo = min(B, warp * run), b_hi = min(B, b_lo + run);
-  int64_t ct = 0, cp = 0;
-  for (int b0 = b_lo; b0 < b_hi; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t t = 0, g = 0;
-    if (b < b_hi) {
-      const Req r = load_req(p, b);
-      t = r.tokens;
-      g = r.need;
+  // ---- exclusive sums: thread t takes the requests [t run, (t + 1) run)
+  if (unit == 1) {
+    for (int b0 = tid; b0 < B; b0 += kAhead * threads) {
+      Raw x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (b0 + k * threads < B) x[k] = load_raw(p, b0 + k * threads);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int b = b0 + k * threads;
+        if (b < B) {
+          req_c[pad(b)] = x[k].c;
+          req_n[pad(b)] = x[k].n;
+          req_row[pad(b)] = x[k].row;
+        }
+      }
     }
-    const int64_t ti = warp_scan(t, lane), gi = warp_scan(g, lane);
-    if (b < b_hi && b % unit == 0) {
-      pre_tok[b / unit] = clamp32(ct + ti - t);
-      pre_page[b / unit] = clamp32(cp + gi - g);
-    }
-    ct += __shfl_sync(kAll, ti, 31);
-    cp += __shfl_sync(kAll, gi, 31);
+    __syncthreads();
   }
-  if (lane == 0) {
-    base_tok[warp] = ct;
-    base_page[warp] = cp;
+  auto req_of = [&](int b) {
+    return make_req(p, unit == 1 ? Raw{req_c[pad(b)], req_n[pad(b)], req_row[pad(b)]} : load_raw(p, b));
+  };
+  const int run = (units + threads - 1) / threads * unit;
+  const int b_lo = int(min(int64_t(B), int64_t(tid) * run)), b_hi = min(B, b_lo + run);
+  int64_t ct = 0, cp = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Req r = req_of(b);
+    ct += r.tokens;
+    cp += r.need;
+  }
+  const int64_t ti = warp_scan(ct, lane), gi = warp_scan(cp, lane);
+  if (lane == 31) {
+    base_tok[warp] = ti;
+    base_page[warp] = gi;
   }
   __syncthreads();
   if (warp == 0) {
-    const int64_t t = lane < kTabWarps ? base_tok[lane] : 0, g = lane < kTabWarps ? base_page[lane] : 0;
-    const int64_t ti = warp_scan(t, lane), gi = warp_scan(g, lane);
+    const int64_t t = lane < cta_warps ? base_tok[lane] : 0, g = lane < cta_warps ? base_page[lane] : 0;
+    const int64_t te = warp_scan(t, lane), ge = warp_scan(g, lane);
     __syncwarp();
-    if (lane < kTabWarps) {
-      base_tok[lane] = ti - t;
-      base_page[lane] = gi - g;
+    if (lane < cta_warps) {
+      base_tok[lane] = te - t;
+      base_page[lane] = ge - g;
     }
-    if (lane == kTabWarps - 1) {
-      total_tok = ti;
-      pre_tok[units] = clamp32(ti);
-      pre_page[units] = clamp32(gi);
+    if (lane == 31) {
+      total_tok = te;
+      pre_tok[units] = clamp32(te);
+      pre_page[units] = clamp32(ge);
     }
   }
   __syncthreads();
-  for (int u = tid; u < units; u += kTabThreads) {
-    const int w = u * unit / run;
-    pre_tok[u] = clamp32(pre_tok[u] + base_tok[w]);
-    pre_page[u] = clamp32(pre_page[u] + base_page[w]);
+  ct = base_tok[warp] + ti - ct;
+  cp = base_page[warp] + gi - cp;
+  for (int b = b_lo; b < b_hi; ++b) {
+    if (b % unit == 0) {
+      pre_tok[b / unit] = clamp32(ct);
+      pre_page[b / unit] = clamp32(cp);
+      if (unit != 1 && b + unit >= b_hi) break;
+    }
+    const Req r = req_of(b);
+    ct += r.tokens;
+    cp += r.need;
   }
   __syncthreads();
 
-  const int nfree_raw = p.num_free ? *p.num_free : p.max_free;
   const int nfree = min(max(nfree_raw, 0), p.max_free);
-  const int gw = blockIdx.x * kTabWarps + warp, warps = gridDim.x * kTabWarps;
+  // warps of the grid, those of one CTA far apart in the order of the work
+  const int gw = warp * gridDim.x + blockIdx.x, warps = gridDim.x * cta_warps;
 
   // ---- per-request words, 32 requests per warp; the pages taken
   for (int b0 = 32 * gw; b0 < B; b0 += 32 * warps) {
     const int b = b0 + lane;
     Req r{};
-    if (b < B) r = load_req(p, b);
+    if (b < B) r = req_of(b);
     const int64_t t = pre_tok[b0 / unit] + warp_scan(r.tokens, lane);
     const int64_t g = pre_page[b0 / unit] + warp_scan(r.need, lane);
     if (b < B) {
@@ -159,7 +203,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
       if (!fits) report(p.dev_status, SAW_ERR_DEVICE_PAGES);
     }
   }
-  if (blockIdx.x == 0 && warp == 0) {
+  if (blockIdx.x == 0 && warp == cta_warps - 1) {
     if (lane == 0) {
       p.cu_q_lens[0] = 0;
       if (total_tok > p.max_tokens || nfree_raw != nfree) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
@@ -176,7 +220,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
       }
       const int b = lo * kGroup + lane;
       int64_t need = 0;
-      if (b < B) need = load_req(p, b).need;
+      if (b < B) need = req_of(b).need;
       const int64_t first = pre_page[lo * step], g = first + warp_scan(need, lane);
       int64_t best = g <= nfree ? g : first;
 #pragma unroll
@@ -186,16 +230,16 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
   }
 
   // first page of request b in the free list
-  auto page_base = [&](int b) -> int64_t {  // whole warp, b uniform
-    if (unit == 1) return pre_page[b];
+  auto page_base = [&](int b) -> int {  // whole warp, b uniform
+    if constexpr (unit == 1) return pre_page[b];
     const int b0 = b / kGroup * kGroup;
     int64_t n = 0;
     if (b0 + lane < b) n = load_req(p, b0 + lane).need;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(kAll, n, d);
-    return pre_page[b / kGroup] + n;
+    return clamp32(pre_page[b / kGroup] + n);
   };
-  auto free_page = [&](int64_t i) {  // i < nfree
+  auto free_page = [&](int i) {  // i < nfree
     const int id = p.free_pages[i];
     if (id >= 0 && id < p.num_pages) return id;
     report(p.dev_status, SAW_ERR_DEVICE_INDEX);
@@ -203,81 +247,95 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
   };
 
   // ---- table rows, kPiece entries per warp item
-  const int pieces = (p.max_blocks + kPiece - 1) / kPiece;
+  const int pieces = max(1, (p.max_blocks + kPiece - 1) / kPiece);
   const bool in_place = p.block_tables == p.src_tables;
-  for (int64_t it = gw; it < int64_t(B) * pieces; it += warps) {
-    const int b = int(it / pieces), e0 = int(it % pieces) * kPiece;
-    const Req r = load_req(p, b);
+  const int rows_on = warps / pieces, pieces_on = warps % pieces;
+  int64_t row = gw / pieces;
+  int piece = gw % pieces;
+  for (; row < B; row += rows_on, piece += pieces_on) {
+    if (piece >= pieces) {
+      piece -= pieces;
+      if (++row >= B) break;
+    }
+    const int b = int(row), e0 = piece * kPiece;
+    const Req r = req_of(b);
     const int last = r.old + r.need;
     if (e0 >= last || (in_place && e0 + kPiece <= r.old)) continue;
-    int64_t off = 0;
+    int off = 0;
     bool fits = true;
     if (r.need > 0 && e0 + kPiece > r.old) {
       off = page_base(b);
-      fits = off + r.need <= nfree;
+      fits = covered(off, r.need, nfree);
     }
     const int32_t* src = p.src_tables + int64_t(r.row) * p.src_blocks;
     int32_t* dst = p.block_tables + int64_t(b) * p.max_blocks;
     int v[kPiece / 32];
+    if (!in_place && e0 < r.old) {
 #pragma unroll
-    for (int k = 0; k < kPiece / 32; ++k) {
-      const int e = e0 + 32 * k + lane;
-      if (e < r.old) {
-        v[k] = in_place ? 0 : src[e];
-      } else if (e < last && fits) {
-        v[k] = free_page(off + e - r.old);
-      }
+      for (int k = 0; k < kPiece / 32; ++k)
+        if (e0 + 32 * k + lane < r.old) v[k] = src[e0 + 32 * k + lane];
+#pragma unroll
+      for (int k = 0; k < kPiece / 32; ++k)
+        if (e0 + 32 * k + lane < r.old) dst[e0 + 32 * k + lane] = v[k];
     }
-#pragma unroll
-    for (int k = 0; k < kPiece / 32; ++k) {
-      const int e = e0 + 32 * k + lane;
-      if (e < r.old ? !in_place : (e < last && fits)) dst[e] = v[k];
+    if (fits) {
+      const int e1 = min(e0 + kPiece, last);
+      for (int e = max(e0, r.old) + lane; e < e1; e += 32) dst[e] = free_page(off + (e - r.old));
     }
   }
 
   // ---- tokens
   const int total = int(min(total_tok, int64_t(p.max_tokens)));
   const int64_t step = int64_t(warps) * 32 * kTokPerLane;
-  for (int64_t t0 = int64_t(gw) * 32 * kTokPerLane; t0 < p.max_tokens; t0 += step) {
+  // (from the far end of the grid: the near warps have the requests' words)
+  for (int64_t t0 = int64_t(warps - 1 - gw) * 32 * kTokPerLane; t0 < p.max_tokens; t0 += step) {
+    // the requests of the warp's first and last token bound every lane's search
+    const int t_end = int(min(t0 + 32 * kTokPerLane, int64_t(total))) - 1;
+    int u_lo = 0, u_hi = 0;
+    if (t0 < total) {
+      const int u = find_last(pre_tok, 0, units, lane < 16 ? int(t0) : t_end);
+      u_lo = __shfl_sync(kAll, u, 0);
+      u_hi = __shfl_sync(kAll, u, 31) + 1;
+    }
+    // each token's place and the word that names its page; then all the words
+    const int32_t* word[kTokPerLane];
+    int at[kTokPerLane];
 #pragma unroll
     for (int k = 0; k < kTokPerLane; ++k) {
-      const int64_t t64 = t0 + 32 * k + lane;
-      if (t64 >= p.max_tokens) break;
-      const int t = int(t64);
-      int slot = -1, pos = 0;
-      if (t < total) {
-        int b = find_last(pre_tok, units, t) * unit;
-        int64_t off = pre_page[b / unit];
-        Req r;
-        int i = t - pre_tok[b / unit];
-        if (unit == 1) {
-          r = load_req(p, b);
-        } else {
-          for (;; ++b) {  // within 32 requests (t < total: one of them holds it)
-            r = load_req(p, b);
-            if (i < r.tokens || b + 1 >= B) break;
-            i -= r.tokens;
-            off += r.need;
-          }
+      const int64_t t = t0 + 32 * k + lane;
+      word[k] = nullptr;
+      at[k] = 0;
+      if (t >= total) continue;
+      int b = find_last(pre_tok, u_lo, u_hi, int(t)) * unit;
+      int off = pre_page[b / unit];
+      int i = int(t) - pre_tok[b / unit];
+      Req r = req_of(b);
+      if constexpr (unit != 1) {  // one of 32 holds it
+        int64_t pages = off;
+        while (i >= r.tokens && b + 1 < B) {
+          i -= r.tokens;
+          pages += r.need;
+          r = load_req(p, ++b);
         }
-        if (r.ok && (r.need == 0 || off + r.need <= nfree)) {
-          const int at = r.cached + i, lp = at >> p.page_shift;
-          int id;
-          if (lp < r.old) {
-            id = p.src_tables[int64_t(r.row) * p.src_blocks + lp];
-            if (id < 0 || id >= p.num_pages) {
-              report(p.dev_status, SAW_ERR_DEVICE_INDEX);
-              id = -1;
-            }
-          } else {
-            id = free_page(off + lp - r.old);
-          }
-          if (id >= 0) slot = (id << p.page_shift) + (at & (p.page_size - 1));
-          pos = at;
-        }
+        off = clamp32(pages);
       }
-      p.slot_mapping[t] = slot;
-      if (p.positions) p.positions[t] = pos;
+      if (!r.ok || !covered(off, r.need, nfree)) continue;
+      at[k] = r.cached + i;
+      const int lp = at[k] >> p.page_shift;
+      word[k] = lp < r.old ? p.src_tables + (int64_t(r.row) * p.src_blocks + lp)
+                           : p.free_pages + (off + (lp - r.old));
+    }
+    int id[kTokPerLane];
+#pragma unroll
+    for (int k = 0; k < kTokPerLane; ++k) id[k] = word[k] ? *word[k] : -1;
+#pragma unroll
+    for (int k = 0; k < kTokPerLane; ++k) {
+      const int64_t t = t0 + 32 * k + lane;
+      if (t >= p.max_tokens) break;
+      const bool good = id[k] >= 0 && id[k] < p.num_pages;
+      if (word[k] && !good) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+      p.slot_mapping[t] = good ? (id[k] << p.page_shift) + (at[k] & (p.page_size - 1)) : -1;
+      if (p.positions) p.positions[t] = at[k];
     }
   }
 }
@@ -287,15 +345,24 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
 cudaError_t launch_build_tables(const TablesParams& p, int sms, cudaStream_t stream) {
   const int unit = p.num_seqs <= kDirect ? 1 : kGroup;
   const int units = (p.num_seqs + unit - 1) / unit;
-  const size_t smem = size_t(2) * (units + 1) * sizeof(int);
-  // warps for every row piece and token, at most two CTAs per SM
+  const int padded = units + units / 32 + 1;
+  const size_t smem = (size_t(2) * (units + 1) + (unit == 1 ? size_t(3) * padded : 0)) * sizeof(int);
+  const auto kernel = unit == 1 ? &build_tables_kernel<1> : &build_tables_kernel<kGroup>;
+  if (smem > 48 * 1024) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (err != cudaSuccess) return err;
+  }
+  // a warp for every row piece or 128 tokens, at most one full CTA per SM
   const int64_t pieces = int64_t(p.num_seqs) * ((p.max_blocks + kPiece - 1) / kPiece);
   const int64_t tok = (int64_t(p.max_tokens) + 32 * kTokPerLane - 1) / (32 * kTokPerLane);
-  const int64_t want = ((pieces > tok ? pieces : tok) + kTabWarps - 1) / kTabWarps;
-  const int grid = int(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
+  const int64_t items = pieces > tok ? pieces : tok;
+  const int threads = items > 8 * sms ? kTabMaxThreads : 256;
+  const int64_t want = (items + threads / 32 - 1) / (threads / 32);
+  const int grid = int(want < 1 ? 1 : want > sms ? sms : want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kTabThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -303,7 +370,7 @@ cudaError_t launch_build_tables(const TablesParams& p, int sms, cudaStream_t str
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace saw
