@@ -26,6 +26,10 @@
 // 256 new tokens, 13.1 us, move 42 MB (6.2 us at the measured copy rate); the
 // rest is issue: 17.6 us with 64-bit sums and the group size a variable, 33.9
 // with a scan per 32 requests in two CTAs per SM.
+#include "saw_device.cuh"
+#include "saw_int4.h"
+#include "saw_quant_row.cuh"
+
 namespace saw {
 namespace {
 
