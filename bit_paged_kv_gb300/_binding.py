@@ -8,6 +8,8 @@ the library has not been built this module raises on first use.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -348,44 +350,36 @@ def saw_prefill_attn_int4(q: torch.Tensor, cu_q_lens: torch.Tensor, k_cache: tor
 
 # ---------------------------------------------------------------- a serving step
 # These calls run once or more per layer on small batches, where the host's
-# share of a call is what a user waits for: pointers are passed as plain
-# integers and every check is one comparison.
+# share of a call is what a user waits for: a CPython extension checks and
+# marshals their arguments.
 
-_INT32 = torch.int32
-# The current stream as an integer, without building a Stream object (2 us of
-# a 10 us call).
-_raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_step = None
 
 
-def _dev(t: torch.Tensor) -> int:
-    """The library launches on the current device: it has to be the tensors'."""
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
+def _bind_step():
+    """Load the in-tree extension of the serving step's calls (raises if it has
+    not been built)."""
+    global _step
+    L = lib()
+    path = os.path.join(HERE, "_build", "_saw_step.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} not found; build it with `python bit_paged_kv_gb300/build.py`")
+    loader = importlib.machinery.ExtensionFileLoader("_saw_step", path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_saw_step", loader))
+    loader.exec_module(m)
+    at = [C.cast(getattr(L, f), C.c_void_p).value
+          for f in ("saw_build_tables", "saw_rope_table", "saw_rope_append", "saw_prefix_decode_int4")]
+    m.init(*at, torch.int32, torch.float32, torch.bfloat16, torch.float16,
+           getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+           getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream))
+    _step = m
+    return m
 
 
-def _on(stream, dev: int) -> int:
-    if stream is None:
-        if _raw_current is not None:
-            return _raw_current(dev)
-        return torch.cuda.current_stream(dev).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _i32(t, what: str, n: int = -1):
-    if t is None:
-        return None
-    if t.dtype is not _INT32 or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous int32")
-    if n >= 0 and t.numel() != n:
-        raise ValueError(f"{what} must have {n} entries, not {t.numel()}")
-    return t.data_ptr()
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _raw_stream(dev: int) -> int:
+    """The current stream as an integer (torch's own call for it, where there is
+    one, builds no Stream object: 2 us less)."""
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def saw_build_tables(cached_lens, new_lens: torch.Tensor, free_pages: torch.Tensor, num_free,
@@ -398,20 +392,9 @@ def saw_build_tables(cached_lens, new_lens: torch.Tensor, free_pages: torch.Tens
     [B] and a list of free pages; num_free: int32 [1] or None (all of the
     list).  src_tables [R, blocks] with src_rows [B]: the requests' tables so
     far (None: nothing cached; block_tables itself: extended in place)."""
-    dev = _dev(new_lens)
-    B, tokens = new_lens.numel(), slot_mapping.numel()
-    rows, blocks = src_tables.shape if src_tables is not None else (0, 0)
-    b, width = block_tables.shape
-    if b != B:
-        raise ValueError(f"block_tables must have {B} rows, not {b}")
-    rc = (_lib or lib()).saw_build_tables(
-        _i32(src_tables, "src_tables"), rows, blocks, _i32(src_rows, "src_rows", B),
-        _i32(cached_lens, "cached_lens", B), _i32(new_lens, "new_lens"),
-        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(num_free, "num_free", 1), B,
-        tokens, num_pages, page_size, _i32(block_tables, "block_tables"), width, _i32(seq_lens, "seq_lens", B),
-        _i32(cu_q_lens, "cu_q_lens", B + 1), _i32(slot_mapping, "slot_mapping"),
-        _i32(positions, "positions", tokens), _i32(pages_taken, "pages_taken", 1),
-        _i32(dev_status, "dev_status"), _on(stream, dev))
+    rc = (_step or _bind_step()).build_tables(
+        cached_lens, new_lens, free_pages, num_free, page_size, num_pages, block_tables, seq_lens,
+        cu_q_lens, slot_mapping, positions, pages_taken, src_tables, src_rows, dev_status, stream)
     if rc:
         _raise(rc, "saw_build_tables")
 
@@ -421,24 +404,10 @@ def saw_rope_table(cos_sin: torch.Tensor, base: float = 10000.0, scaling: int = 
                    high: float = 0.0, att_scale: float = 0.0, stream=None) -> None:
     """Fill cos_sin (float32 [max_pos, rope_dim]): cosines of the rope_dim/2
     pairs, then sines.  scaling: one of SAW_ROPE_*; see include/saw_int4.h."""
-    dev = _dev(cos_sin)
-    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be contiguous float32 [max_pos, rope_dim]")
-    n, r = cos_sin.shape
-    rc = (_lib or lib()).saw_rope_table(cos_sin.data_ptr(), n, r, base, scaling, factor,
-                                        orig_max_pos, low, high, att_scale, _on(stream, dev))
+    rc = (_step or _bind_step()).rope_table(cos_sin, base, scaling, factor, orig_max_pos, low, high,
+                                            att_scale, stream)
     if rc:
         _raise(rc, "saw_rope_table")
-
-
-def _rows(t: torch.Tensor, dtype, T: int, D: int, what: str):
-    """(heads, token stride) of rows [T, heads, D] with only the token dimension strided."""
-    n, h, d = t.shape
-    s0, s1, s2 = t.stride()
-    if t.dtype is not dtype or n != T or d != D or s2 != 1 or (s1 != D and h != 1):
-        raise ValueError(f"{what} must be [{T}, heads, {D}] rows of k's type, each token's contiguous")
-    # (a single token's stride is whatever the view says; it is never used)
-    return h, (s0 if T > 1 else h * D)
 
 
 def saw_rope_append(q, k: torch.Tensor, v, positions: torch.Tensor, cos_sin: torch.Tensor,
@@ -450,32 +419,9 @@ def saw_rope_append(q, k: torch.Tensor, v, positions: torch.Tensor, cos_sin: tor
     [T, Hq, D], k, v: [T, Hkv, D], bfloat16 or float16, token dim strided;
     q (with q_out) and v may be None; q_out may be q.  positions,
     slot_mapping: int32 [T]; cos_sin: float32 [max_pos, rope_dim]."""
-    dev = _dev(k)
-    T, _, d = k.shape
-    dtype = k.dtype
-    hkv, ks = _rows(k, dtype, T, d, "k")
-    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be contiguous float32 [max_pos, rope_dim]")
-    max_pos, rope_dim = cos_sin.shape
-    pq = pqo = pv = pvc = None
-    qs = qos = hq = vs = 0
-    if q is not None:
-        hq, qs = _rows(q, dtype, T, d, "q")
-        ho, qos = _rows(q_out, dtype, T, d, "q_out")
-        if ho != hq:
-            raise ValueError("q_out must have q's heads")
-        pq, pqo = q.data_ptr(), q_out.data_ptr()
-    if v is not None:
-        hv, vs = _rows(v, dtype, T, d, "v")
-        if hv != hkv:
-            raise ValueError("v must have k's heads")
-        pv, pvc = v.data_ptr(), v_cache.data_ptr()
-    rc = (_lib or lib()).saw_rope_append(
-        pq, qs, k.data_ptr(), ks, pv, vs, _i32(positions, "positions", T), cos_sin.data_ptr(),
-        max_pos, rope_dim, 1 if interleaved else 0, _i32(slot_mapping, "slot_mapping", T), T, hq,
-        hkv, d, pqo, qos, k_cache.data_ptr(), pvc, num_pages, page_size, 1 if rotate_k else 0,
-        1 if rotate_v else 0, block_h, _formats(k, meta_bf16), _i32(dev_status, "dev_status"),
-        _on(stream, dev))
+    rc = (_step or _bind_step()).rope_append(
+        q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, num_pages, page_size,
+        rotate_k, rotate_v, block_h, interleaved, dev_status, stream, meta_bf16)
     if rc:
         _raise(rc, "saw_rope_append")
 
@@ -502,29 +448,10 @@ def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     or q's type; cu_group_seqs: int32 [groups + 1], prefix_lens: int32
     [groups]; workspace: saw_prefix_decode_workspace_bytes() bytes,
     zero-filled before its first use."""
-    dev = _dev(q)
-    B, hq, d = q.shape
-    fmt = _formats(q, meta_bf16)
-    if out.dtype is q.dtype:
-        fmt |= SAW_FMT_OUT_INPUT
-    elif out.dtype is not torch.float32:
-        raise ValueError("out must be float32 or q's type")
-    if not (q.is_contiguous() and out.is_contiguous() and out.shape == q.shape):
-        raise ValueError("q and out must be contiguous and of one shape")
-    groups = prefix_lens.numel()
-    b, width = block_tables.shape
-    if b != B:
-        raise ValueError(f"block_tables must have {B} rows, not {b}")
-    pw, ws_bytes = None, 0
-    if workspace is not None:
-        pw, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    rc = (_lib or lib()).saw_prefix_decode_int4(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _i32(block_tables, "block_tables"),
-        width, _i32(seq_lens, "seq_lens", B), _i32(cu_group_seqs, "cu_group_seqs", groups + 1),
-        _i32(prefix_lens, "prefix_lens"), groups, B, max_prefix_len, max_own_len, hq,
-        num_kv_heads, d, num_pages, page_size, 1 if rotate_k else 0, 1 if rotate_v else 0,
-        block_h, sm_scale, out.data_ptr(), pw, ws_bytes, mode, fmt,
-        _i32(dev_status, "dev_status"), _on(stream, dev))
+    rc = (_step or _bind_step()).prefix_decode(
+        q, k_cache, v_cache, block_tables, seq_lens, cu_group_seqs, prefix_lens, max_prefix_len,
+        max_own_len, num_kv_heads, num_pages, page_size, rotate_k, rotate_v, block_h, out,
+        workspace, sm_scale, dev_status, stream, meta_bf16, mode)
     if rc:
         _raise(rc, "saw_prefix_decode_int4")
 

@@ -2,13 +2,16 @@
 
 Each translation unit is compiled for sm_103a only (one -gencode), in
 parallel, then linked into one shared library exporting the C ABI of
-include/saw_int4.h.  No torch headers are involved.
+include/saw_int4.h.  Beside it goes _saw_step.so, a small CPython extension
+through which Python makes the serving step's calls.  No torch headers are
+involved.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsaw_int4.so")
+STEP = os.path.join(OUT_DIR, "_saw_step.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -63,9 +67,9 @@ def _deps() -> list[str]:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB):
+    if not force and os.path.exists(LIB) and os.path.exists(STEP):
         newest = max(os.path.getmtime(f) for f in _deps())
-        if os.path.getmtime(LIB) >= newest:
+        if min(os.path.getmtime(LIB), os.path.getmtime(STEP)) >= newest:
             return LIB
     nvcc = _nvcc()
 
@@ -82,8 +86,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(UNITS)) as ex:
+    def compile_step() -> None:
+        tmp = STEP + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I",
+               sysconfig.get_paths()["include"], os.path.join(CSRC, "step_binding.cpp"), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for step_binding.cpp:\n{r.stderr}")
+        os.replace(tmp, STEP)
+
+    with ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
+        step = ex.submit(compile_step)
         objs = list(ex.map(compile_one, UNITS))
+        step.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
