@@ -564,7 +564,8 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
     return SAW_ERR_INVALID_ARG;
   if (num_q_heads % num_kv_heads) return SAW_ERR_INVALID_ARG;
   if (head_dim != kHeadDim || !page_size_ok(page_size) ||
-      num_q_heads / num_kv_heads > saw::kMaxGroup || num_seqs > 65535 || num_kv_heads > 65535)
+      num_q_heads / num_kv_heads > saw::kMaxGroup || num_seqs > 65535 || num_groups > 65535 ||
+      num_kv_heads > 65535)
     return SAW_ERR_UNSUPPORTED;
   PrefixPlan p{};
   const int sms_raw = sm_count();
@@ -650,10 +651,6 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
                       workspace, workspace_bytes, 0, formats, dev_status);
   if (rc != SAW_OK || num_seqs == 0) return rc;
   if (out16) p.out16 = static_cast<uint16_t*>(out);
-  // short own parts, one split: four 4-warp CTAs per SM already when that saves
-  // a wave
-  const int sms_now = sm_count();
-  if (p.num_splits == 1 && int64_t(num_seqs) * num_kv_heads > 2 * int64_t(sms_now)) p.warps = 4;
   p.max_blocks = max_blocks_per_seq;
   p.max_seq_len = int32_t(std::min<int64_t>(int64_t(max_prefix_len) + max_own_len,
                                             int64_t(max_blocks_per_seq) * page_size));

@@ -564,7 +564,8 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  *
  * A group with inconsistent entries is reported as SAW_ERR_DEVICE_INDEX and
  * shares nothing.  Other arguments and errors as saw_paged_decode_int4;
- * head_dim 128 and at most 8 q-heads per kv-head (else SAW_ERR_UNSUPPORTED).
+ * head_dim 128, at most 8 q-heads per kv-head and 65535 groups (else
+ * SAW_ERR_UNSUPPORTED).
  */
 #define SAW_FMT_OUT_INPUT 4
 #define SAW_PREFIX_AUTO 0

@@ -106,7 +106,7 @@ def _prefix(L, **kw):
     (dict(mb=-1), INV), (dict(cu=None), INV), (dict(pre=None), INV), (dict(q=None), INV), (dict(kc=None), INV),
     (dict(bt=None), INV), (dict(sl=None), INV), (dict(out=None), INV), (dict(out=MIS), INV), (dict(q=MIS), INV),
     (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV), (dict(fmt=8), INV), (dict(h=48), INV),
-    (dict(rk=2), INV), (dict(hkv=0), INV), (dict(mode=3), INV), (dict(mode=-1), INV),
+    (dict(rk=2), INV), (dict(hkv=0), INV), (dict(mode=3), INV), (dict(mode=-1), INV), (dict(groups=65536), UNS),
     (dict(B=0), saw.SAW_OK),
 ])
 def test_prefix_refused(L, kw, expect):
