@@ -55,7 +55,9 @@
 //    this CTA attends over the rest, and the merge takes the prefix kernel's
 //    partials as further splits.  It is launched right behind that kernel and
 //    waits for it only when it merges, so its page copies overlap the other's
-//    tail.
+//    tail.  Short own parts are bound by a CTA's start and end and by issue:
+//    256 sequences of 64 to 1024 own tokens, 8 kv-heads, GQA 8 (163 MB), take
+//    about 67 of the call's 130 us.
 #include <type_traits>
 
 #include "saw_device.cuh"
