@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     // max_seq_len bounds the whole sequence here, max_own_len what follows
     // the prefix.  A length inside the prefix is an error (0: an idle row).
     bool bad = false;
-    pg = prefix_of_seq(p.prefix, seq, P, p.group, p.num_seqs, lane, &bad);
-    if (bad && seq == 0 && split == 0 && kvh == 0 && warp == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+    const bool reports = seq == 0 && split == 0 && kvh == 0;
+    pg = prefix_of_seq(p.prefix, seq, P, p.group, p.num_seqs, lane, reports, &bad);
+    if (bad && reports && warp == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     if (L < pg.tokens || L - pg.tokens > p.max_own_len) {
       if (L != 0 && split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
       pg.tokens = 0;

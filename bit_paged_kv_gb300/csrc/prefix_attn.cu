@@ -321,13 +321,12 @@ __device__ __forceinline__ bool rows_sync(bool ok) {
 
 struct __align__(16) Segment {
   int kvh;
-  int leader;        // the group's first sequence, whose table row is read
+  int first, end;    // the group's sequences
   int seq0, rows;    // first sequence of the block; its (sequence, head) rows (at most 128)
   int tile, tiles;   // key tiles of the prefix to do
   int tokens;        // tokens of the whole prefix
   int more;          // 0: no segment, the end
   int64_t slot;
-  int pad[2];
 };
 static_assert(sizeof(Segment) == 48, "kOffSeg");
 
@@ -424,7 +423,8 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Work& w, Seg
       const int per = prefix_seqs_per_block(p.group);
       s.kvh = int(u / uint32_t(g.blocks));
       const int blk = int(u - uint32_t(s.kvh) * g.blocks);
-      s.leader = g.first;
+      s.first = g.first;
+      s.end = g.end;
       s.seq0 = g.first + blk * per;
       s.rows = min(per, g.end - s.seq0) * p.group;
       s.tile = int(j * uint32_t(g.tiles) / per_unit);
@@ -868,8 +868,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
       __syncwarp();
       arrive_elect(&bars[kSegFull + e]);
       if (!more) break;
-      const int32_t* btab = p.block_tables + int64_t(sg.leader) * p.max_blocks;
-      const int n_pages = sg.tokens / P;
+      // the pages' ids from the table row of the group's first sequence that
+      // has the prefix (an idle row's may hold anything; none: nothing to read)
+      int reader = -1;
+      for (int s0 = sg.first; s0 < sg.end && reader < 0; s0 += 32) {
+        const uint32_t has = __ballot_sync(kAll, s0 + lane < sg.end && p.seq_lens[s0 + lane] >= sg.tokens);
+        if (has) reader = s0 + __ffs(has) - 1;
+      }
+      const int32_t* btab = p.block_tables + int64_t(max(reader, 0)) * p.max_blocks;
+      const int n_pages = reader < 0 ? 0 : sg.tokens / P;
       int ids = -1;
       for (int i = 0; i < sg.tiles; ++i, ++it) {
         const int st = it % kRawStages;

@@ -675,6 +675,7 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
     x.k_cache = p.k_cache;
     x.v_cache = p.v_cache;
     x.block_tables = block_tables;
+    x.seq_lens = seq_lens;
     x.prefix = p.prefix;
     x.dev_status = dev_status;
     x.max_blocks = max_blocks_per_seq;
@@ -804,6 +805,7 @@ int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double
       w = (1.0 - keep) * w / factor + keep * w;
     }
     const double t = w / two_pi;
+    if (!std::isfinite(t)) return SAW_ERR_INVALID_ARG;  // (a vanishing factor)
     p.turns[i] = uint64_t(std::ldexp(t - std::floor(t), 64));
   }
   p.att = att_scale > 0.0f ? att_scale : float(att);

@@ -143,6 +143,7 @@ struct PrefixParams {
   const uint8_t* k_cache;
   const uint8_t* v_cache;
   const int32_t* block_tables;  // [B][max_blocks]
+  const int32_t* seq_lens;      // [B]
   PrefixSide prefix;
   int32_t* dev_status;
   int32_t max_blocks;

@@ -89,15 +89,18 @@ __device__ __forceinline__ PrefixGroup prefix_from(const PrefixGroup& r, int lan
 }
 
 // Whole warp: the group that holds sequence `seq` (nothing shared if none does).
+// all: every group is looked at, for *bad.
 __device__ __forceinline__ PrefixGroup prefix_of_seq(const PrefixSide& s, int seq, int page_size, int group,
-                                                     int num_seqs, int lane, bool* bad) {
+                                                     int num_seqs, int lane, bool all, bool* bad) {
   int top = 0;
+  PrefixGroup mine{0, 0, 0, 0, 0, 0};
   for (int g0 = 0; g0 < s.num_groups; g0 += 32) {
     const PrefixGroup r = prefix_load(s, g0, page_size, group, num_seqs, lane, &top, bad);
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, r.first <= seq && seq < r.end);
-    if (hit) return prefix_from(r, __ffs(hit) - 1);
+    if (hit) mine = prefix_from(r, __ffs(hit) - 1);
+    if (hit && !all) break;
   }
-  return PrefixGroup{0, 0, 0, 0, 0, 0};
+  return mine;
 }
 
 // Partial results: slot s holds numerators as [32 groups of 4 dims][128

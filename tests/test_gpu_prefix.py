@@ -3,10 +3,11 @@ sequence over its own whole table (the definition: sharing changes nothing
 but what is read).
 
 Bar: max |o - o_ref| / max |o_ref| <= 2e-3 for a float32 output, the
-decode's.  The prefix pass rounds the rotated q, the dequantized K and V and
-p to binary16, 2^-12 of each value on average: for rows of N(0, 1) to
-Student-t entries that is below 1e-3 of a logit and of the output.  A 16-bit
-output adds its one rounding, at most half a step of the value: 2^-8 or 2^-11.
+decode's.  The prefix pass takes K's codes exactly and q in two binary16
+parts; it rounds the dequantized V and p to binary16 once each, at most 2^-11
+of each value and 2^-12 on average, in a weighted mean of V: below 2^-10 of the
+largest V.  A 16-bit output adds its one rounding, at most half a step of the
+value: 2^-8 or 2^-11.
 """
 import numpy as np
 import pytest
@@ -141,6 +142,26 @@ def test_sequences_that_end_with_the_prefix_and_idle_rows():
     s["lens"][7] = s["lens"][20] = 0
     out = check(s, "empty-own")
     assert (out[7] == 0).all() and (out[20] == 0).all()
+
+
+def test_idle_rows_may_hold_anything_in_their_tables():
+    """Groups whose first sequences (more than a warp's lanes of them), or all, are idle, with no page in their
+    table rows: as if they were not there."""
+    for sizes, idle in (([12], [0]), ([50], list(range(40))), ([6, 5, 9], [0, 1, 6, 7, 8, 9, 10, 19])):
+        s = setup(21, sizes, [272, 400, 160][:len(sizes)], np.arange(1, sum(sizes) + 1), hq=8, hkv=2)
+        s["lens"][idle] = 0
+        s["bt"][idle] = -1
+        out = check(s, "idle-first")
+        assert (out[idle] == 0).all()
+
+
+def test_bad_group_behind_many_is_reported():
+    s = setup(22, [2] * 40, [32] * 40, np.arange(1, 81), hq=8, hkv=2)
+    s["cu"], s["pre"] = np.append(s["cu"], 80), np.append(s["pre"], -1)
+    want = reference(s).reshape(80, 8, 128)
+    for mode in (SHARE, SEPARATE):
+        out, st = run(s, mode=mode)
+        assert st == saw.SAW_ERR_DEVICE_INDEX and rel_err(out.cpu().numpy(), want, "prefix-bad-last") <= ATTN_TOL
 
 
 def test_one_sequence_and_one_token():

@@ -57,6 +57,7 @@ def _rope_table(L, **kw):
     (dict(kind=saw.SAW_ROPE_YARN), INV), (dict(kind=saw.SAW_ROPE_BANDS, orig=-1), INV),
     (dict(kind=saw.SAW_ROPE_BANDS, orig=64, low=4.0, high=1.0), INV),
     (dict(kind=saw.SAW_ROPE_YARN, orig=64, low=0.0, high=1.0), INV),
+    (dict(kind=saw.SAW_ROPE_LINEAR, f=1e-320), INV),  # 1 / factor is infinite
     (dict(cs=None), INV), (dict(cs=MIS), INV), (dict(n=0), saw.SAW_OK),
 ])
 def test_rope_table_refused(L, kw, expect):
