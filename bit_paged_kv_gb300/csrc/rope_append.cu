@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const RopeTab
 // ------------------------------------------------------------ one row per warp
 //
 // Lane l holds elements E l .. E l + E - 1 (E = D / 32).  Any size, layout and
-// stride; the bulk kernel takes over for large batches.
+// stride; the bulk kernel takes over for large batches.  Bound by latency: one
+// token, 32 and 8 heads, 2.6 us, a launch and three dependent loads.
 constexpr int kRowWarps = 4;
 
 template <int D>
@@ -293,25 +294,30 @@ cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
 // Large batches.  Item = (token, part): up to kQPart q-heads, or the token's K
 // rows, or its V rows; every warp walks items on its own, so that the q parts
 // (pure traffic) and the K and V parts (150 or so instructions a row, which
-// alone would be bound by issue) of different warps share an SM.  Lane a of
-// the D / 16 that share a row holds its 16-byte chunks a and a + D / 16, dims 8
-// a .. + 7 and the same + D / 2: the (i, i + D/2) pairs of a whole-head rotary
-// sit in one lane, the butterfly's strides 1, 2, 4 and D / 2 too, and only 8 ..
-// D / 4 cross lanes.  The lane's cosines and sines serve all heads of the
-// token.
+// alone would be bound by issue) of different warps share an SM.  A lane holds
+// two 16-byte chunks (8 dims) of a row, D / 16 lanes share it.  The chunks lie
+// r / 2 dims apart where r / 16 is a power of two (else, and interleaved, D / 2
+// apart): the (i, i + r/2) pairs sit in one lane, the butterfly's strides 1, 2,
+// 4 and that one too, and only the others cross lanes.  The lane's cosines and
+// sines serve all heads of the token.
 //
-// Bound: HBM.  131072 tokens, Hq 32, Hkv 8, D 128: 2.90 GB, 426 us at the
-// measured copy rate.
+// Bound: HBM.  131072 tokens, Hq 32, Hkv 8, D 128: 2.90 GB in 484 us, 6.0 TB/s
+// (426 us at the measured copy rate); 2047 tokens, half the head turned (45
+// MB), 12.7 us, where a warp has an item or two and latency counts.
 constexpr int kBulkWarps = 8;
 constexpr int kRounds = 4;  // rounds of q-head loads in flight
-constexpr int64_t kBulkMinElems = int64_t(1) << 21;  // smaller batches: a warp per row
+// Smaller batches take a warp per row.  That against this kernel, us: 64
+// q-heads 96 tokens 3.5 / 3.7, 128 tokens 3.7 / 3.7, 160 tokens 4.6 / 3.7, 256
+// tokens 6.1 / 4.4; 32 q-heads, half the head turned, 64 tokens 2.8 / 4.9, 256
+// tokens 5.0 / 4.9, 512 tokens 8.2 / 5.6.
+constexpr int64_t kBulkMinElems = int64_t(5) << 18;
 constexpr int kQPart = 16;  // q-heads per item
+enum { kHalfWhole = 0, kHalfPart = 1, kInter = 2, kHalfBit = 3 };  // whole head; any part; -; r / 16 a power of two
 // CTAs per SM (85 or 128 registers a thread): 131072 tokens 484 us with three,
-// 527 with two; the layout that exchanges partners by shuffles keeps two (its
-// 2047-token case 14.4 us, 22.3 with three and spills).
-constexpr int bulk_ctas(int layout) { return layout == 1 ? 2 : 3; }
-
-enum { kHalfWhole = 0, kHalfPart = 1, kInter = 2 };
+// 527 with two; the layout that exchanges partners by shuffles keeps two (2047
+// tokens, half the head: 14.4 us, 22.3 with three and spills; by kHalfBit 12.7,
+// 8192 tokens 47.2 against 37.9).
+constexpr int bulk_ctas(int layout) { return layout == kHalfPart ? 2 : 3; }
 
 template <bool F16IN>
 __device__ __forceinline__ void widen8(const uint4& w, float* x) {
@@ -331,8 +337,8 @@ __device__ __forceinline__ uint4 narrow8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A lane's cosines and sines: of its pairs (kHalfWhole, 8), of its chunks' 2 x
-// 4 pairs (kInter), or of its chunks' 2 x 8 elements (kHalfPart).
+// A lane's cosines and sines: of its pairs (kHalfWhole, kHalfBit: 8), of its
+// chunks' 2 x 4 pairs (kInter), or of its chunks' 2 x 8 elements (kHalfPart).
 template <int LAYOUT>
 struct Angles {
   static constexpr int kN = LAYOUT == kHalfPart ? 16 : 8;
@@ -356,6 +362,8 @@ __device__ __forceinline__ void load_angles(Angles<LAYOUT>& t, const float* cs, 
   using N8 = std::integral_constant<int, 8>;
   if constexpr (LAYOUT == kHalfWhole) {
     run(0, 8 * a, N8{});
+  } else if constexpr (LAYOUT == kHalfBit) {  // (a: the lane's first chunk)
+    if (8 * a < half) run(0, 8 * a, N8{});
   } else {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -372,7 +380,8 @@ __device__ __forceinline__ void load_angles(Angles<LAYOUT>& t, const float* cs, 
 // (scalar sums: packed products and packed sums were fused by the assembler).
 template <int D, int LAYOUT>
 __device__ __forceinline__ void turn16(float (&x)[16], const Angles<LAYOUT>& t, int r, int a, int lane) {
-  if constexpr (LAYOUT == kHalfWhole) {
+  if constexpr (LAYOUT == kHalfWhole || LAYOUT == kHalfBit) {
+    if (LAYOUT == kHalfBit && 16 * a >= r) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float u = x[e], v = x[8 + e];
@@ -423,9 +432,10 @@ __device__ __forceinline__ void turn16(float (&x)[16], const Angles<LAYOUT>& t, 
 }
 
 // The row's butterfly (blocks of h, ascending strides), then the factor.
-// Sums with a partner lane as RN(+-x + o), the +-1 product exact.
+// Sums with a partner lane as RN(+-x + o), the +-1 product exact.  The lane's
+// two chunks are hc chunks apart.
 template <int D>
-__device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int lane) {
+__device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int hc, int lane) {
 #pragma unroll
   for (int s = 1; s < 8; s <<= 1) {  // (h >= 16)
 #pragma unroll
@@ -437,19 +447,20 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int l
       }
   }
 #pragma unroll
-  for (int s = 8; s < D / 2; s <<= 1) {
-    if (s < h) {
-      const float sign = (lane & (s >> 3)) ? -1.0f : 1.0f;
+  for (int s = 8; s < D; s <<= 1) {
+    if (s >= h) continue;
+    if (s == 8 * hc) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(x[i], sign, __shfl_xor_sync(kAll, x[i], s >> 3));
-    }
-  }
-  if (h == D) {
+      for (int i = 0; i < 8; ++i) {
+        const float a = x[i], b = x[i + 8];
+        x[i] = __fadd_rn(a, b);
+        x[i + 8] = __fsub_rn(a, b);
+      }
+    } else {
+      const int m = s < 8 * hc ? s >> 3 : s >> 4;
+      const float sign = (lane & m) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[i], b = x[i + 8];
-      x[i] = __fadd_rn(a, b);
-      x[i + 8] = __fsub_rn(a, b);
+      for (int i = 0; i < 16; ++i) x[i] = __fmaf_rn(x[i], sign, __shfl_xor_sync(kAll, x[i], m));
     }
   }
 #pragma unroll
@@ -488,7 +499,10 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
   pdl_wait_then_release();
   constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp
   const int lane = threadIdx.x & 31;
-  const int a = lane & (LPR - 1), sub = lane / LPR;
+  const int sub = lane / LPR;
+  // the lane's chunks are a and a + hc: its index with a zero put in at hc's bit
+  const int hc = LAYOUT == kHalfBit ? p.rope_dim >> 4 : LPR;
+  const int a = LAYOUT == kHalfBit ? ((lane & (LPR - 1) & -hc) << 1) | (lane & (hc - 1)) : lane & (LPR - 1);
   const int nq = (p.num_q_heads + kQPart - 1) / kQPart;
   const uint32_t parts = uint32_t(nq + p.num_tensors);
   const uint32_t items = uint32_t(p.num_tokens) * parts;
@@ -522,7 +536,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
           w[k][0] = w[k][1] = make_uint4(0u, 0u, 0u, 0u);
           if (h < h1) {
             w[k][0] = *reinterpret_cast<const uint4*>(src + h * D);
-            w[k][1] = *reinterpret_cast<const uint4*>(src + h * D + D / 2);
+            w[k][1] = *reinterpret_cast<const uint4*>(src + h * D + 8 * hc);
           }
         }
 #pragma unroll
@@ -535,7 +549,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
           turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
           if (h < h1) {
             *reinterpret_cast<uint4*>(dst + h * D) = narrow8<F16IN>(x);
-            *reinterpret_cast<uint4*>(dst + h * D + D / 2) = narrow8<F16IN>(x + 8);
+            *reinterpret_cast<uint4*>(dst + h * D + 8 * hc) = narrow8<F16IN>(x + 8);
           }
         }
       }
@@ -557,7 +571,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
     uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
     if (sub < hkv) {
       w0 = *reinterpret_cast<const uint4*>(src + sub * D);
-      w1 = *reinterpret_cast<const uint4*>(src + sub * D + D / 2);
+      w1 = *reinterpret_cast<const uint4*>(src + sub * D + 8 * hc);
     }
     Angles<LAYOUT> ang;
     if (tensor == 0) load_angles<D>(ang, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, a);
@@ -568,10 +582,10 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
       widen8<F16IN>(w1, x + 8);
       if (h + RPW < hkv) {  // the next rows, under way while these are worked on
         w0 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D);
-        w1 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D + D / 2);
+        w1 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D + 8 * hc);
       }
       if (tensor == 0) turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
-      if (rot) rotate16<D>(x, p.block_h, p.c_h, lane);
+      if (rot) rotate16<D>(x, p.block_h, p.c_h, hc, lane);
       float mn = fminf(x[0], x[1]), mx = fmaxf(x[0], x[1]);
 #pragma unroll
       for (int i = 2; i < 16; ++i) {
@@ -589,7 +603,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
         uint8_t* chunk = chunk0 + int64_t(h) * (P * (D / 2 + 4));
         uint32_t* codes = reinterpret_cast<uint32_t*>(chunk + off * (D / 2));
         codes[a] = c0;
-        codes[a + LPR] = c1;
+        codes[a + hc] = c1;
         if (a == 0)
           *reinterpret_cast<uint32_t*>(chunk + P * (D / 2) + 4 * off) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
       }
@@ -621,14 +635,18 @@ cudaError_t launch_bulk_l(const RopeParams& p, int sms, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_bulk(const RopeParams& p, int sms, cudaStream_t stream) {
-  const int layout = p.interleaved ? kInter : p.rope_dim == D ? kHalfWhole : kHalfPart;
-  if (p.in_f16)
-    return layout == kInter        ? launch_bulk_l<D, true, kInter>(p, sms, stream)
-           : layout == kHalfWhole  ? launch_bulk_l<D, true, kHalfWhole>(p, sms, stream)
-                                   : launch_bulk_l<D, true, kHalfPart>(p, sms, stream);
-  return layout == kInter       ? launch_bulk_l<D, false, kInter>(p, sms, stream)
-         : layout == kHalfWhole ? launch_bulk_l<D, false, kHalfWhole>(p, sms, stream)
-                                : launch_bulk_l<D, false, kHalfPart>(p, sms, stream);
+  const int hc = p.rope_dim >> 4;
+  const int layout = p.interleaved ? kInter : p.rope_dim == D ? kHalfWhole : hc & (hc - 1) ? kHalfPart : kHalfBit;
+  auto with = [&](auto f16) {
+    constexpr bool F = decltype(f16)::value;
+    switch (layout) {
+      case kInter: return launch_bulk_l<D, F, kInter>(p, sms, stream);
+      case kHalfWhole: return launch_bulk_l<D, F, kHalfWhole>(p, sms, stream);
+      case kHalfBit: return launch_bulk_l<D, F, kHalfBit>(p, sms, stream);
+      default: return launch_bulk_l<D, F, kHalfPart>(p, sms, stream);
+    }
+  };
+  return p.in_f16 ? with(std::true_type{}) : with(std::false_type{});
 }
 
 }  // namespace

@@ -209,6 +209,17 @@ def test_bulk(D, hkv, inter):
         check(*case, 16, True, True, h, inter, meta)
 
 
+@pytest.mark.parametrize("D,r", [(64, 16), (64, 32), (128, 16), (128, 32), (128, 64), (256, 16), (256, 64), (256, 128)])
+@pytest.mark.parametrize("h", [16, 32, 64, 128])
+def test_bulk_parts(D, r, h):
+    """Turned parts whose pairs lie a power of two chunks apart, each with every block of the butterfly."""
+    if h > D:
+        h = 256 if D == 256 else D
+    T = (5 << 18) // (13 * D) + 1
+    case = make(D + r + h, T, 7, 3, D, 16, r, torch.bfloat16)
+    check(*case, 16, True, h != 32, h, False, False)
+
+
 @pytest.mark.parametrize("T", [64, 3000])
 def test_padding_and_bad_entries(T):
     """Slot -1 appends nothing and turns q; a bad slot or position is skipped and reported."""
