@@ -493,7 +493,8 @@ int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double
  *               the first rope_dim elements of a head are turned.
  * interleaved   0: pair i is elements (i, i + rope_dim/2); 1: (2i, 2i + 1).
  * q_out         [num_tokens][num_q_heads][head_dim], token stride
- *               q_out_token_stride; may be q itself with the same stride.
+ *               q_out_token_stride; may be q itself with the same stride, and
+ *               must not overlap q, k or v otherwise.
  * Other arguments as saw_quantize_append_ex.  A slot of -1 appends nothing;
  * the token's q is turned all the same.
  *

@@ -144,6 +144,11 @@ def test_sequences_that_end_with_the_prefix_and_idle_rows():
     assert (out[7] == 0).all() and (out[20] == 0).all()
 
 
+def test_nothing_behind_the_prefix():
+    """Every sequence ends with its prefix: max_own_len 0."""
+    check(setup(23, [40, 3], [512, 128], [0] * 43, hq=8, hkv=2), "no-own")
+
+
 def test_idle_rows_may_hold_anything_in_their_tables():
     """Groups whose first sequences (more than a warp's lanes of them), or all, are idle, with no page in their
     table rows: as if they were not there."""
