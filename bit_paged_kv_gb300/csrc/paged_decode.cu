@@ -57,7 +57,7 @@
 //    waits for it only when it merges, so its page copies overlap the other's
 //    tail.  Short own parts are bound by a CTA's start and end and by issue:
 //    256 sequences of 64 to 1024 own tokens, 8 kv-heads, GQA 8 (163 MB), take
-//    about 67 of the call's 130 us.
+//    about 60 of the call's 123 us.
 #include <type_traits>
 
 #include "saw_device.cuh"
@@ -995,7 +995,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     // tile at a time: its accumulators leave no registers for a second
     // tile's operands)
     const int lim = clean ? min(n_full, new_i >= 0 ? new_i : n_my) : 0;
-    if constexpr (kStages == 4) {
+    // (SHARED with 4-warp CTAs, short own parts: without these copies of the
+    // step, instruction fetches being a third of what an issue waits for: 256
+    // sequences, GQA 8 / 4, own parts to 1024 tokens 123 / 86 us against 131 / 89,
+    // of 2048 186 / 189, of 4096 274 / 270)
+    if constexpr (SHARED && kWarps == 4) {
+    } else if constexpr (kStages == 4) {
       for (; i + 3 < lim; i += 4) {
         if (!step(I2{}, I0{}, i) || !step(I2{}, I2{}, i + 2)) {
           failed = true;
@@ -1216,7 +1221,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       return j < nt ? __ldcg(po + prefix_part_index(j - others) + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
-    constexpr int kBatch = 12 / kHeads;  // loads in flight per head
+    // loads in flight per head (twice and three times as many: 0.3 to 0.8 us more)
+    constexpr int kBatch = kWarps == 4 ? 2 : 4;
     float2 ml[kHeads];
     float4 v[kHeads][kBatch];  // every head's first loads before any is used
 #pragma unroll

@@ -144,6 +144,26 @@ def test_sequences_that_end_with_the_prefix_and_idle_rows():
     assert (out[7] == 0).all() and (out[20] == 0).all()
 
 
+@pytest.mark.parametrize("G,P", [(8, 16), (4, 64), (3, 32)])
+def test_many_sequences(G, P):
+    """More (sequence, kv-head) pairs than four per SM: the second pass in its smallest CTAs, own parts from nothing
+    to many turns of their rings, an unreadable page in one of them."""
+    rng = np.random.default_rng(G)
+    own = rng.integers(0, 900, 320)
+    own[:4] = 0, 1, 63, 64
+    s = setup(24, [300, 20], [256, 64], own, hq=2 * G, hkv=2, P=P)
+    check(s, f"many-G{G}-P{P}")
+    b = int(np.argmax(own[:300]))
+    bt, e = s["bt"].copy(), 256 // P + 1
+    bt[b, e] = -1
+    out, st = run(dict(s, bt=bt))
+    keep = [i for i in range(bt.shape[1]) if i != e]
+    ref = reference(s, bt=np.where(np.arange(320)[:, None] == b, np.pad(s["bt"][:, keep], ((0, 0), (0, 1))), s["bt"]),
+                    lens=np.where(np.arange(320) == b, s["lens"] - P, s["lens"]))
+    assert st == saw.SAW_ERR_DEVICE_INDEX
+    assert rel_err(out.cpu().numpy().reshape(-1, 128), ref, f"many-bad-G{G}-P{P}") <= ATTN_TOL
+
+
 def test_nothing_behind_the_prefix():
     """Every sequence ends with its prefix: max_own_len 0."""
     check(setup(23, [40, 3], [512, 128], [0] * 43, hq=8, hkv=2), "no-own")
