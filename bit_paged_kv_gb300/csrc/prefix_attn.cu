@@ -496,7 +496,9 @@ __device__ __forceinline__ uint4 dequant8_wide(uint32_t w, float s, float z) {
 }
 
 // Key n's 64 code bytes into an operand tile: dims 8u .. 8u+7 at u * 2048 +
-// n * 16.  widen(word) gives the 16 bytes.
+// n * 16.  widen(word) gives the 16 bytes.  kUnroll: V one piece at a time (the
+// instruction cache: 64 sequences behind 16384 tokens 65.5 us, 66.5 with four),
+// K four (it comes first: 37 behind five prompts 73.4 us, 77 with one).
 template <int kUnroll, typename Widen>
 __device__ __forceinline__ void expand_key(const uint8_t* codes, uint8_t* dst, int n, Widen widen) {
 #pragma unroll kUnroll
@@ -1004,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
           if (it >= 2 && !wait_parked(&bars[kPvDone + b], ((it >> 1) - 1) & 1, failed)) break;
           uint8_t* dst = smem + kOffV + b * kOpBytes;
           if (__all_sync(kAll, plain && ok))
-            expand_key<4>(codes, dst, n, [&](uint32_t x) { return dequant8(x, s, z); });
+            expand_key<1>(codes, dst, n, [&](uint32_t x) { return dequant8(x, s, z); });
           else  // (a key past the prefix or on a bad page: zeros, whatever lies there)
             expand_key<1>(codes, dst, n, [&](uint32_t x) {
               return ok ? dequant8_wide(x, sf, zf) : make_uint4(0u, 0u, 0u, 0u);
