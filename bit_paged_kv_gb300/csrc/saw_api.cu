@@ -575,14 +575,17 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
   const int64_t tiles = ceil_div(max_prefix_len, saw::kPrefixKeys);
   if (units * tiles > INT32_MAX) return SAW_ERR_UNSUPPORTED;
   // The prefix pass costs its launch, a part's start and end and the merge
-  // (10 us more than the decode alone) and 1.6 us per key tile of the fullest
-  // SM; without it the decode reads every sequence's copy, 32768 (token,
-  // kv-head) rows of K and V per us.  Both sides on GB300, Hq 32, Hkv 8, short
-  // own parts: 64 x 1024 tokens 23.0 against 22.0 us, 32 x 1024 20.6 / 11.6,
-  // 8 x 4096 20.6 / 13.6, 32 x 4096 24.1 / 27.7, 16 x 8192 24.2 / 39.7, 4 x
-  // 32768 35.6 / 35.6, 128 x 1024 in 40 groups 48.3 / 27.3.
-  const double apart = double(num_seqs) * max_prefix_len * num_kv_heads / 32768.0;
-  const double together = 10.0 + 1.6 * double(ceil_div(units * tiles, sms));
+  // (about 15 us more than the decode alone) and 1.2 us per key tile of the
+  // fullest SM; without it the decode reads every sequence's copy, 32768 (token,
+  // kv-head) rows of K and V per us, 25000 with more than 4 q-heads to one.
+  // Both sides on GB300, shared / apart, Hkv 8, GQA 4, own parts to 64 tokens:
+  // 16 x 4096 tokens 21.1 / 16.8 us, 16 x 8192 23.6 / 39.9, 32 x 2048 23.1 /
+  // 17.2, 32 x 4096 23.8 / 27.8, 64 x 1024 23.1 / 22.3 (GQA 8 25.3 / 28.5), 128 x
+  // 512 27.9 / 22.1, 256 x 256 37.5 / 31.2, 256 x 512 38.2 / 41.0, 4 x 32768 33.2 /
+  // 37.2, 64 x 2048 in 8 groups 21.8 / 24.2, 128 x 1024 in 40 groups 44.3 / 27.6.
+  const double apart = double(num_seqs) * max_prefix_len * num_kv_heads /
+                       (num_q_heads / num_kv_heads > 4 ? 25000.0 : 32768.0);
+  const double together = 15.0 + 1.2 * double(ceil_div(units * tiles, sms));
   const bool can_share = num_groups > 0 && num_seqs > 0 && max_prefix_len >= page_size;
   if (can_share && (mode == SAW_PREFIX_SHARE || (mode == SAW_PREFIX_AUTO && apart > together))) {
     p.ctas = int32_t(sms);
@@ -651,6 +654,14 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
                       workspace, workspace_bytes, 0, formats, dev_status);
   if (rc != SAW_OK || num_seqs == 0) return rc;
   if (out16) p.out16 = static_cast<uint16_t*>(out);
+  // Own parts of one short split: 4-warp CTAs when 8-warp ones would take a
+  // second wave, which costs another start and end.  Both, us, 64 sequences, 8
+  // kv-heads, GQA 4 behind 4096 tokens, own parts to 64 tokens 26.8 / 31.3, 512
+  // 31.0 / 34.7, 1024 38.0 / 39.7, 2048 49.4 / 45.8; GQA 8, 256 36.0 / 41.2, 1024
+  // 48.6 / 50.7.
+  if (p.num_splits == 1 && p.pages_per_split * page_size <= 1024 &&
+      int64_t(num_seqs) * num_kv_heads > 2 * int64_t(sm_count()))
+    p.warps = 4;
   p.max_blocks = max_blocks_per_seq;
   p.max_seq_len = int32_t(std::min<int64_t>(int64_t(max_prefix_len) + max_own_len,
                                             int64_t(max_blocks_per_seq) * page_size));
