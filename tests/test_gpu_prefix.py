@@ -351,6 +351,27 @@ def test_graph_replay_with_new_inputs_and_other_stream():
     assert rel_err(out.cpu().numpy().reshape(-1, 128), reference(t), "prefix-graph") <= ATTN_TOL
 
 
+def test_two_streams_at_once():
+    """Calls of different batches in flight on two streams, each with its own workspace."""
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()
+    sides = []
+    for seed, B, pre in ((25, 64, 2048), (26, 90, 800)):
+        s = setup(seed, [B], [pre], np.arange(1, B + 1) * 9, hq=32, hkv=8)
+        need = saw.saw_prefix_decode_workspace_bytes(B, 1, 32, 8, 128, 16, pre, s["max_own"], SHARE)
+        sides.append(dict(s=s, want=run(s)[0], args=[i32(s[k]) for k in ("bt", "lens", "cu", "pre")],
+                          ws=torch.zeros(need, dtype=torch.uint8, device="cuda"), stream=torch.cuda.Stream(),
+                          outs=[torch.empty(s["q"].shape, device="cuda") for _ in range(8)]))
+    torch.cuda.synchronize()
+    for i in range(8):
+        for x in sides:
+            s = x["s"]
+            saw.saw_prefix_decode_int4(s["q"], s["kc"], s["vc"], *x["args"], s["max_pre"], s["max_own"], 8, s["pages"],
+                                       16, True, True, 128, x["outs"][i], x["ws"], stream=x["stream"], mode=SHARE)
+    torch.cuda.synchronize()
+    for x in sides:
+        assert all(torch.equal(o, x["want"]) for o in x["outs"])
+
+
 def test_long_prefix():
     """One 100000-token prefix, page 64: offsets, many partials per row."""
     s = setup(18, [24], [100032], np.arange(1, 25) * 3, hq=8, hkv=2, P=64)
