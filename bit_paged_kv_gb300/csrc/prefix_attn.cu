@@ -39,6 +39,11 @@
 //          before tile i's P V, so that the softmax of tile i runs behind them
 // Latency, not any unit's rate, sets the pace: a set's softmax (2 warps per
 // scheduler) and the two products it waits for follow one another.
+// Measured (GB300): 64 sequences, 32 q-heads over 8, behind 16384 tokens, 2048
+// tiles on 152 SMs, 34 us: 1.3 us a tile (its three products alone 1.0), 9.7 us
+// from the start to the first score -- the plan, page ids, first copies and
+// first K tile one after the other, all of it code fetched cold -- and 1.1 us for
+// a part's results.
 // The softmax warps draw registers from the others (96 and 48 a thread).
 // The 512 tensor-memory columns hold two score tiles (the second one makes the
 // overlap), O, and q' hi and lo: the score products read only K from shared
