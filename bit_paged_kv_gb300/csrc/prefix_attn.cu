@@ -765,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
             const float to = g1 ? at : now[i];
             f[i] = ex2(now[i] - to);
             sh[i] = m[i] - to;
-            const float fl = ex2(sh[i]);
+            // (no l yet: the shift up to a first reference below -127 would be infinite, and 0 times it NaN)
+            const float fl = ex2(fminf(sh[i], 0.0f));
             l[i] = mul2(l[i], make_float2(fl, fl));
             m[i] = to;
             grow = grow || g1;

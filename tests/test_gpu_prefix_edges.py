@@ -1,0 +1,52 @@
+"""saw_prefix_decode_int4 where its arithmetic and its work list can go wrong:
+scores far below zero, unreadable pages at the start of a part, faint keys,
+lengths and groups that are refused next to good ones, own parts split over
+CTAs behind a prefix.
+
+Bar, where no other is derived at the test: the decode's, 2e-3 of the largest
+output against the oracle's float64.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_paged_kv_gb300 as saw
+import test_gpu_prefix as base
+from gpu_helpers import ATTN_TOL, rel_err
+from test_gpu_prefix import AUTO, SEPARATE, SHARE
+
+pytestmark = pytest.mark.gpu
+
+
+def append_rows(s, k=None, v=None):
+    """Overwrite every slot's K rows, or V rows, or both: k, v float [slots] (the row's 128 values alike)."""
+    wl, n = s["wl"], s["pages"] * s["wl"].page_size
+    for cache, x, rot in (("kc", k, wl.rotate_k), ("vc", v, wl.rotate_v)):
+        if x is not None:
+            rows = torch.as_tensor(x, device="cuda").bfloat16()[:, None, None].expand(n, wl.num_kv_heads, 128)
+            saw.saw_quantize_append(rows.contiguous(), None, torch.arange(n, device="cuda", dtype=torch.int32), s[cache],
+                                    None, s["pages"], wl.page_size, rot, False, wl.block_h)
+
+
+def slot_of(s, b, token):
+    P = s["wl"].page_size
+    return int(s["bt"][b, token // P]) * P + token % P
+
+
+def steps_down(s, seed, top, by, levels=16):
+    """Every slot's K row alike, and q all ones: scores -top, -(top + by), .. (natural, at sm_scale 1)."""
+    i = np.random.default_rng(seed).integers(0, levels, s["pages"] * s["wl"].page_size)
+    append_rows(s, k=-(top + by * i) / 128.0)
+    s["q"] = torch.ones_like(s["q"])
+
+
+@pytest.mark.parametrize("top", [32.0, 96.0, 128.0, 1024.0])
+def test_scores_far_below_zero(top):
+    """Every score of every tile is far below zero, past the exponents of binary32."""
+    s = base.setup(31, [40, 7], [1024, 384], np.arange(47) % 30 + 1, rk=False)
+    steps_down(s, 1, top, 2.0)
+    base.check(s, f"below-{top}", sm_scale=1.0)
+
+
