@@ -747,29 +747,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
         // before, and this tile moves it when its maximum outgrew it (the first
         // tile to its maximum).  Both are rare, so the scores above are taken
         // against the one known here, and shifted if it was not the last word.
+        // In rowm -inf says that no key has counted yet (unreadable pages may
+        // open a part); m is 0 then, and the row has neither l nor O.
         if (it > first) wait_all(&turn[par ^ 1], ((it - 1) >> 1) & 1, failed);
         float now[2];
-        bool move = it == first;
+        bool move = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          now[i] = it > first ? rowm[r2 + 8 * i] : 0.0f;
+          now[i] = it > first ? rowm[r2 + 8 * i] : -INFINITY;
           move = move || now[i] != m[i] || top[i] > 8.0f;
         }
         if (__any_sync(kAll, move)) {
           float f[2], sh[2];
-          bool grow = it == first;
+          bool grow = it == first, any[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float at = m[i] + top[i];  // this tile's maximum
-            const bool g1 = it == first ? top[i] > -INFINITY : at > now[i] + 8.0f;
-            const float to = g1 ? at : now[i];
-            f[i] = ex2(now[i] - to);
+            const bool g1 = at > now[i] + 8.0f;
+            const float to = g1 ? at : now[i] > -INFINITY ? now[i] : 0.0f;
+            // (nothing to scale yet: 1; the shift to a first reference below
+            // -127 would be infinite, and 0 times it NaN)
+            f[i] = now[i] > -INFINITY ? ex2(now[i] - to) : 1.0f;
             sh[i] = m[i] - to;
-            // (no l yet: the shift up to a first reference below -127 would be infinite, and 0 times it NaN)
             const float fl = ex2(fminf(sh[i], 0.0f));
             l[i] = mul2(l[i], make_float2(fl, fl));
             m[i] = to;
             grow = grow || g1;
+            any[i] = g1 || now[i] > -INFINITY;
           }
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
             }
             if (c == 0) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) rowm[r2 + 8 * i] = m[i];
+              for (int i = 0; i < 2; ++i) rowm[r2 + 8 * i] = any[i] ? m[i] : -INFINITY;
             }
           }
         }

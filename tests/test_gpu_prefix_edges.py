@@ -50,3 +50,25 @@ def test_scores_far_below_zero(top):
     base.check(s, f"below-{top}", sm_scale=1.0)
 
 
+@pytest.mark.parametrize("P", [64, 16])
+@pytest.mark.parametrize("top", [32.0, 128.0])
+@pytest.mark.parametrize("bad", [(0,), (0, 1), (0, 1, 2, 3, 4), (1,), (0, 2, 7), tuple(range(1, 8)), tuple(range(8))])
+def test_unreadable_tiles(P, top, bad):
+    """Tiles of 128 keys with no valid page id, at a part's start and elsewhere: their keys do not count, the others
+    do.  128 kv-heads: one part of all eight tiles each."""
+    own = np.array([5, 40, 17])
+    s = base.setup(32, [3], [1024], own, hq=128, hkv=128, P=P, rk=False)
+    steps_down(s, 2, top, 2.0)
+    per = 128 // P
+    gone = [t * per + i for t in bad for i in range(per)]
+    bt = s["bt"].copy()
+    bt[:, gone] = -1
+    out, st = base.run(dict(s, bt=bt), sm_scale=1.0)
+    keep = [e for e in range(bt.shape[1]) if e not in gone]
+    ref_bt = np.full_like(bt, -1)
+    ref_bt[:, :len(keep)] = s["bt"][:, keep]
+    ref = base.reference(s, sm_scale=1.0, bt=ref_bt, lens=s["lens"] - P * len(gone))
+    assert st == saw.SAW_ERR_DEVICE_INDEX
+    assert rel_err(out.cpu().numpy().reshape(-1, 128), ref, f"unreadable-{P}-{bad}") <= ATTN_TOL
+
+
