@@ -16,10 +16,13 @@
 // 65504, a score of thousands).  V^ = n s_V + z_V is dequantized and rounded once
 // to binary16 (no coarser than the 16-bit rows the cache was made from), p
 // too: O += P V^ in binary32, where sum(p s n) + sum(p z) would cancel.
-// Softmax in base 2 in binary32 with a running reference m that moves (and
-// rescales O and l) only when a row's maximum has outgrown it by more than
-// 2^8: p <= 2^8 stays far inside binary16, and the merge's normalisation makes
-// the choice of m invisible.
+// Softmax in base 2 in binary32 with a running reference m, set 7 below the
+// row's maximum, that moves (and rescales O and l) only when the maximum has
+// come to exceed it by more than 15: p <= 2^15 stays inside binary16, and the
+// merge's normalisation makes the choice of m invisible.  The 2^7 are for faint
+// keys: l counts p before its rounding, O after, and binary16 ends at 2^-24, so
+// a key counts in both down to 2^-32 of the row's heaviest (with m the maximum,
+// 2^-25: 100000 such keys would take 0.3 % from the output).
 //
 // Twenty-four warps, specialised:
 //   0-7, 8-15  softmax of even and odd tiles, run a tile apart so that one
@@ -98,6 +101,7 @@ enum { kRawFull = 0, kRawEmpty = kRawFull + kRawStages, kKFull = kRawEmpty + kRa
 constexpr int kOffTmem = kOffBar + kBars * 8;
 constexpr int kSmem = kOffTmem + 16;
 static_assert(kOffBar % 8 == 0 && kOffMeta % 16 == 0 && kOffM % 16 == 0 && kSmem <= 227 * 1024, "shared memory");
+constexpr float kRefBelow = 7.0f, kRefMost = 15.0f;  // a row's maximum above its reference
 constexpr uint32_t kColO = 256, kColQh = 384, kColQl = 448;
 
 // ------------------------------------------------------------ PTX pieces
@@ -755,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           now[i] = it > first ? rowm[r2 + 8 * i] : -INFINITY;
-          move = move || now[i] != m[i] || top[i] > 8.0f;
+          move = move || now[i] != m[i] || top[i] > kRefMost;
         }
         if (__any_sync(kAll, move)) {
           float f[2], sh[2];
@@ -763,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float at = m[i] + top[i];  // this tile's maximum
-            const bool g1 = at > now[i] + 8.0f;
-            const float to = g1 ? at : now[i] > -INFINITY ? now[i] : 0.0f;
+            const bool g1 = at > now[i] + kRefMost;
+            const float to = g1 ? at - kRefBelow : now[i] > -INFINITY ? now[i] : 0.0f;
             // (nothing to scale yet: 1; the shift to a first reference below
             // -127 would be infinite, and 0 times it NaN)
             f[i] = now[i] > -INFINITY ? ex2(now[i] - to) : 1.0f;

@@ -562,7 +562,9 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  * Arithmetic of the prefix pass: scores to about 2^-22 of their terms (codes
  * exact, q' in two binary16 parts; a |q'| whose product with the softmax scale
  * and log2 e exceeds 4094 saturates), dequantized V and p rounded once to
- * binary16 (V beyond +-65504 saturates), sums and softmax in binary32.
+ * binary16 (V beyond +-65504 saturates; p of 2^7 at the row's maximum, so a key
+ * fainter than 2^-32 of the heaviest adds to the denominator only), sums and
+ * softmax in binary32.
  *
  * A group with inconsistent entries is reported as SAW_ERR_DEVICE_INDEX and
  * shares nothing.  Other arguments and errors as saw_paged_decode_int4;

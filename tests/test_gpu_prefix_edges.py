@@ -72,3 +72,21 @@ def test_unreadable_tiles(P, top, bad):
     assert rel_err(out.cpu().numpy().reshape(-1, 128), ref, f"unreadable-{P}-{bad}") <= ATTN_TOL
 
 
+def test_faint_keys_count():
+    """One key of weight 1 and value 0, and n of weight w = 2^-25.2 and value 1: the output is n w / (1 + n w).
+    p is held as a binary16 of 2^7 times its weight, so a faint key is off by at most half a step of 2^-24, 2^-32 of
+    the first key's weight; what else rounds (the score 25.2 to 2^-19, the exponential to 2^-22, binary32 sums of
+    n / 16 terms at 2^-23 each) is below 2^-12 of the output together."""
+    s = base.setup(33, [3], [4096], np.array([1, 1, 1]), hq=128, hkv=128, rk=False, rv=False)
+    n = s["pages"] * 16
+    k, v = np.full(n, -1.0), np.ones(n)
+    k[slot_of(s, 0, 700)] = v[slot_of(s, 0, 700)] = 0.0
+    append_rows(s, k, v)
+    s["q"] = torch.ones_like(s["q"])
+    out, st = base.run(s, sm_scale=25.2 * math.log(2) / 128)
+    w = 4096 * 2.0 ** -25.2
+    want = w / (1 + w)
+    assert st == 0
+    assert np.abs(out.double().cpu().numpy() - want).max() <= 4096 * 2.0 ** -32 + want * 2.0 ** -12
+
+
