@@ -885,10 +885,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
       arrive_elect(&bars[kSegFull + e]);
       if (!more) break;
       // the pages' ids from the table row of the group's first sequence that
-      // has the prefix (an idle row's may hold anything; none: nothing to read)
+      // has the prefix and is served (the row of one that is idle or refused
+      // for its length may hold anything; none: nothing to read)
       int reader = -1;
       for (int s0 = sg.first; s0 < sg.end && reader < 0; s0 += 32) {
-        const uint32_t has = __ballot_sync(kAll, s0 + lane < sg.end && p.seq_lens[s0 + lane] >= sg.tokens);
+        const int len = s0 + lane < sg.end ? p.seq_lens[s0 + lane] : 0;
+        const uint32_t has = __ballot_sync(
+            kAll, len >= sg.tokens && len <= p.max_seq_len && len - sg.tokens <= p.max_own_len);
         if (has) reader = s0 + __ffs(has) - 1;
       }
       const int32_t* btab = p.block_tables + int64_t(max(reader, 0)) * p.max_blocks;

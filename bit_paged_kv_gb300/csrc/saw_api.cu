@@ -691,6 +691,8 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
     x.dev_status = dev_status;
     x.max_blocks = max_blocks_per_seq;
     x.num_seqs = num_seqs;
+    x.max_seq_len = p.max_seq_len;
+    x.max_own_len = max_own_len;
     x.num_q_heads = num_q_heads;
     x.num_kv_heads = num_kv_heads;
     x.group = p.group;

@@ -148,6 +148,8 @@ struct PrefixParams {
   int32_t* dev_status;
   int32_t max_blocks;
   int32_t num_seqs;
+  int32_t max_seq_len;          // bounds of a length that is served: whole,
+  int32_t max_own_len;          // and behind the prefix
   int32_t num_q_heads;
   int32_t num_kv_heads;
   int32_t group;

@@ -540,7 +540,7 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  *               (the rest of the last page is read per sequence).  The table
  *               rows of the group's sequences that reach that far hold the same
  *               ids there (the caller's contract; any of them may be the one
- *               read; an idle row may hold anything).
+ *               read; one that is idle or refused may hold anything).
  * seq_lens      device int32 [num_seqs]: all tokens, the prefix included.  0:
  *               an idle row, its output zero.  A length below the prefix's
  *               whole pages, beyond max_blocks_per_seq pages, or of more than

@@ -90,3 +90,17 @@ def test_faint_keys_count():
     assert np.abs(out.double().cpu().numpy() - want).max() <= 4096 * 2.0 ** -32 + want * 2.0 ** -12
 
 
+@pytest.mark.parametrize("length", [1 << 20, 512 + 200, 512 + 101, -3, 100])
+def test_refused_rows_are_not_read_for_the_others(length):
+    """A group's first sequence is refused for its length: its table row, which then may hold anything, is not the
+    one that the prefix is read through."""
+    s = base.setup(34, [20], [512], np.full(20, 100), hq=8, hkv=2)
+    ref = base.reference(s).reshape(20, 8, 128)
+    s["lens"][0] = length
+    s["bt"][0] = np.random.default_rng(0).permutation(s["pages"])[:s["bt"].shape[1]]
+    for mode in (SHARE, SEPARATE):
+        out, st = base.run(s, mode=mode)
+        assert st == saw.SAW_ERR_DEVICE_INDEX and (out[0] == 0).all()
+        assert rel_err(out[1:].cpu().numpy(), ref[1:], f"refused-{length}") <= ATTN_TOL
+
+
