@@ -42,7 +42,8 @@ __device__ __forceinline__ uint32_t warp_scan_u32(uint32_t v, int lane) {  // in
 // furthest end of the groups before g0, moves on.  A group whose entries are
 // inconsistent -- out of range, descending, or reaching back over an earlier
 // one, so that the others stay disjoint and their units within the workspace --
-// shares nothing; *bad is set in its lane.
+// shares nothing; *bad is set in its lane.  The ends of groups out of range or
+// descending do not count for the later ones.
 __device__ __forceinline__ PrefixGroup prefix_load(const PrefixSide& s, int g0, int page_size, int group,
                                                    int num_seqs, int lane, int* top, bool* bad) {
   const int g = g0 + lane;
@@ -53,7 +54,7 @@ __device__ __forceinline__ PrefixGroup prefix_load(const PrefixSide& s, int g0, 
     hi = s.cu_groups[g + 1];
     pre = s.prefix_lens[g];
   }
-  int reach = hi;  // furthest end up to this group
+  int reach = lo >= 0 && hi >= lo && hi <= num_seqs ? hi : 0;  // furthest end up to this group
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xFFFFFFFFu, reach, d);

@@ -104,3 +104,21 @@ def test_refused_rows_are_not_read_for_the_others(length):
         assert rel_err(out[1:].cpu().numpy(), ref[1:], f"refused-{length}") <= ATTN_TOL
 
 
+@pytest.mark.parametrize("entry", [1000, 41, -5, 5, 25])
+@pytest.mark.parametrize("generous", [False, True])
+def test_a_bad_group_between_good_ones(entry, generous):
+    """One wrong entry of cu_group_seqs: the groups it bounds share nothing, the others are as before."""
+    s = base.setup(35, [10] * 4, [512, 256, 384, 320], np.full(40, 20), hq=8, hkv=2)
+    ref = base.reference(s).reshape(40, 8, 128)
+    s["cu"][2] = entry
+    if generous:
+        s["max_own"] = 512 + 20
+    good = list(range(40)) if generous else list(range(10)) + list(range(30, 40))
+    if entry == 25:  # in range: the second group takes rows of the third, whose prefix is another
+        good = [b for b in good if not 20 <= b < 25]
+    for mode in (SHARE, SEPARATE):
+        out, st = base.run(s, mode=mode)
+        assert st == saw.SAW_ERR_DEVICE_INDEX or entry == 25
+        assert rel_err(out[good].cpu().numpy(), ref[good], f"bad-middle-{entry}") <= ATTN_TOL
+
+
