@@ -1210,15 +1210,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     const float2* pm = reinterpret_cast<const float2*>(p.prefix.part_ml) + slot * kPrefixRows + row0;
     const int others = merge_ok && !direct ? ns : 0;  // splits, this one among them
     const int nt = others + np;
-    // partial j of nt: a split's, or the prefix's
+    // partial j of nt: a split's, or the prefix's.  This split's own takes its
+    // place among the others', so that the sum does not depend on which split
+    // arrived last.
     auto load_ml = [&](int h, int64_t srow, int j) {
       if (j < others) return j != split ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + srow + j)
-                                        : make_float2(-INFINITY, 0.0f);
+                                        : make_float2(tot[2 * kMaxGroup + h], tot[h]);
       return j < nt ? __ldcg(pm + int64_t(j - others) * kPrefixRows + h) : make_float2(-INFINITY, 0.0f);
     };
-    auto load_o = [&](int h, int64_t srow, int j) {
-      if (j < others) return j != split ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (srow + j) * D) + lane)
-                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto load_o = [&](int h, int64_t srow, int j, const float4& own) {
+      if (j < others) return j != split ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (srow + j) * D) + lane) : own;
       return j < nt ? __ldcg(po + prefix_part_index(j - others) + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
     // loads in flight per head (twice and three times as many: 0.3 to 0.8 us more)
@@ -1233,7 +1234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       if (h < G) {
         ml[i] = load_ml(h, srow, lane);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) v[i][b] = load_o(h, srow, b);
+        for (int b = 0; b < kBatch; ++b) v[i][b] = load_o(h, srow, b, num[i]);
       }
     }
 #pragma unroll
@@ -1241,8 +1242,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const int h = warp + i * kWarps;
       if (h >= G) continue;
       const int64_t srow = (int64_t(seq) * p.num_q_heads + hq0 + h) * p.num_splits;
-      float M = tot[2 * kMaxGroup + h], den = tot[h];
-      float4 o = num[i];
+      float M = -INFINITY, den = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (others == 0) {
+        M = tot[2 * kMaxGroup + h];
+        den = tot[h];
+        o = num[i];
+      }
       for (int j0 = 0; j0 < nt; j0 += 32) {
         if (j0 > 0) ml[i] = load_ml(h, srow, j0 + lane);
         float Mn = fmaxf(M, ml[i].x);
@@ -1260,7 +1266,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         for (int b0 = 0; b0 < n; b0 += kBatch) {
           if (j0 + b0 > 0) {
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) v[i][b] = load_o(h, srow, j0 + b0 + b);
+            for (int b = 0; b < kBatch; ++b) v[i][b] = load_o(h, srow, j0 + b0 + b, num[i]);
           }
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {

@@ -122,3 +122,34 @@ def test_a_bad_group_between_good_ones(entry, generous):
         assert rel_err(out[good].cpu().numpy(), ref[good], f"bad-middle-{entry}") <= ATTN_TOL
 
 
+SPLIT = [
+    (6, 1, 2, 16, 5000, torch.float32), (6, 4, 2, 64, 9000, torch.bfloat16), (10, 8, 2, 32, 3000, torch.float32),
+    (3, 7, 1, 16, 20000, torch.float32), (20, 4, 8, 16, 2500, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("B,G,hkv,P,longest,dt", SPLIT)
+def test_own_parts_split_over_ctas(B, G, hkv, P, longest, dt):
+    """Own parts of several splits each behind shared prefixes: none, one token, and up to the longest; an idle row;
+    two groups and a sequence in none."""
+    own = np.random.default_rng(B).integers(1, longest, B)
+    own[:3] = longest, 0, 1
+    s = base.setup(B, [B - 1, 1], [640, 192], own, hq=G * hkv, hkv=hkv, P=P)
+    assert saw.saw_decode_plan(B, hkv, P, s["max_own"])[0] > 1
+    base.check(s, f"split-{B}-{G}-{P}", dt)
+    s["cu"], s["pre"] = s["cu"][:2], s["pre"][:1]
+    s["lens"][1] = 0
+    base.check(s, f"split-idle-{B}-{G}-{P}", dt)
+
+
+@pytest.mark.parametrize("mode", [SHARE, SEPARATE])
+def test_split_own_parts_repeat_bit_for_bit(mode):
+    """Whichever split of a sequence ends last, the same sum: 200 calls, one result."""
+    s = base.setup(37, [8], [1024], np.random.default_rng(3).integers(2000, 9000, 8), hq=8, hkv=2)
+    assert saw.saw_decode_plan(8, 2, 16, s["max_own"])[0] > 2
+    need = saw.saw_prefix_decode_workspace_bytes(8, 1, 8, 2, 128, 16, s["max_pre"], s["max_own"], mode)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    first, st = base.run(s, ws=ws, mode=mode)
+    assert st == 0
+    differ = sum(not torch.equal(base.run(s, ws=ws, mode=mode)[0], first) for _ in range(200))
+    assert differ == 0
