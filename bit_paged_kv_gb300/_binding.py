@@ -368,7 +368,8 @@ def _bind_step():
     m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_saw_step", loader))
     loader.exec_module(m)
     at = [C.cast(getattr(L, f), C.c_void_p).value
-          for f in ("saw_build_tables", "saw_rope_table", "saw_rope_append", "saw_prefix_decode_int4")]
+          for f in ("saw_build_tables", "saw_rope_table", "saw_rope_append", "saw_prefix_decode_int4",
+                    "saw_cache_bytes")]
     m.init(*at, torch.int32, torch.float32, torch.bfloat16, torch.float16,
            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
            getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream))

@@ -5,9 +5,10 @@
 //
 // These calls run once or more per layer on small batches, where the host's
 // share of a call is what a user of eager steps waits for.  A rotary append of
-// one token takes 5.3 us of a Grace core here, 2 of them the launch; through
-// ctypes, with the checks in Python, 9.7 us (2 for the conversion of its 28
-// arguments).
+// one token takes 6.0 us of a Grace core here, 2 of them the launch and 0.7 the
+// checks that every tensor is on the call's device and the caches are as large
+// as its counts say; through ctypes, with fewer checks, in Python, 9.7 us (2
+// for the conversion of its 28 arguments).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -22,11 +23,12 @@ struct Entry {
   decltype(&saw_rope_table) rope_table;
   decltype(&saw_rope_append) rope_append;
   decltype(&saw_prefix_decode_int4) prefix_decode;
+  decltype(&saw_cache_bytes) cache_bytes;
 } g_entry;
 PyObject *g_int32, *g_f32, *g_bf16, *g_f16;     // dtypes
 PyObject *g_device, *g_raw_stream;              // current device; its current stream
 PyObject *n_dtype, *n_data_ptr, *n_contiguous, *n_numel, *n_shape, *n_stride, *n_get_device,
-    *n_cuda_stream, *n_element_size;
+    *n_cuda_stream, *n_nbytes;
 
 // Every helper returns false with a Python exception set.
 
@@ -80,13 +82,20 @@ bool entries(PyObject* tuple, const char* what, int n, int64_t* out) {
 bool shape(PyObject* t, const char* what, int n, int64_t* out) {
   return entries(PyObject_GetAttr(t, n_shape), what, n, out);
 }
-// Contiguous int32 of n entries (any number for n < 0; `size` may take it).
-bool words(PyObject* t, const char* what, int64_t n, int32_t** out, int64_t* size = nullptr) {
+// Every tensor has to be on the call's device: the kernels take it by address.
+bool on_device(PyObject* t, const char* what, int64_t dev) {
+  int64_t at;
+  if (!call_i64(t, n_get_device, &at)) return false;
+  if (at != dev) PyErr_Format(PyExc_ValueError, "%s must be on cuda:%lld", what, (long long)dev);
+  return at == dev;
+}
+// Contiguous int32 on the device, of n entries (any number for n < 0; `size` may take it).
+bool words(PyObject* t, const char* what, int64_t dev, int64_t n, int32_t** out, int64_t* size = nullptr) {
   *out = nullptr;
   if (size) *size = 0;
   if (t == Py_None) return true;
   bool type, cont;
-  if (!has_dtype(t, g_int32, &type) || !contiguous(t, &cont)) return false;
+  if (!on_device(t, what, dev) || !has_dtype(t, g_int32, &type) || !contiguous(t, &cont)) return false;
   if (!type || !cont) {
     PyErr_Format(PyExc_ValueError, "%s must be contiguous int32", what);
     return false;
@@ -104,6 +113,35 @@ bool words(PyObject* t, const char* what, int64_t n, int32_t** out, int64_t* siz
   if (!address(t, &p)) return false;
   *out = as<int32_t>(p);
   return true;
+}
+// The status word (one entry or more), or None.
+bool status_word(PyObject* t, int64_t dev, int32_t** out) {
+  int64_t n;
+  if (!words(t, "dev_status", dev, -1, out, &n)) return false;
+  if (t != Py_None && n < 1) PyErr_SetString(PyExc_ValueError, "dev_status must have an entry");
+  return t == Py_None || n >= 1;
+}
+// Contiguous memory of any type on the device, of `need` bytes or more (None:
+// null, for the library to judge).
+bool memory(PyObject* t, const char* what, int64_t dev, size_t need, void** out, int64_t* size = nullptr) {
+  bool cont;
+  *out = nullptr;
+  if (t == Py_None) return true;
+  if (!on_device(t, what, dev) || !contiguous(t, &cont) || !address(t, out)) return false;
+  if (!cont) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous", what);
+    return false;
+  }
+  PyObject* r = PyObject_GetAttr(t, n_nbytes);
+  if (!r) return false;
+  const int64_t have = PyLong_AsLongLong(r);
+  Py_DECREF(r);
+  if (have == -1 && PyErr_Occurred()) return false;
+  if (size) *size = have;
+  if (uint64_t(have) < need)
+    PyErr_Format(PyExc_ValueError, "%s must have %llu bytes, not %lld", what, (unsigned long long)need,
+                 (long long)have);
+  return uint64_t(have) >= need;
 }
 bool int32_of(PyObject* o, int32_t* out) {
   const long v = PyLong_AsLong(o);
@@ -182,11 +220,11 @@ struct Rows {
   void* p = nullptr;
   int64_t heads = 0, stride = 0;
 };
-bool rows_of(PyObject* t, PyObject* dtype, int64_t T, int64_t D, const char* what, Rows* out) {
+bool rows_of(PyObject* t, PyObject* dtype, int64_t dev, int64_t T, int64_t D, const char* what, Rows* out) {
   int64_t n[3], s[3];
   bool type;
-  if (!shape(t, what, 3, n) || !entries(PyObject_CallMethodNoArgs(t, n_stride), what, 3, s) ||
-      !has_dtype(t, dtype, &type) || !address(t, &out->p))
+  if (!on_device(t, what, dev) || !shape(t, what, 3, n) ||
+      !entries(PyObject_CallMethodNoArgs(t, n_stride), what, 3, s) || !has_dtype(t, dtype, &type) || !address(t, &out->p))
     return false;
   if (!type || n[0] != T || n[2] != D || s[2] != 1 || (s[1] != D && n[1] != 1)) {
     PyErr_Format(PyExc_ValueError, "%s must be [%lld, heads, %lld] rows of k's type, each token's contiguous", what,
@@ -198,9 +236,9 @@ bool rows_of(PyObject* t, PyObject* dtype, int64_t T, int64_t D, const char* wha
   out->stride = T > 1 ? s[0] : n[1] * D;
   return true;
 }
-bool f32_table(PyObject* t, const char* what, int64_t* dims, void** out) {
+bool f32_table(PyObject* t, const char* what, int64_t dev, int64_t* dims, void** out) {
   bool type, cont;
-  if (!has_dtype(t, g_f32, &type) || !contiguous(t, &cont)) return false;
+  if (!on_device(t, what, dev) || !has_dtype(t, g_f32, &type) || !contiguous(t, &cont)) return false;
   if (!type || !cont) {
     PyErr_Format(PyExc_ValueError, "%s must be contiguous float32 [max_pos, rope_dim]", what);
     return false;
@@ -229,20 +267,20 @@ PyObject* build_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
       *status;
   int32_t page_size, num_pages, nb, nt, nf, nr, ns, width;
   void* stream;
-  if (!on_current(a[1], &dev) || !words(a[1], "new_lens", -1, &fresh, &B) ||
-      !words(a[9], "slot_mapping", -1, &slots, &tokens) || !shape(a[6], "block_tables", 2, dst))
+  if (!on_current(a[1], &dev) || !words(a[1], "new_lens", dev, -1, &fresh, &B) ||
+      !words(a[9], "slot_mapping", dev, -1, &slots, &tokens) || !shape(a[6], "block_tables", 2, dst))
     return nullptr;
   if (dst[0] != B) {
     PyErr_Format(PyExc_ValueError, "block_tables must have %lld rows, not %lld", (long long)B, (long long)dst[0]);
     return nullptr;
   }
   if (a[12] != Py_None && !shape(a[12], "src_tables", 2, src)) return nullptr;
-  if (!words(a[0], "cached_lens", B, &cached) || !words(a[2], "free_pages", -1, &free_pages, &frees) ||
-      !words(a[3], "num_free", 1, &num_free) || !int32_of(a[4], &page_size) || !int32_of(a[5], &num_pages) ||
-      !words(a[6], "block_tables", -1, &tables) || !words(a[7], "seq_lens", B, &seq_lens) ||
-      !words(a[8], "cu_q_lens", B + 1, &cu) || !words(a[10], "positions", tokens, &positions) ||
-      !words(a[11], "pages_taken", 1, &taken) || !words(a[12], "src_tables", -1, &from) ||
-      !words(a[13], "src_rows", B, &from_rows) || !words(a[14], "dev_status", -1, &status) ||
+  if (!words(a[0], "cached_lens", dev, B, &cached) || !words(a[2], "free_pages", dev, -1, &free_pages, &frees) ||
+      !words(a[3], "num_free", dev, 1, &num_free) || !int32_of(a[4], &page_size) || !int32_of(a[5], &num_pages) ||
+      !words(a[6], "block_tables", dev, -1, &tables) || !words(a[7], "seq_lens", dev, B, &seq_lens) ||
+      !words(a[8], "cu_q_lens", dev, B + 1, &cu) || !words(a[10], "positions", dev, tokens, &positions) ||
+      !words(a[11], "pages_taken", dev, 1, &taken) || !words(a[12], "src_tables", dev, -1, &from) ||
+      !words(a[13], "src_rows", dev, B, &from_rows) || !status_word(a[14], dev, &status) ||
       !stream_of(a[15], dev, &stream) || !size32(B, &nb) || !size32(tokens, &nt) || !size32(frees, &nf) ||
       !size32(src[0], &nr) || !size32(src[1], &ns) || !size32(dst[1], &width))
     return nullptr;
@@ -258,7 +296,7 @@ PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int32_t max_pos, rope_dim, scaling, orig;
   double base, factor, low, high, att;
   void *p, *stream;
-  if (!on_current(a[0], &dev) || !f32_table(a[0], "cos_sin", dims, &p) || !size32(dims[0], &max_pos) ||
+  if (!on_current(a[0], &dev) || !f32_table(a[0], "cos_sin", dev, dims, &p) || !size32(dims[0], &max_pos) ||
       !size32(dims[1], &rope_dim) || !real_of(a[1], &base) || !int32_of(a[2], &scaling) || !real_of(a[3], &factor) ||
       !int32_of(a[4], &orig) || !real_of(a[5], &low) || !real_of(a[6], &high) || !real_of(a[7], &att) ||
       !stream_of(a[8], dev, &stream))
@@ -279,9 +317,11 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void *cos_sin, *kc, *vc = nullptr, *stream;
   if (!on_current(k, &dev) || !shape(k, "k", 3, dims) || !formats_of(k, a[17], &formats)) return nullptr;
   PyObject* dtype = (formats & SAW_FMT_F16_INPUT) ? g_f16 : g_bf16;
-  if (!rows_of(k, dtype, dims[0], dims[2], "k", &rk) || !f32_table(a[4], "cos_sin", table, &cos_sin)) return nullptr;
+  if (!rows_of(k, dtype, dev, dims[0], dims[2], "k", &rk) || !f32_table(a[4], "cos_sin", dev, table, &cos_sin))
+    return nullptr;
   if (q != Py_None) {
-    if (!rows_of(q, dtype, dims[0], dims[2], "q", &rq) || !rows_of(a[6], dtype, dims[0], dims[2], "q_out", &ro))
+    if (!rows_of(q, dtype, dev, dims[0], dims[2], "q", &rq) ||
+        !rows_of(a[6], dtype, dev, dims[0], dims[2], "q_out", &ro))
       return nullptr;
     if (rq.heads != ro.heads) {
       PyErr_SetString(PyExc_ValueError, "q_out must have q's heads");
@@ -289,18 +329,21 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   if (v != Py_None) {
-    if (!rows_of(v, dtype, dims[0], dims[2], "v", &rv) || !address(a[8], &vc)) return nullptr;
+    if (!rows_of(v, dtype, dev, dims[0], dims[2], "v", &rv)) return nullptr;
     if (rv.heads != rk.heads) {
       PyErr_SetString(PyExc_ValueError, "v must have k's heads");
       return nullptr;
     }
   }
-  if (!words(a[3], "positions", dims[0], &positions) || !words(a[5], "slot_mapping", dims[0], &slots) ||
-      !address(a[7], &kc) || !int32_of(a[9], &num_pages) || !int32_of(a[10], &page_size) || !flag_of(a[11], &rot_k) ||
+  if (!words(a[3], "positions", dev, dims[0], &positions) || !words(a[5], "slot_mapping", dev, dims[0], &slots) ||
+      !int32_of(a[9], &num_pages) || !int32_of(a[10], &page_size) || !flag_of(a[11], &rot_k) ||
       !flag_of(a[12], &rot_v) || !int32_of(a[13], &h) || !flag_of(a[14], &inter) ||
-      !words(a[15], "dev_status", -1, &status) || !stream_of(a[16], dev, &stream) || !size32(dims[0], &T) ||
+      !status_word(a[15], dev, &status) || !stream_of(a[16], dev, &stream) || !size32(dims[0], &T) ||
       !size32(dims[2], &D) || !size32(rq.heads, &hq) || !size32(rk.heads, &hkv) || !size32(table[0], &max_pos) ||
       !size32(table[1], &rope_dim))
+    return nullptr;
+  const size_t need = g_entry.cache_bytes(num_pages, page_size, hkv, D);
+  if (!memory(a[7], "k_cache", dev, need, &kc) || (v != Py_None && !memory(a[8], "v_cache", dev, need, &vc)))
     return nullptr;
   return status_of([&] {
     return g_entry.rope_append(rq.p, rq.stride, rk.p, rk.stride, rv.p, rv.stride, positions, as<float>(cos_sin),
@@ -312,14 +355,14 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 22)) return nullptr;
   PyObject *q = a[0], *out = a[15], *ws = a[16];
-  int64_t dev, dims[3], od[3], td[2], groups, bytes = 0, each;
+  int64_t dev, dims[3], od[3], td[2], groups, bytes = 0;
   int32_t *tables, *seq_lens, *cu, *prefix, *status;
   int32_t max_prefix, max_own, hkv, num_pages, page_size, rot_k, rot_v, h, mode, formats, B, hq, D, G, width;
   double scale;
   void *pq, *kc, *vc, *po, *pw, *stream;
   bool cq, co, same, f32;
   if (!on_current(q, &dev) || !shape(q, "q", 3, dims) || !formats_of(q, a[20], &formats) ||
-      !shape(out, "out", 3, od) || !contiguous(q, &cq) || !contiguous(out, &co) ||
+      !on_device(out, "out", dev) || !shape(out, "out", 3, od) || !contiguous(q, &cq) || !contiguous(out, &co) ||
       !has_dtype(out, (formats & SAW_FMT_F16_INPUT) ? g_f16 : g_bf16, &same) || !has_dtype(out, g_f32, &f32))
     return nullptr;
   if (!same && !f32) {
@@ -336,20 +379,18 @@ PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_Format(PyExc_ValueError, "block_tables must have %lld rows, not %lld", (long long)dims[0], (long long)td[0]);
     return nullptr;
   }
-  if (ws != Py_None) {
-    if (!call_i64(ws, n_numel, &bytes) || !call_i64(ws, n_element_size, &each)) return nullptr;
-    bytes *= each;
-  }
-  if (!words(a[3], "block_tables", -1, &tables) || !words(a[4], "seq_lens", dims[0], &seq_lens) ||
-      !words(a[6], "prefix_lens", -1, &prefix, &groups) || !words(a[5], "cu_group_seqs", groups + 1, &cu) ||
+  if (!memory(ws, "workspace", dev, 0, &pw, &bytes)) return nullptr;
+  if (!words(a[3], "block_tables", dev, -1, &tables) || !words(a[4], "seq_lens", dev, dims[0], &seq_lens) ||
+      !words(a[6], "prefix_lens", dev, -1, &prefix, &groups) || !words(a[5], "cu_group_seqs", dev, groups + 1, &cu) ||
       !int32_of(a[7], &max_prefix) || !int32_of(a[8], &max_own) || !int32_of(a[9], &hkv) ||
       !int32_of(a[10], &num_pages) || !int32_of(a[11], &page_size) || !flag_of(a[12], &rot_k) ||
       !flag_of(a[13], &rot_v) || !int32_of(a[14], &h) || !real_of(a[17], &scale) ||
-      !words(a[18], "dev_status", -1, &status) || !stream_of(a[19], dev, &stream) || !int32_of(a[21], &mode) ||
-      !address(q, &pq) || !address(a[1], &kc) || !address(a[2], &vc) || !address(out, &po) || !address(ws, &pw) ||
-      !size32(dims[0], &B) || !size32(dims[1], &hq) || !size32(dims[2], &D) || !size32(groups, &G) ||
-      !size32(td[1], &width))
+      !status_word(a[18], dev, &status) || !stream_of(a[19], dev, &stream) || !int32_of(a[21], &mode) ||
+      !address(q, &pq) || !address(out, &po) || !size32(dims[0], &B) || !size32(dims[1], &hq) ||
+      !size32(dims[2], &D) || !size32(groups, &G) || !size32(td[1], &width))
     return nullptr;
+  const size_t need = g_entry.cache_bytes(num_pages, page_size, hkv, D);
+  if (!memory(a[1], "k_cache", dev, need, &kc) || !memory(a[2], "v_cache", dev, need, &vc)) return nullptr;
   return status_of([&] {
     return g_entry.prefix_decode(pq, kc, vc, tables, width, seq_lens, cu, prefix, G, B, max_prefix, max_own, hq, hkv, D,
                                  num_pages, page_size, rot_k, rot_v, h, float(scale), po, pw, size_t(bytes), mode,
@@ -357,20 +398,21 @@ PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (four entry points' addresses; dtypes int32, float32, bfloat16, float16;
+// (five entry points' addresses; dtypes int32, float32, bfloat16, float16;
 // current device; current raw stream of a device)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 10)) return nullptr;
-  uint64_t at[4];
-  for (int i = 0; i < 4; ++i) {
+  if (!count(n, 11)) return nullptr;
+  uint64_t at[5];
+  for (int i = 0; i < 5; ++i) {
     at[i] = PyLong_AsUnsignedLongLong(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
   g_entry = {reinterpret_cast<decltype(Entry::build_tables)>(at[0]), reinterpret_cast<decltype(Entry::rope_table)>(at[1]),
              reinterpret_cast<decltype(Entry::rope_append)>(at[2]),
-             reinterpret_cast<decltype(Entry::prefix_decode)>(at[3])};
+             reinterpret_cast<decltype(Entry::prefix_decode)>(at[3]),
+             reinterpret_cast<decltype(Entry::cache_bytes)>(at[4])};
   PyObject** const keep[6] = {&g_int32, &g_f32, &g_bf16, &g_f16, &g_device, &g_raw_stream};
-  for (int i = 0; i < 6; ++i) Py_XSETREF(*keep[i], Py_NewRef(a[4 + i]));
+  for (int i = 0; i < 6; ++i) Py_XSETREF(*keep[i], Py_NewRef(a[5 + i]));
   Py_RETURN_NONE;
 }
 
@@ -391,7 +433,7 @@ PyMODINIT_FUNC PyInit__saw_step(void) {
     const char* name;
   } const names[] = {{&n_dtype, "dtype"},   {&n_data_ptr, "data_ptr"},     {&n_contiguous, "is_contiguous"},
                      {&n_numel, "numel"},   {&n_shape, "shape"},           {&n_stride, "stride"},
-                     {&n_get_device, "get_device"}, {&n_cuda_stream, "cuda_stream"}, {&n_element_size, "element_size"}};
+                     {&n_get_device, "get_device"}, {&n_cuda_stream, "cuda_stream"}, {&n_nbytes, "nbytes"}};
   for (const auto& x : names)
     if (!(*x.at = PyUnicode_InternFromString(x.name))) return nullptr;
   return PyModule_Create(&g_module);
