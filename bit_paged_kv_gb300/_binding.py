@@ -361,9 +361,10 @@ def _bind_step():
     not been built)."""
     global _step
     L = lib()
-    path = os.path.join(HERE, "_build", "_saw_step.so")
+    path = os.path.join(HERE, "_build", "_saw_step" + importlib.machinery.EXTENSION_SUFFIXES[0])
     if not os.path.exists(path):
-        raise RuntimeError(f"{path} not found; build it with `python bit_paged_kv_gb300/build.py`")
+        raise RuntimeError(f"{path} not found; build it with `python bit_paged_kv_gb300/build.py` (it needs this "
+                           "interpreter's headers and a C++ compiler)")
     loader = importlib.machinery.ExtensionFileLoader("_saw_step", path)
     m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_saw_step", loader))
     loader.exec_module(m)

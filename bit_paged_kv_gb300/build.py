@@ -2,13 +2,16 @@
 
 Each translation unit is compiled for sm_103a only (one -gencode), in
 parallel, then linked into one shared library exporting the C ABI of
-include/saw_int4.h.  Beside it goes _saw_step.so, a small CPython extension
-through which Python makes the serving step's calls.  No torch headers are
-involved.
+include/saw_int4.h.  Beside it goes _saw_step, a small CPython extension
+through which Python makes the serving step's calls, under the interpreter's
+own suffix; where the interpreter has no headers it is left out, and only
+those calls are missing.  No torch headers are involved.
 """
 from __future__ import annotations
 
+import importlib.machinery
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -20,7 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsaw_int4.so")
-STEP = os.path.join(OUT_DIR, "_saw_step.so")
+STEP = os.path.join(OUT_DIR, "_saw_step" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -67,10 +70,38 @@ def _deps() -> list[str]:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.exists(STEP):
-        newest = max(os.path.getmtime(f) for f in _deps())
-        if min(os.path.getmtime(LIB), os.path.getmtime(STEP)) >= newest:
-            return LIB
+    newest = max(os.path.getmtime(f) for f in _deps())
+
+    def fresh(path: str) -> bool:
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= newest
+
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        step = None if fresh(STEP) else ex.submit(_build_step)
+        if not fresh(LIB):
+            _build_lib(verbose)
+        if step is not None:
+            step.result()  # (the library is there whatever became of the extension)
+    return LIB
+
+
+def _build_step() -> None:
+    headers = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(headers, "Python.h")) or not shutil.which("g++"):
+        if os.path.exists(STEP):
+            os.remove(STEP)  # of older sources
+        sys.stderr.write(f"_saw_step is not built: no Python.h in {headers}, or no g++; the serving step's calls are "
+                         "missing from Python\n")
+        return
+    tmp = STEP + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", headers,
+           os.path.join(CSRC, "step_binding.cpp"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for step_binding.cpp:\n{r.stderr}")
+    os.replace(tmp, STEP)
+
+
+def _build_lib(verbose: bool) -> None:
     nvcc = _nvcc()
 
     def compile_one(unit) -> str:
@@ -86,25 +117,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    def compile_step() -> None:
-        tmp = STEP + f".tmp{os.getpid()}"
-        cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I",
-               sysconfig.get_paths()["include"], os.path.join(CSRC, "step_binding.cpp"), "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for step_binding.cpp:\n{r.stderr}")
-        os.replace(tmp, STEP)
-
-    with ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
-        step = ex.submit(compile_step)
+    with ThreadPoolExecutor(max_workers=len(UNITS)) as ex:
         objs = list(ex.map(compile_one, UNITS))
-        step.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
