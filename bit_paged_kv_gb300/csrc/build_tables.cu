@@ -349,12 +349,17 @@ __global__ void __launch_bounds__(kTabMaxThreads) build_tables_kernel(const Tabl
 cudaError_t launch_build_tables(const TablesParams& p, int sms, cudaStream_t stream) {
   const int unit = p.num_seqs <= kDirect ? 1 : kGroup;
   const int units = (p.num_seqs + unit - 1) / unit;
-  const int padded = units + units / 32 + 1;
-  const size_t smem = (size_t(2) * (units + 1) + (unit == 1 ? size_t(3) * padded : 0)) * sizeof(int);
+  constexpr auto bytes = [](int unit, int units) {
+    return (2 * (units + 1) + (unit == 1 ? 3 * (units + units / 32 + 1) : 0)) * int(sizeof(int));
+  };
+  const int smem = bytes(unit, units);
+  static_assert(bytes(kGroup, (65535 + kGroup - 1) / kGroup) <= 48 * 1024, "no attribute for the grouped form");
   const auto kernel = unit == 1 ? &build_tables_kernel<1> : &build_tables_kernel<kGroup>;
   if (smem > 48 * 1024) {
+    // (the most any batch takes: the attribute is the process's, and a call of
+    // another thread between this line and the launch must not lower it)
     const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(1, kDirect));
     if (err != cudaSuccess) return err;
   }
   // a warp for every row piece or 128 tokens, at most one full CTA per SM

@@ -1,0 +1,49 @@
+"""saw_build_tables as a server calls it: from several threads at once, and in
+place in tables with more rows than the batch."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import bit_paged_kv_gb300 as saw
+from test_gpu_tables import batch, model
+
+pytestmark = pytest.mark.gpu
+
+
+def test_threads_at_once():
+    """Eight threads, batches of two sizes that want more than 48 KB of shared memory: every call is launched, every
+    batch right."""
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+    L, sides = saw.lib(), []
+    for B in (2500, 4096) * 4:
+        cached, fresh, free, pages, blocks, src, rows = batch(B, B, 60, 2, 16)
+        T = int(fresh.sum())
+        bt = np.full((B, blocks), -7, np.int32)
+        want, _ = model(cached, fresh, free, len(free), 16, pages, blocks, T, src, rows, bt)
+        out = dict(bt=i32(bt), lens=i32(np.zeros(B)), cu=i32(np.zeros(B + 1)), slots=i32(np.zeros(T)),
+                   pos=i32(np.zeros(T)), taken=i32([0]))
+        ins = [i32(x) for x in (src, rows, cached, fresh, free)]
+        stream = torch.cuda.Stream()
+        s, r, c, n, f = (x.data_ptr() for x in ins)
+        o = {k: v.data_ptr() for k, v in out.items()}
+        args = (s, len(src), blocks, r, c, n, f, len(free), None, B, T, pages, 16, o["bt"], blocks, o["lens"], o["cu"],
+                o["slots"], o["pos"], o["taken"], None, stream.cuda_stream)
+        sides.append((args, want, out, stream, ins))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(args):
+        with torch.cuda.device(0):
+            failed.append(sum(L.saw_build_tables(*args) != saw.SAW_OK for _ in range(5000)))
+
+    threads = [threading.Thread(target=work, args=(side[0],)) for side in sides]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * 8
+    for _, want, out, *_ in sides:
+        assert all(np.array_equal(out[k].cpu().numpy(), want[k]) for k in want)
