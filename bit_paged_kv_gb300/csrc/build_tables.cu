@@ -353,9 +353,11 @@ cudaError_t launch_build_tables(const TablesParams& p, int sms, cudaStream_t str
     return (2 * (units + 1) + (unit == 1 ? 3 * (units + units / 32 + 1) : 0)) * int(sizeof(int));
   };
   const int smem = bytes(unit, units);
-  static_assert(bytes(kGroup, (65535 + kGroup - 1) / kGroup) <= 48 * 1024, "no attribute for the grouped form");
+  // the kernel's static arrays, 520 bytes, count towards the first 48 KB too
+  constexpr int kFree = 47 * 1024;
+  static_assert(bytes(kGroup, (65535 + kGroup - 1) / kGroup) <= kFree, "no attribute for the grouped form");
   const auto kernel = unit == 1 ? &build_tables_kernel<1> : &build_tables_kernel<kGroup>;
-  if (smem > 48 * 1024) {
+  if (smem > kFree) {
     // (the most any batch takes: the attribute is the process's, and a call of
     // another thread between this line and the launch must not lower it)
     const cudaError_t err =

@@ -1,5 +1,7 @@
 """saw_build_tables as a server calls it: from several threads at once, and in
 place in tables with more rows than the batch."""
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -7,6 +9,7 @@ import pytest
 import torch
 
 import bit_paged_kv_gb300 as saw
+from conftest import ROOT
 from test_gpu_tables import batch, model
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +50,23 @@ def test_threads_at_once():
     assert failed == [0] * 8
     for _, want, out, *_ in sides:
         assert all(np.array_equal(out[k].cpu().numpy(), want[k]) for k in want)
+
+
+SIZES = """
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import bit_paged_kv_gb300 as saw
+i32 = lambda n, v=0: torch.full((n,), v, dtype=torch.int32, device="cuda")
+for B in range(2370, 2420):
+    lens, cu, slots, taken = i32(B), i32(B + 1), i32(B), i32(1)
+    saw.saw_build_tables(None, i32(B, 1), torch.arange(B, device="cuda", dtype=torch.int32), None, 16, B,
+                         i32(B).view(B, 1), lens, cu, slots, pages_taken=taken)
+    assert taken.item() == B and lens.sum().item() == B and (slots == 16 * torch.arange(B, device="cuda")).all(), B
+"""
+
+
+def test_every_size_around_the_shared_memory_limit():
+    """Batches whose sums take just under and over 48 KB, in a process that launched no larger one before."""
+    r = subprocess.run([sys.executable, "-c", SIZES, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
