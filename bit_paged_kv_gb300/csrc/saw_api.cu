@@ -803,7 +803,7 @@ int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double
     auto pair_of = [&](double beta) { return r * std::log(orig_max_pos / (two_pi * beta)) / (2.0 * std::log(base)); };
     lo = std::max(std::floor(pair_of(high)), 0.0);
     hi = std::min(std::ceil(pair_of(low)), r - 1.0);
-    att = 0.1 * std::log(factor) + 1.0;
+    att = factor > 1.0 ? 0.1 * std::log(factor) + 1.0 : 1.0;
   }
   for (int i = 0; i < p.pairs; ++i) {
     double w = std::pow(b, -2.0 * i / r);

@@ -459,7 +459,8 @@ int32_t saw_build_tables(const int32_t* src_tables, int32_t num_src_rows, int32_
  *   SAW_ROPE_YARN    w_i for pairs that turn more than `high` times within
  *                    orig_max_pos positions, w_i / factor for those below
  *                    `low`, a linear ramp over the pair index between (its
- *                    ends rounded outwards); a = 0.1 ln(factor) + 1
+ *                    ends rounded outwards); a = 0.1 ln(factor) + 1, or 1
+ *                    for factor < 1
  *   SAW_ROPE_BANDS   the same ends, a linear ramp over the number of turns
  * low = high = 0 means 1 and 32 (YARN) or 1 and 4 (BANDS).  a is 1 except for
  * YARN; att_scale > 0 sets it.  Angles are exact to 2^-32 turns at any
