@@ -850,7 +850,9 @@ int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
     if (!pow2(block_h) || block_h > head_dim || head_dim % block_h) return SAW_ERR_INVALID_ARG;
     if (!block_h_ok(block_h)) return SAW_ERR_UNSUPPORTED;
   }
-  if (int64_t(num_tokens) * (int64_t(num_q_heads) + 2 * int64_t(num_kv_heads)) > INT32_MAX / 2)
+  // (a token's elements are counted in 32 bits)
+  if (num_q_heads > 65535 || num_kv_heads > 65535 ||
+      int64_t(num_tokens) * (int64_t(num_q_heads) + 2 * int64_t(num_kv_heads)) > INT32_MAX / 2)
     return SAW_ERR_UNSUPPORTED;
   if (num_tokens == 0) return SAW_OK;
   if (!k || !positions || !cos_sin || !slot_mapping || !k_cache || (has_v && !v_cache) ||

@@ -497,7 +497,8 @@ int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double
  *               q_out_token_stride; may be q itself with the same stride, and
  *               must not overlap q, k or v otherwise.
  * Other arguments as saw_quantize_append_ex.  A slot of -1 appends nothing;
- * the token's q is turned all the same.
+ * the token's q is turned all the same.  At most 65535 q-heads and kv-heads,
+ * and 2^30 - 1 rows of q, k and v together (else SAW_ERR_UNSUPPORTED).
  *
  * Per pair, in binary32 with products rounded separately: y0 = x0 c - x1 s,
  * y1 = x1 c + x0 s.  k is not rounded in between: its binary32 values go into
