@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
     float* rowm = reinterpret_cast<float*>(smem + kOffM);
     uint64_t* turn = &bars[kTurn + 2 * (warp & 7)];  // [parity]: that tile's m is in rowm
     float2* rowx = reinterpret_cast<float2*>(smem + kOffRow);
+    bool agreed = false;  // on a failure, all four
     for (Segment sg; take(sg);) {
       // ---- q: this thread's quarter row into the A operand (V buffer 0)
       const bool live = row < sg.rows;
@@ -863,6 +864,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
                failed || !(ll > 0.0f) ? make_float2(-INFINITY, 0.0f) : make_float2(mm, ll));
       }
       failed = !rows_sync(!failed);  // rowx has been read
+      agreed = failed;
+    }
+    // One of the four warps that meet may have given up waiting for a segment
+    // that another still got: those that end here without having agreed to
+    // meet as often as the other does in that segment, so that it ends too.
+    if (!agreed) {
+#pragma unroll 1
+      for (int i = 0; i < 3; ++i) (void)rows_sync(!failed);
     }
     if (failed && lane == 0) report(p.dev_status, SAW_ERR_DEVICE_TIMEOUT);
   } else {
