@@ -239,7 +239,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // and the new token are read (and before anything is written).
   // SHARED behind a prefix kernel: that kernel writes only the partials read
   // by the merge and itself waited for everything before it, so nothing here
-  // waits until then.
+  // waits until then.  This grid starts when every CTA of the prefix kernel has
+  // returned from its wait, that is when the kernels before it have completed
+  // and what they wrote is in L2 -- from where everything read ahead of this
+  // grid's own wait is taken (q, lengths, groups and tables by loads that pass
+  // over L1, pages by bulk copies): the programming model promises a grid the
+  // writes of earlier ones only behind its own wait.
   const bool behind = SHARED && p.prefix.ctas > 0;
   const bool early = p.early_pages != 0;
   if (!early && !behind) pdl_wait_then_release();
@@ -273,11 +278,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const int h = warp + i * kWarps;
       qpre[i] = make_uint2(0u, 0u);
       if (behind && h < G)
-        qpre[i] = reinterpret_cast<const uint2*>(p.q + (int64_t(seq) * p.num_q_heads + hq0 + h) * D)[lane];
+        qpre[i] = __ldcg(reinterpret_cast<const uint2*>(p.q + (int64_t(seq) * p.num_q_heads + hq0 + h) * D) + lane);
     }
   }
 
-  int L = p.seq_lens[seq];
+  int L = behind ? __ldcg(p.seq_lens + seq) : p.seq_lens[seq];
   if (L < 0 || L > p.max_seq_len) {
     if (split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     L = 0;
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     // the prefix.  A length inside the prefix is an error (0: an idle row).
     bool bad = false;
     const bool reports = seq == 0 && split == 0 && kvh == 0;
-    pg = prefix_of_seq(p.prefix, seq, P, p.group, p.num_seqs, lane, reports, &bad);
+    pg = prefix_of_seq(p.prefix, seq, P, p.group, p.num_seqs, lane, reports, behind, &bad);
     if (bad && reports && warp == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     if (L < pg.tokens || L - pg.tokens > p.max_own_len) {
       if (L != 0 && split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
@@ -340,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // the (page, kv-head) chunk index of this warp's step i (-1: invalid page)
   auto chunk_id = [&](int i) {
     const int lp = p_begin + (warp + i * kWarps) / C::kStepsPerPage;
-    const int id = btab[lp];
+    const int id = behind ? __ldcg(btab + lp) : btab[lp];
     if (id < 0 || id >= p.num_pages) {
       report(p.dev_status, SAW_ERR_DEVICE_INDEX);
       return -1;

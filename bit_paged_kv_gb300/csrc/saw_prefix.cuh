@@ -45,14 +45,16 @@ __device__ __forceinline__ uint32_t warp_scan_u32(uint32_t v, int lane) {  // in
 // shares nothing; *bad is set in its lane.  The ends of groups out of range or
 // descending do not count for the later ones.
 __device__ __forceinline__ PrefixGroup prefix_load(const PrefixSide& s, int g0, int page_size, int group,
-                                                   int num_seqs, int lane, int* top, bool* bad) {
+                                                   int num_seqs, int lane, int* top, bool* bad,
+                                                   bool past_l1 = false) {
   const int g = g0 + lane;
   PrefixGroup r{0, 0, 0, 0, 0, g};
   int lo = 0, hi = 0, pre = 0;
   if (g < s.num_groups) {
-    lo = s.cu_groups[g];
-    hi = s.cu_groups[g + 1];
-    pre = s.prefix_lens[g];
+    auto load = [&](const int32_t* at) { return past_l1 ? __ldcg(at) : *at; };
+    lo = load(s.cu_groups + g);
+    hi = load(s.cu_groups + g + 1);
+    pre = load(s.prefix_lens + g);
   }
   int reach = lo >= 0 && hi >= lo && hi <= num_seqs ? hi : 0;  // furthest end up to this group
 #pragma unroll
@@ -90,13 +92,14 @@ __device__ __forceinline__ PrefixGroup prefix_from(const PrefixGroup& r, int lan
 }
 
 // Whole warp: the group that holds sequence `seq` (nothing shared if none does).
-// all: every group is looked at, for *bad.
+// all: every group is looked at, for *bad.  past_l1: the entries are taken from
+// L2, for a caller ahead of its dependency wait.
 __device__ __forceinline__ PrefixGroup prefix_of_seq(const PrefixSide& s, int seq, int page_size, int group,
-                                                     int num_seqs, int lane, bool all, bool* bad) {
+                                                     int num_seqs, int lane, bool all, bool past_l1, bool* bad) {
   int top = 0;
   PrefixGroup mine{0, 0, 0, 0, 0, 0};
   for (int g0 = 0; g0 < s.num_groups; g0 += 32) {
-    const PrefixGroup r = prefix_load(s, g0, page_size, group, num_seqs, lane, &top, bad);
+    const PrefixGroup r = prefix_load(s, g0, page_size, group, num_seqs, lane, &top, bad, past_l1);
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, r.first <= seq && seq < r.end);
     if (hit) mine = prefix_from(r, __ffs(hit) - 1);
     if (hit && !all) break;
