@@ -29,11 +29,12 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
 // ------------------------------------------------------------ table
 //
 // The angle of position p is p w_i / 2 pi turns.  turns_i arrives as a 64-bit
-// binary fraction, so p * turns_i modulo 2^64 is the exact angle modulo one
-// turn (error below p 2^-64 turns); its top two bits, rounded, are the
-// quarter, the rest an angle within 1/8 turn that binary32 holds to 2^-27
-// turns.  There the Taylor series of sine (to x^9) and cosine (to x^10) are
-// within 2^-29, two pairs per packed instruction.
+// binary fraction (of a binary64: a relative error of 2^-52, which moves the
+// angle by p w_i 2^-52 radians), so p * turns_i modulo 2^64 is the angle modulo
+// one turn; its top two bits, rounded, are the quarter, the rest an angle within
+// 1/8 turn that binary32 holds to 2^-27 turns.  There the Taylor series of sine
+// (to x^9) and cosine (to x^10) are within 2^-29, two pairs per packed
+// instruction.
 //
 // Bound: HBM writes; 131072 x 128 floats (67 MB) in 10.9 us, 6.1 TB/s, 9.9 us
 // at the measured copy rate.  With sincospif, bound by issue, 17.4 us.

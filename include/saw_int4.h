@@ -463,8 +463,9 @@ int32_t saw_build_tables(const int32_t* src_tables, int32_t num_src_rows, int32_
  *                    for factor < 1
  *   SAW_ROPE_BANDS   the same ends, a linear ramp over the number of turns
  * low = high = 0 means 1 and 32 (YARN) or 1 and 4 (BANDS).  a is 1 except for
- * YARN; att_scale > 0 sets it.  Angles are exact to 2^-32 turns at any
- * position; values are within 2^-22 of a times the true ones.
+ * YARN; att_scale > 0 sets it.  w_i is a binary64: its 2^-52 moves the angle
+ * of position p by p w_i 2^-52 radians, 2^-28 at 16 million positions.  Beside
+ * that, values are within 2^-22 a of the true ones at every position.
  * rope_dim a multiple of 16, at most 256 (else SAW_ERR_UNSUPPORTED).
  */
 #define SAW_ROPE_NONE 0

@@ -70,3 +70,23 @@ def test_every_size_around_the_shared_memory_limit():
     """Batches whose sums take just under and over 48 KB, in a process that launched no larger one before."""
     r = subprocess.run([sys.executable, "-c", SIZES, ROOT], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("B,more", [(1, 1), (5, 3), (70, 1), (200, 130), (4500, 60)])
+def test_in_place_leaves_the_rows_behind_the_batch(B, more):
+    """A server's table of more rows than the batch, every row with pages, extended in place: the batch's rows get
+    their new entries, the rows behind it keep all of theirs."""
+    cached, fresh, free, pages, blocks, src, rows = batch(B, B, 300, 20, 16, extra_rows=0)
+    src = np.concatenate((src[rows], np.random.default_rng(1).integers(0, pages, (more, blocks)))).astype(np.int32)
+    T = int(fresh.sum()) + 3
+    want, codes = model(cached, fresh, free, len(free), 16, pages, blocks, T, src, None, src[:B])
+    whole = torch.from_numpy(src).cuda()
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+    out = dict(bt=whole[:B], lens=i32(np.zeros(B)), cu=i32(np.zeros(B + 1)), slots=i32(np.zeros(T)),
+               pos=i32(np.zeros(T)), taken=i32([0]))
+    status = i32([0])
+    saw.saw_build_tables(i32(cached), i32(fresh), i32(free), None, 16, pages, *out.values(), whole, None, status)
+    assert status.item() == 0 and not codes
+    for k in want:
+        assert np.array_equal(out[k].cpu().numpy(), want[k]), k
+    assert np.array_equal(whole[B:].cpu().numpy(), src[B:])
