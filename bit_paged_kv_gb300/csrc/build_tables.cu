@@ -15,7 +15,7 @@
 // exclusive sums (tokens, pages) over all requests itself -- coalesced loads
 // into shared memory, each thread the sum of a run of requests, one scan over
 // threads -- and keeps them with the requests' lengths and rows (above kDirect
-// requests, the sums of every 32nd only).  That is 12 bytes per request and
+// requests, 229 KB, the sums of every 32nd only).  That is 12 bytes per request and
 // CTA from L2, against a second launch or a look-back between CTAs.  Then the
 // grid shares out (request, 512 entries) pieces of table rows and runs of 128
 // tokens to warps.  A warp's first and last token, found by bisection, bound
@@ -34,8 +34,12 @@ namespace saw {
 namespace {
 
 constexpr int kTabMaxThreads = 1024;
-constexpr int kDirect = 4096;   // up to this many requests: one prefix entry per request
-constexpr int kGroup = 32;      // above: one per 32
+// Up to this many requests: one prefix entry per request, as many as 227 KB of
+// shared memory hold.  Above: one per 32, the requests read again where they are
+// needed (1000 cached and one new token each, us: 4097 requests 8.6 / 23.6, 6000
+// 9.7 / 26.9, 10240 12.6 / 35.2; 16384 only so, 45.7; 65535 of 200 tokens 176).
+constexpr int kDirect = 11264;
+constexpr int kGroup = 32;
 constexpr int kPiece = 512;     // table entries per warp item
 constexpr int kAhead = 4;       // requests a thread loads at once
 constexpr int kTokPerLane = 4;

@@ -10,7 +10,7 @@ import torch
 
 import bit_paged_kv_gb300 as saw
 from conftest import ROOT
-from test_gpu_tables import batch, model
+from test_gpu_tables import batch, check, model
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,17 @@ def test_in_place_leaves_the_rows_behind_the_batch(B, more):
     for k in want:
         assert np.array_equal(out[k].cpu().numpy(), want[k]), k
     assert np.array_equal(whole[B:].cpu().numpy(), src[B:])
+
+
+@pytest.mark.parametrize("B", [4096, 4097, 8191, 11263, 11264, 11265, 65535])
+@pytest.mark.parametrize("lists", ["all", "half"])
+def test_large_batches(B, lists):
+    """Around the largest batch whose sums fit shared memory one by one, and the largest of all; the free list covers
+    all of it, or half."""
+    check(*batch_args(B, lists))
+
+
+def batch_args(B, lists):
+    cached, fresh, free, pages, blocks, src, rows = batch(B, B, 40, 3, 16)
+    nfree = len(free) if lists == "all" else len(free) // 2
+    return cached, fresh, free, nfree, 16, pages, blocks, int(fresh.sum()) + 2, src, rows
