@@ -577,7 +577,10 @@ int32_t plan_prefix(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
   // The prefix pass costs its launch, a part's start and end and the merge
   // (about 15 us more than the decode alone) and 1.2 us per key tile of the
   // fullest SM; without it the decode reads every sequence's copy, 32768 (token,
-  // kv-head) rows of K and V per us, 25000 with more than 4 q-heads to one.
+  // kv-head) rows of K and V per us, 25000 with more than 4 q-heads to one.  The
+  // lengths and groups are on the device: both sides are priced by the bounds,
+  // every sequence behind a prefix of max_prefix_len.  Where few are, sharing is
+  // chosen too early and costs those 15 us.
   // Both sides on GB300, shared / apart, Hkv 8, GQA 4, own parts to 64 tokens:
   // 16 x 4096 tokens 21.1 / 16.8 us, 16 x 8192 23.6 / 39.9, 32 x 2048 23.1 /
   // 17.2, 32 x 4096 23.8 / 27.8, 64 x 1024 23.1 / 22.3 (GQA 8 25.3 / 28.5), 128 x

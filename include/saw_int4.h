@@ -498,7 +498,8 @@ int32_t saw_rope_table(float* cos_sin, int32_t max_pos, int32_t rope_dim, double
  *               q_out_token_stride; may be q itself with the same stride, and
  *               must not overlap q, k or v otherwise.
  * Other arguments as saw_quantize_append_ex.  A slot of -1 appends nothing;
- * the token's q is turned all the same.  At most 65535 q-heads and kv-heads,
+ * the token's q is turned all the same.  Of two tokens with one slot either may
+ * be stored, or codes of one with the scale of the other.  At most 65535 q-heads and kv-heads,
  * and 2^30 - 1 rows of q, k and v together (else SAW_ERR_UNSUPPORTED).
  *
  * Per pair, in binary32 with products rounded separately: y0 = x0 c - x1 s,
@@ -521,7 +522,7 @@ int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
  * current device; 0 when it needs none or the sizes are bad.  Zero-fill a workspace
  * before its first use; each call leaves it ready for the next, of whatever
  * sizes (up to 131072 (sequence, kv-head) pairs; a larger batch wants one of
- * its own).
+ * its own).  It is not one for the other decode calls, whose layouts differ.
  */
 size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
                                          int32_t num_q_heads, int32_t num_kv_heads,
@@ -557,9 +558,13 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  * workspace     saw_prefix_decode_workspace_bytes(...) bytes, 16-byte
  *               aligned, zero-filled before its first use.  Calls sharing one
  *               must be ordered (one stream).
- * mode          SAW_PREFIX_AUTO: by size, whichever is faster (short prefixes
- *               and few sequences are not worth a pass of their own);
- *               SAW_PREFIX_SHARE, SAW_PREFIX_SEPARATE: always, never (tests).
+ * mode          SAW_PREFIX_AUTO: by size, whichever should be faster (short
+ *               prefixes and few sequences are not worth a pass of their own).
+ *               It goes by the bounds given here, as if every sequence had a
+ *               prefix of max_prefix_len; and as the two forms round
+ *               differently, a row's last bits can change with the batch it is
+ *               in.  SAW_PREFIX_SHARE, SAW_PREFIX_SEPARATE: always, never --
+ *               for a caller that knows better, or wants one rounding.
  * formats       SAW_FMT_F16_INPUT, SAW_FMT_BF16_META, SAW_FMT_OUT_INPUT.
  *
  * Arithmetic of the prefix pass: scores to about 2^-22 of their terms (codes
@@ -567,10 +572,12 @@ size_t saw_prefix_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  * and log2 e exceeds 4094 saturates), dequantized V and p rounded once to
  * binary16 (V beyond +-65504 saturates; p of 2^7 at the row's maximum, so a key
  * fainter than 2^-32 of the heaviest adds to the denominator only), sums and
- * softmax in binary32.
+ * softmax in binary32.  A sequence's result does not depend on which of its
+ * splits ends first: the same call gives the same bits.
  *
- * A group with inconsistent entries is reported as SAW_ERR_DEVICE_INDEX and
- * shares nothing.  Other arguments and errors as saw_paged_decode_int4;
+ * A group with inconsistent entries -- out of range, descending, a prefix beyond
+ * max_prefix_len, or reaching back over an earlier group's sequences -- is
+ * reported as SAW_ERR_DEVICE_INDEX and shares nothing; the others do.  Other arguments and errors as saw_paged_decode_int4;
  * head_dim 128, at most 8 q-heads per kv-head and 65535 groups (else
  * SAW_ERR_UNSUPPORTED).
  */
