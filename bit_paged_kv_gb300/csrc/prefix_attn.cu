@@ -259,6 +259,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Within binary16's finite range; a NaN stays one.
+__device__ __forceinline__ float clamp16(float x) {
+  asm("{\n\tmax.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;\n\t}" : "+f"(x) : "f"(-65504.0f), "f"(65504.0f));
+  return x;
+}
+
 // {x, x} as a register pair, built once instead of per packed instruction.
 __device__ __forceinline__ uint64_t twice(float x) {
   uint64_t r;
@@ -659,8 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             // (pairs 1 and 3 of each 8 columns carry 2^-4)
-            const float y0 = fminf(fmaxf(x[2 * j] * f, -65504.0f), 65504.0f);
-            const float y1 = fminf(fmaxf(x[2 * j + 1] * f, -65504.0f), 65504.0f);
+            const float y0 = clamp16(x[2 * j] * f), y1 = clamp16(x[2 * j + 1] * f);
             sum += (y0 + y1) * ((j & 1) ? 1.0f : 0.0625f);
             const __half h0 = __float2half_rn(y0), h1 = __float2half_rn(y1);
             hw[j] = uint32_t(__half_as_ushort(h0)) | (uint32_t(__half_as_ushort(h1)) << 16);
@@ -857,11 +862,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
       }
       if (live && quart == 0) {
         // rowm is the reference that O refers to; nothing counted: m = -inf
+        // (a q with a NaN never sets it, and its l, a NaN, goes on to the merge)
         const float2 x = rowx[r], y = rowx[128 + r];
         const float mm = rowm[r];
-        const float ll = (x.y > 0.0f ? x.y * ex2(x.x - mm) : 0.0f) + (y.y > 0.0f ? y.y * ex2(y.x - mm) : 0.0f);
+        const float ll = (x.y != 0.0f ? x.y * ex2(x.x - mm) : 0.0f) + (y.y != 0.0f ? y.y * ex2(y.x - mm) : 0.0f);
         __stcg(reinterpret_cast<float2*>(p.prefix.part_ml) + sg.slot * kPrefixRows + row,
-               failed || !(ll > 0.0f) ? make_float2(-INFINITY, 0.0f) : make_float2(mm, ll));
+               failed || ll == 0.0f ? make_float2(-INFINITY, 0.0f) : make_float2(mm, ll));
       }
       failed = !rows_sync(!failed);  // rowx has been read
       agreed = failed;

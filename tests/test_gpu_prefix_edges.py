@@ -153,3 +153,22 @@ def test_split_own_parts_repeat_bit_for_bit(mode):
     assert st == 0
     differ = sum(not torch.equal(base.run(s, ws=ws, mode=mode)[0], first) for _ in range(200))
     assert differ == 0
+
+
+@pytest.mark.parametrize("rk", [True, False])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_nan_queries_stay_nan(rk, dt):
+    """A NaN in a head's q makes that row of the output NaN, as the plain decode does, and no other."""
+    s = base.setup(38, [30], [768], np.arange(30) % 3 * 20, hq=8, hkv=2, rk=rk, dt=dt)
+    ref = base.reference(s).reshape(30, 8, 128)
+    s["q"] = s["q"].clone()
+    rows = [(0, 0, 0), (7, 3, 127), (9, 7, 64), (29, 5, 1)]
+    bad = torch.zeros(30, 8, dtype=torch.bool)
+    for b, h, d in rows:
+        s["q"][b, h, d] = float("nan")
+        bad[b, h] = True
+    for mode in (SHARE, SEPARATE):
+        out, st = base.run(s, mode=mode)
+        out = out.cpu()
+        assert st == 0 and out[bad].isnan().all()
+        assert rel_err(out[~bad].numpy(), ref[~bad.numpy()], f"nan-{mode}") <= ATTN_TOL
