@@ -23,8 +23,8 @@
 //
 // Bound: 64 requests with tables of up to 16384 tokens (0.3 MB), 4.2 us, are
 // a launch and four dependent loads.  4096 requests of up to 32768 cached and
-// 256 new tokens, 13.1 us, move 42 MB (6.2 us at the measured copy rate); the
-// rest is issue: 17.6 us with 64-bit sums and the group size a variable, 33.9
+// 256 new tokens, 13.1 us over one batch again and again and 15.3 over three in
+// turn, move 42 MB (6.2 us at the measured copy rate); the rest is issue: 17.6 us with 64-bit sums and the group size a variable, 33.9
 // with a scan per 32 requests in two CTAs per SM.
 #include "saw_device.cuh"
 #include "saw_int4.h"
