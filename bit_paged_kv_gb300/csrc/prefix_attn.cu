@@ -91,9 +91,12 @@ constexpr int kOffRaw = kOffV + 2 * kOpBytes;
 constexpr int kOffMeta = kOffRaw + kRawStages * kRawBytes;
 constexpr int kOffOk = kOffMeta + kMetas * kMetaBytes;  // valid 16-key slices of the raw stages
 constexpr int kOffM = kOffOk + 4 * kRawStages;          // f32 [128]: the rows' running references
-constexpr int kOffRow = kOffM + 128 * 4;                // f32x2 [4][128]: parts of sum(q'); (m, l) at the end
+// (apart: with one tile the set without it writes its (m, l) while the other may
+// still be adding up sum(q'))
+constexpr int kOffSum = kOffM + 128 * 4;                // f32 [4][128]: parts of sum(q')
+constexpr int kOffRow = kOffSum + 4 * 128 * 4;          // f32x2 [2][128]: each set's (m, l) at the end
 constexpr int kSegs = 4;                                // segments announced ahead
-constexpr int kOffSeg = kOffRow + 4 * 128 * 8;
+constexpr int kOffSeg = kOffRow + 2 * 128 * 8;
 constexpr int kOffBar = kOffSeg + kSegs * 48;
 enum { kRawFull = 0, kRawEmpty = kRawFull + kRawStages, kKFull = kRawEmpty + kRawStages, kKEmpty = kKFull + 2,
        kVFull = kKEmpty + 2, kPvDone = kVFull + 2, kMetaFull = kPvDone + 2, kSFull = kMetaFull + kMetas,
@@ -628,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
     const uint32_t ts = tl + (uint32_t(16 * (quart & 1)) << 16);
     float* rowm = reinterpret_cast<float*>(smem + kOffM);
     uint64_t* turn = &bars[kTurn + 2 * (warp & 7)];  // [parity]: that tile's m is in rowm
+    float* rowsum = reinterpret_cast<float*>(smem + kOffSum);
     float2* rowx = reinterpret_cast<float2*>(smem + kOffRow);
     bool agreed = false;  // on a failure, all four
     for (Segment sg; take(sg);) {
@@ -675,13 +679,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
           tmem_st8u(tl + kColQl + 16 * quart + 8 * k, lw);
         }
         tmem_wait_st();
-        rowx[quart * 128 + r] = make_float2(sum, 0.0f);
+        rowsum[quart * 128 + r] = sum;
       }
       ++segs;
       tc_fence_before();
       __syncwarp();
       arrive_elect(&bars[kQFull]);
-      failed = !rows_sync(!failed);  // rowx
+      failed = !rows_sync(!failed);  // rowsum
       uint64_t qs[2];  // a row's sum(q'), twice
       float m[2];      // and reference
       float2 l[2];
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const PrefixPa
       for (int i = 0; i < 2; ++i) {
         float x = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x += rowx[k * 128 + r2 + 8 * i].x;
+        for (int k = 0; k < 4; ++k) x += rowsum[k * 128 + r2 + 8 * i];
         qs[i] = twice(x);
         m[i] = 0.0f;
         l[i] = make_float2(0.0f, 0.0f);

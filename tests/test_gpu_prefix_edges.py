@@ -172,3 +172,16 @@ def test_nan_queries_stay_nan(rk, dt):
         out = out.cpu()
         assert st == 0 and out[bad].isnan().all()
         assert rel_err(out[~bad].numpy(), ref[~bad.numpy()], f"nan-{mode}") <= ATTN_TOL
+
+
+@pytest.mark.parametrize("tokens,groups", [(128, 1), (128, 150), (64, 400)])
+def test_parts_of_one_tile(tokens, groups):
+    """Parts of a single tile, one and many to a CTA: one set of softmax warps has nothing to do but the part's end.
+    Every call of two hundred gives the same bits."""
+    B = 2 * groups
+    s = base.setup(46, [2] * groups, [tokens] * groups, np.arange(B) % 5 * 3, hq=16, hkv=4)
+    base.check(s, f"one-tile-{tokens}x{groups}")
+    need = saw.saw_prefix_decode_workspace_bytes(B, groups, 16, 4, 128, 16, s["max_pre"], s["max_own"], SHARE)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    first, _ = base.run(s, ws=ws)
+    assert all(torch.equal(base.run(s, ws=ws)[0], first) for _ in range(200))
