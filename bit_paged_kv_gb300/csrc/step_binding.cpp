@@ -122,7 +122,7 @@ bool status_word(PyObject* t, int64_t dev, int32_t** out) {
   return t == Py_None || n >= 1;
 }
 // Contiguous memory of any type on the device, of `need` bytes or more (None:
-// null, for the library to judge).
+// null, for the library to refuse or take).
 bool memory(PyObject* t, const char* what, int64_t dev, size_t need, void** out, int64_t* size = nullptr) {
   bool cont;
   *out = nullptr;
