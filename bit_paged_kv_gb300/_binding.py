@@ -28,6 +28,7 @@ SAW_STEP_EARLY_PAGES = 1
 SAW_FMT_F16_INPUT = 1
 SAW_FMT_BF16_META = 2
 SAW_FMT_OUT_INPUT = 4
+SAW_FMT_F32_WEIGHT = 8
 SAW_PREFIX_AUTO, SAW_PREFIX_SHARE, SAW_PREFIX_SEPARATE = range(3)
 SAW_ROPE_NONE, SAW_ROPE_LINEAR, SAW_ROPE_NTK, SAW_ROPE_YARN, SAW_ROPE_BANDS = range(5)
 
@@ -38,7 +39,8 @@ EXPORTS = ("saw_status_string", "saw_cache_bytes", "saw_quantize_append", "saw_d
            "saw_quantize_append_ex", "saw_paged_decode_int4_ex", "saw_decode_step_ex",
            "saw_prefill_attn_int4_ex", "saw_paged_decode_int4_noalloc_ex", "saw_build_tables",
            "saw_rope_table", "saw_rope_append", "saw_prefix_decode_workspace_bytes",
-           "saw_prefix_decode_int4")
+           "saw_prefix_decode_int4", "saw_norm_rope_append", "saw_summary_bytes", "saw_page_summary",
+           "saw_select_pages", "saw_sparse_decode_workspace_bytes", "saw_sparse_decode_int4")
 
 _lib = None
 
@@ -107,6 +109,21 @@ def lib() -> C.CDLL:
     L.saw_prefix_decode_int4.restype = i32
     L.saw_prefix_decode_int4.argtypes = [P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
                                          i32, i32, i32, i32, i32, i32, f32, P, P, sz, i32, i32, P, P]
+    L.saw_norm_rope_append.restype = i32
+    L.saw_norm_rope_append.argtypes = [P, i64, P, i64, P, i64, P, P, f32, f32, P, P, i32, i32, i32, P, i32, i32, i32,
+                                       i32, P, i64, P, P, i32, i32, i32, i32, i32, i32, P, P]
+    L.saw_summary_bytes.restype = sz
+    L.saw_summary_bytes.argtypes = [i32] * 3
+    L.saw_page_summary.restype = i32
+    L.saw_page_summary.argtypes = [P, P, i32, P, P, i32, i32, i32, i32, i32, i32, P, i32, P, P]
+    L.saw_select_pages.restype = i32
+    L.saw_select_pages.argtypes = [P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, P, P,
+                                   P, i32, P, P]
+    L.saw_sparse_decode_workspace_bytes.restype = sz
+    L.saw_sparse_decode_workspace_bytes.argtypes = [i32] * 6
+    L.saw_sparse_decode_int4.restype = i32
+    L.saw_sparse_decode_int4.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, P,
+                                         P, sz, i32, P, P]
     # the *_ex calls: the same arguments plus `formats` before dev_status
     for name in ("saw_quantize_append", "saw_paged_decode_int4", "saw_decode_step",
                  "saw_prefill_attn_int4", "saw_paged_decode_int4_noalloc"):
@@ -374,6 +391,9 @@ def _bind_step():
     m.init(*at, torch.int32, torch.float32, torch.bfloat16, torch.float16,
            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
            getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream))
+    m.init_sparse(*[C.cast(getattr(L, f), C.c_void_p).value
+                    for f in ("saw_norm_rope_append", "saw_page_summary", "saw_select_pages",
+                              "saw_sparse_decode_int4", "saw_summary_bytes")])
     _step = m
     return m
 
@@ -456,6 +476,79 @@ def saw_prefix_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
         workspace, sm_scale, dev_status, stream, meta_bf16, mode)
     if rc:
         _raise(rc, "saw_prefix_decode_int4")
+
+
+# ---------------------------------------------------------------- a sparse decode step
+
+
+def saw_norm_rope_append(q, k: torch.Tensor, v, q_weight, k_weight, positions: torch.Tensor,
+                         cos_sin: torch.Tensor, slot_mapping: torch.Tensor, q_out,
+                         k_cache: torch.Tensor, v_cache, num_pages: int, page_size: int,
+                         rotate_k: bool, rotate_v: bool, block_h: int, eps: float = 1e-6,
+                         weight_offset: float = 0.0, interleaved: bool = False, dev_status=None,
+                         stream=None, meta_bf16: bool = False) -> None:
+    """RMS norm of every q and k head (gains q_weight, k_weight [D] of k's type
+    or float32, plus weight_offset; None: no gains), then saw_rope_append."""
+    rc = (_step or _bind_step()).norm_rope_append(
+        q, k, v, q_weight, k_weight, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, num_pages, page_size,
+        rotate_k, rotate_v, block_h, eps, weight_offset, interleaved, dev_status, stream, meta_bf16)
+    if rc:
+        _raise(rc, "saw_norm_rope_append")
+
+
+def saw_summary_bytes(num_pages: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib().saw_summary_bytes(num_pages, num_kv_heads, head_dim))
+
+
+def saw_page_summary(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, new_lens,
+                     max_new_len: int, num_kv_heads: int, head_dim: int, num_pages: int, page_size: int,
+                     summary: torch.Tensor, dev_status=None, stream=None, meta_bf16: bool = False) -> None:
+    """The mean key of every page that a step completed, into summary
+    (saw_summary_bytes() bytes).  new_lens: int32 [B], the step's new tokens, or
+    None (all); max_new_len: a bound on them."""
+    rc = (_step or _bind_step()).page_summary(
+        k_cache, block_tables, seq_lens, new_lens, max_new_len, num_kv_heads, head_dim, num_pages, page_size, summary,
+        dev_status, stream, meta_bf16)
+    if rc:
+        _raise(rc, "saw_page_summary")
+
+
+def saw_select_pages(q: torch.Tensor, summary: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     max_seq_len: int, num_kv_heads: int, num_pages: int, page_size: int, rotate_k: bool,
+                     block_h: int, first_pages: int, last_pages: int, sel_tables: torch.Tensor,
+                     sel_lens: torch.Tensor, sel_pages=None, dev_status=None, stream=None,
+                     meta_bf16: bool = False) -> None:
+    """The pages that each kv-head's queries attend over, by the scores of their
+    summaries.  q: [B, Hq, D] contiguous; sel_tables (physical ids) and sel_pages
+    (page numbers, may be None): int32 [B, Hkv, max_selected]; sel_lens: int32
+    [B, Hkv]."""
+    rc = (_step or _bind_step()).select_pages(
+        q, summary, block_tables, seq_lens, max_seq_len, num_kv_heads, num_pages, page_size, rotate_k, block_h,
+        first_pages, last_pages, sel_tables, sel_lens, sel_pages, dev_status, stream, meta_bf16)
+    if rc:
+        _raise(rc, "saw_select_pages")
+
+
+def saw_sparse_decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                      page_size: int, max_sel_len: int) -> int:
+    return int(lib().saw_sparse_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, page_size,
+                                                       max_sel_len))
+
+
+def saw_sparse_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, sel_tables: torch.Tensor,
+                           sel_lens: torch.Tensor, max_sel_len: int, num_kv_heads: int, num_pages: int,
+                           page_size: int, rotate_k: bool, rotate_v: bool, block_h: int, out: torch.Tensor,
+                           workspace=None, sm_scale: float = 0.0, dev_status=None, stream=None,
+                           meta_bf16: bool = False) -> None:
+    """Decode over a list of pages per (sequence, kv-head): sel_tables int32 [B,
+    Hkv, pages], sel_lens int32 [B, Hkv].  q: [B, Hq, D] contiguous; out: the
+    same shape, float32 or q's type; workspace:
+    saw_sparse_decode_workspace_bytes() bytes, zero-filled before its first use."""
+    rc = (_step or _bind_step()).sparse_decode(
+        q, k_cache, v_cache, sel_tables, sel_lens, max_sel_len, num_kv_heads, num_pages, page_size, rotate_k, rotate_v,
+        block_h, out, workspace, sm_scale, dev_status, stream, meta_bf16)
+    if rc:
+        _raise(rc, "saw_sparse_decode_int4")
 
 
 # ---------------------------------------------------------------- *_ex twins

@@ -31,7 +31,8 @@ COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE
 # separately rounded binary32 steps; it uses explicit _rn intrinsics and is
 # also compiled with contraction off.  The decode kernel is built once per CTA
 # shape (16, 8 and 4 warps), once more with 16 and 8 warps for head_dim 64
-# and 256, and once more per shape as the shared-prefix decode's second pass.
+# and 256, once more per shape as the shared-prefix decode's second pass, and
+# per shape and size for lists of pages; the rotary append again with norms.
 UNITS = [("saw_api.cu", "saw_api.o", []),
          ("quantize_append.cu", "quantize_append.o", ["-fmad=false"]),
          ("paged_decode.cu", "paged_decode_w16.o", ["-DSAW_DECODE_WARPS=16"]),
@@ -47,9 +48,22 @@ UNITS = [("saw_api.cu", "saw_api.o", []),
           ["-DSAW_DECODE_WARPS=8", "-DSAW_DECODE_SHARED"]),
          ("paged_decode.cu", "paged_decode_shared_w4.o",
           ["-DSAW_DECODE_WARPS=4", "-DSAW_DECODE_SHARED"]),
+         ("paged_decode.cu", "paged_decode_sparse_w16.o",
+          ["-DSAW_DECODE_WARPS=16", "-DSAW_DECODE_SPARSE"]),
+         ("paged_decode.cu", "paged_decode_sparse_w8.o",
+          ["-DSAW_DECODE_WARPS=8", "-DSAW_DECODE_SPARSE"]),
+         ("paged_decode.cu", "paged_decode_sparse_w4.o",
+          ["-DSAW_DECODE_WARPS=4", "-DSAW_DECODE_SPARSE"]),
+         ("paged_decode.cu", "paged_decode_sparse_dims_w16.o",
+          ["-DSAW_DECODE_WARPS=16", "-DSAW_DECODE_OTHER_DIMS", "-DSAW_DECODE_SPARSE"]),
+         ("paged_decode.cu", "paged_decode_sparse_dims_w8.o",
+          ["-DSAW_DECODE_WARPS=8", "-DSAW_DECODE_OTHER_DIMS", "-DSAW_DECODE_SPARSE"]),
          ("prefix_attn.cu", "prefix_attn.o", []),
          ("build_tables.cu", "build_tables.o", []),
          ("rope_append.cu", "rope_append.o", []),
+         ("rope_append.cu", "rope_append_norm.o", ["-DSAW_ROPE_NORM"]),
+         ("page_summary.cu", "page_summary.o", []),
+         ("select_pages.cu", "select_pages.o", []),
          ("paged_decode_bf16.cu", "paged_decode_bf16.o", []),
          ("prefill_attn.cu", "prefill_attn.o", []),
          ("variants.cu", "variants.o", []),

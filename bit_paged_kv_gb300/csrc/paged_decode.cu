@@ -223,11 +223,21 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves
 // zero in the second half of the D dims, v >= 4 one of the second, zero in
 // the first half; each column's output is its own half.  The tensor cores do the
 // zero products; every per-tile cost is shared by the two kv-heads.
-template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false>
+// SPARSE (saw_sparse_decode_int4): block_tables has a row, and seq_lens an
+// entry, per (sequence, kv-head).
+// FINE (sparse, outputs of more than 8 bits): p*s enters the PV product as a
+// binary16 and its remainder, 22 bits together.  As one binary16 its rounding
+// (2^-11) is of the size of a binary16 output's own and shows where few pages
+// are read; below a bfloat16 output's 2^-8 it does not.  PACKED: the remainder
+// is column 2h + 1, zero otherwise, at no product's cost; WIDE: a second product.
+template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false, bool SPARSE = false,
+          bool FINE = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
   static_assert(!APPEND || D == kHeadDim, "the fused step is built for head_dim 128");
   static_assert(!SHARED || (D == kHeadDim && !APPEND && !PAIR), "the shared-prefix pass is built for head_dim 128");
   static_assert(!PAIR || (!PACKED && !APPEND), "pairs use the wide form, without the fused step");
+  static_assert(!SPARSE || (!APPEND && !PAIR && !SHARED), "a list of pages per kv-head: the plain decode");
+  static_assert(!FINE || SPARSE, "remainders are built for lists of pages");
   using C = Cfg<D, P, PAIR>;
   using DM = Dims<D>;
   constexpr int kStages = DM::kStages;
@@ -282,9 +292,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
   }
 
-  int L = behind ? __ldcg(p.seq_lens + seq) : p.seq_lens[seq];
+  const int64_t trow = SPARSE ? int64_t(seq) * p.num_kv_heads + kvh : seq;  // of the tables and lengths
+  int L = behind ? __ldcg(p.seq_lens + trow) : p.seq_lens[trow];
   if (L < 0 || L > p.max_seq_len) {
-    if (split == 0 && kvh == 0 && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+    if (split == 0 && (SPARSE || kvh == 0) && tid == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     L = 0;
   }
   PrefixGroup pg{0, 0, 0, 0, 0, 0};
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     if (split == 0 && n_pages == 0) {
       const int64_t row = (int64_t(seq) * p.num_q_heads + hq0) * kOutD;
       for (int idx = tid; idx < G * kOutD; idx += kThreads) {
-        if (SHARED && p.out16)
+        if ((SHARED || SPARSE) && p.out16)
           p.out16[row + idx] = 0;
         else
           p.out[row + idx] = 0.0f;
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   uint8_t* ring = smem + warp * kStages * C::kStage;
   uint64_t* wbars = bars + warp * kStages;
   int32_t* wok = stage_ok + warp * kStages;
-  const int32_t* btab = p.block_tables + int64_t(seq) * p.max_blocks + skip_pages;
+  const int32_t* btab = p.block_tables + trow * p.max_blocks + skip_pages;
 
   // the (page, kv-head) chunk index of this warp's step i (-1: invalid page)
   auto chunk_id = [&](int i) {
@@ -830,9 +841,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         l_run[0] *= al0;
         z_run[0] *= al0;
 #pragma unroll
-        for (int k = 0; k < kMT; ++k) {  // columns 2c + 1 stay zero
+        for (int k = 0; k < kMT; ++k) {  // columns 2c + 1 stay zero (FINE: the remainders)
           acc[k][0] *= al0;
           acc[k][2] *= al0;
+          if constexpr (FINE) {
+            acc[k][1] *= al0;
+            acc[k][3] *= al0;
+          }
         }
         nmu.x = -mu0;
       } else {
@@ -894,15 +909,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         sv1 = v1 ? sv1 : 0.0f;
         zv1 = v1 ? zv1 : 0.0f;
       }
-      uint32_t b0, b1;
+      uint32_t b0, b1, r0 = 0u, r1 = 0u;  // r: the remainders (FINE, WIDE)
+      auto rest = [](float x) { return x - __half2float(__float2half_rn(x)); };
       if constexpr (PACKED) {
         l_run[0] = l_run[0] + (p01.x + p01.y);
         z_run[0] = z_run[0] + fmaf(p01.y, zv1, p01.x * zv0);
         const float2 ps = mul2(p01, make_float2(sv0, sv1));
         // the two 8 x 8 blocks (score rows 0-7 and 8-15 by columns 2c: head
         // c; columns 2c + 1 zero), transposed: B column 2h carries head h
-        b0 = movm_t(pack_half2(ps.x, 0.0f));
-        b1 = movm_t(pack_half2(ps.y, 0.0f));
+        b0 = movm_t(pack_half2(ps.x, FINE ? rest(ps.x) : 0.0f));
+        b1 = movm_t(pack_half2(ps.y, FINE ? rest(ps.y) : 0.0f));
       } else {
         const float2 l2 = add2(make_float2(l_run[0], l_run[1]), add2(p01, p23));
         const float2 z2 = add2(make_float2(z_run[0], z_run[1]),
@@ -919,6 +935,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         // 2c, 2c+1 (and 2c+8, 2c+9) carry the tokens of score rows 2c, 2c+1
         b0 = movm_t(pack_half2(ps01.x, ps01.y));
         b1 = movm_t(pack_half2(ps23.x, ps23.y));
+        if constexpr (FINE) {
+          r0 = movm_t(pack_half2(rest(ps01.x), rest(ps01.y)));
+          r1 = movm_t(pack_half2(rest(ps23.x), rest(ps23.y)));
+        }
       }
 
       // V^T operands: the 8 x 8 blocks of 16-bit elements (8 token rows of
@@ -958,6 +978,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           a[2] = y & kLoNib;
           a[3] = y & kHiNib;
           mma_16816(acc[2 * db + hh], a, b0, b1);
+          if constexpr (FINE && !PACKED) mma_16816(acc[2 * db + hh], a, r0, r1);
         }
       }
     }
@@ -1062,6 +1083,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // output rows g (even dims) carried n * 2^-24, rows g + 8 (odd) n * 2^-20
 #pragma unroll
   for (int k = 0; k < kMT; ++k) {
+    if constexpr (FINE && PACKED) {
+      acc[k][0] += acc[k][1];
+      acc[k][2] += acc[k][3];
+    }
     acc[k][0] *= 16777216.0f;
     acc[k][1] *= 16777216.0f;
     acc[k][2] *= 1048576.0f;
@@ -1458,6 +1483,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   for (int idx = tid; idx < G * kOutD; idx += kThreads) {
     const int h = idx / kOutD, dd = idx - h * kOutD;
     const float o = PAIR ? qs[h * D + (h >> 2) * kOutD + dd] : qs[idx];
+    if constexpr (SPARSE) {
+      if (p.out16) {  // the one rounding of a 16-bit output
+        const float x = o * post;
+        p.out16[(int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx] =
+            p.in_f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        continue;
+      }
+    }
     p.out[(int64_t(seq) * p.num_q_heads + hq0) * kOutD + idx] = o * post;
   }
 }
@@ -1465,10 +1498,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
 // Launched with programmatic stream serialization: the kernel may start while
 // the previous kernel in the stream drains; it waits for it (griddepcontrol)
 // before reading anything.
-template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false>
+template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false, bool SPARSE = false,
+          bool FINE = false>
 cudaError_t launch_p(const DecodeParams& p, cudaStream_t stream) {
   using C = Cfg<D, P, PAIR>;
-  auto kernel = paged_decode_kernel<D, P, PACKED, APPEND, BFM, PAIR, SHARED>;
+  auto kernel = paged_decode_kernel<D, P, PACKED, APPEND, BFM, PAIR, SHARED, SPARSE, FINE>;
   cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
@@ -1491,6 +1525,12 @@ cudaError_t launch_page_m(const DecodeParams& p, cudaStream_t stream) {
 #ifdef SAW_DECODE_SHARED
   return packed ? launch_p<D, P, true, false, BFM, false, true>(p, stream)
                 : launch_p<D, P, false, false, BFM, false, true>(p, stream);
+#elif defined(SAW_DECODE_SPARSE)
+  if (p.out16 && !p.in_f16)
+    return packed ? launch_p<D, P, true, false, BFM, false, false, true>(p, stream)
+                  : launch_p<D, P, false, false, BFM, false, false, true>(p, stream);
+  return packed ? launch_p<D, P, true, false, BFM, false, false, true, true>(p, stream)
+                : launch_p<D, P, false, false, BFM, false, false, true, true>(p, stream);
 #else
   if constexpr (D == kHeadDim) {
     if (p.append)
@@ -1522,6 +1562,22 @@ cudaError_t launch_dim(const DecodeParams& p, cudaStream_t stream) {
 cudaError_t SAW_CAT(launch_paged_decode_shared_w, SAW_DECODE_WARPS)(const DecodeParams& p,
                                                                     cudaStream_t stream) {
   return launch_dim<kHeadDim>(p, stream);
+}
+#elif defined(SAW_DECODE_SPARSE) && !defined(SAW_DECODE_OTHER_DIMS)
+// a list of pages per (sequence, kv-head), head_dim 128
+cudaError_t SAW_CAT(launch_paged_decode_sparse_w, SAW_DECODE_WARPS)(const DecodeParams& p,
+                                                                    cudaStream_t stream) {
+  return launch_dim<kHeadDim>(p, stream);
+}
+#elif defined(SAW_DECODE_SPARSE)
+// the same at head_dim 64 and 256
+cudaError_t SAW_CAT(launch_paged_decode_sparse_dims_w, SAW_DECODE_WARPS)(const DecodeParams& p,
+                                                                         cudaStream_t stream) {
+  switch (p.head_dim) {
+    case 64: return launch_dim<64>(p, stream);
+    case 256: return launch_dim<256>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 #elif !defined(SAW_DECODE_OTHER_DIMS)
 // head_dim 128 (and the fused decode step)

@@ -20,12 +20,20 @@ namespace saw {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+// This file is built twice: as it is, and with a norm of every q and k row in
+// front (norm_row, norm16; SAW_ROPE_NORM).
+#ifdef SAW_ROPE_NORM
+using Params = NormRopeParams;
+#else
+using Params = RopeParams;
+#endif
 
 __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+#ifndef SAW_ROPE_NORM
 // ------------------------------------------------------------ table
 //
 // The angle of position p is p w_i / 2 pi turns.  turns_i arrives as a 64-bit
@@ -93,6 +101,34 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const RopeTab
     *reinterpret_cast<float4*>(row + p.pairs + i0) = make_float4(sv[0], sv[1], sv[2], sv[3]);
   }
 }
+
+#endif
+
+// ------------------------------------------------------------ norm
+//
+// y_i = RN(RN(x_i r) g_i), g_i = RN(w_i + offset), r = 1 / sqrt(ss / D + eps),
+// ss the sum of the squares by a binary tree over the bits of the element
+// index, lowest first: neighbours, pairs of neighbours, and so on.  A tree is
+// the same sum for every way of dealing a row's elements to lanes, so the row
+// and the bulk kernel give the same bits.
+#ifdef SAW_ROPE_NORM
+__device__ __forceinline__ float gain(const Params& p, int tensor, int d) {
+  const void* w = p.weight[tensor];
+  if (!w) return 1.0f;
+  float g;
+  if (p.weight_f32) {
+    g = __ldg(static_cast<const float*>(w) + d);
+  } else {
+    const uint32_t b = __ldg(static_cast<const uint16_t*>(w) + d);
+    g = in_lo(b, p.in_f16 != 0);
+  }
+  return __fadd_rn(g, p.weight_offset);
+}
+template <int D>
+__device__ __forceinline__ float norm_factor(float ss, float eps) {
+  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps)));
+}
+#endif
 
 // ------------------------------------------------------------ one row per warp
 //
@@ -167,7 +203,7 @@ __device__ __forceinline__ void turn_row(float (&x)[D / 32], const float* cs, in
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kRowWarps) rope_append_row_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kRowWarps) rope_append_row_kernel(const Params p) {
   pdl_wait_then_release();
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
@@ -206,6 +242,25 @@ __global__ void __launch_bounds__(32 * kRowWarps) rope_append_row_kernel(const R
                              : (tensor ? p.v + int64_t(t) * p.v_stride : p.k + int64_t(t) * p.k_stride);
   float x[E];
   load_row<D>(src + int64_t(hd) * D + E * lane, f16, x);
+#ifdef SAW_ROPE_NORM
+  if (turned) {
+    float g[E], s[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      g[i] = gain(p, is_q ? 0 : 1, E * lane + i);
+      s[i] = __fmul_rn(x[i], x[i]);
+    }
+#pragma unroll
+    for (int d = 1; d < E; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < E; i += 2 * d) s[i] = __fadd_rn(s[i], s[i + d]);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], m));
+    const float r = norm_factor<D>(s[0], p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), g[i]);
+  }
+#endif
   if (turned)
     turn_row<D>(x, p.cos_sin + int64_t(pos) * p.rope_dim, p.rope_dim, p.interleaved != 0, lane);
 
@@ -276,7 +331,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) rope_append_row_kernel(const R
 }
 
 template <int D>
-cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
+cudaError_t launch_rows(const Params& p, cudaStream_t stream) {
   const int64_t warps = int64_t(p.num_tokens) * (p.num_q_heads + p.num_kv_heads * p.num_tensors);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((warps + kRowWarps - 1) / kRowWarps));
@@ -468,6 +523,44 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int h
   for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], c_h);
 }
 
+#ifdef SAW_ROPE_NORM
+// The norm of a lane's 16 values; g: the tensor's gains in shared memory, a
+// and hc as below.
+template <int D>
+__device__ __forceinline__ void norm16(float (&x)[16], const float* g, float eps, int a, int hc) {
+  float s[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = __fmul_rn(x[i], x[i]);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; i += 2 * d) s[i] = __fadd_rn(s[i], s[i + d]);
+  float u = s[0], v = s[8];
+  bool joined = false;
+#pragma unroll
+  for (int d = 8; d < D; d <<= 1) {
+    if (d == 8 * hc) {
+      u = __fadd_rn(u, v);
+      joined = true;
+    } else if (!joined) {
+      u = __fadd_rn(u, __shfl_xor_sync(kAll, u, d >> 3));
+      v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d >> 3));
+    } else {
+      u = __fadd_rn(u, __shfl_xor_sync(kAll, u, d >> 4));
+    }
+  }
+  const float r = norm_factor<D>(u, eps);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 w = *reinterpret_cast<const float4*>(g + 8 * (j < 2 ? a : a + hc) + 4 * (j & 1));
+    x[4 * j] = __fmul_rn(__fmul_rn(x[4 * j], r), w.x);
+    x[4 * j + 1] = __fmul_rn(__fmul_rn(x[4 * j + 1], r), w.y);
+    x[4 * j + 2] = __fmul_rn(__fmul_rn(x[4 * j + 2], r), w.z);
+    x[4 * j + 3] = __fmul_rn(__fmul_rn(x[4 * j + 3], r), w.w);
+  }
+}
+#endif
+
 // Eight codes as a word.  fast (no clamp can bite): (y - z) r 2^-24 converts
 // to a binary16 whose bits are the round-half-even code.
 __device__ __forceinline__ uint32_t codes8(const float* x, const RowMeta& m) {
@@ -496,8 +589,13 @@ __device__ __forceinline__ uint32_t codes8(const float* x, const RowMeta& m) {
 
 template <int D, bool F16IN, int LAYOUT>
 __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
-    rope_append_bulk_kernel(const RopeParams p, uint32_t warps) {
+    rope_append_bulk_kernel(const Params p, uint32_t warps) {
   pdl_wait_then_release();
+#ifdef SAW_ROPE_NORM
+  __shared__ __align__(16) float gains[2][D];
+  for (int i = threadIdx.x; i < 2 * D; i += 32 * kBulkWarps) gains[i / D][i % D] = gain(p, i / D, i % D);
+  __syncthreads();
+#endif
   constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR;
@@ -547,6 +645,9 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
           float x[16];
           widen8<F16IN>(w[k][0], x);
           widen8<F16IN>(w[k][1], x + 8);
+#ifdef SAW_ROPE_NORM
+          norm16<D>(x, gains[0], p.eps, a, hc);
+#endif
           turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
           if (h < h1) {
             *reinterpret_cast<uint4*>(dst + h * D) = narrow8<F16IN>(x);
@@ -585,6 +686,9 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
         w0 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D);
         w1 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D + 8 * hc);
       }
+#ifdef SAW_ROPE_NORM
+      if (tensor == 0) norm16<D>(x, gains[1], p.eps, a, hc);
+#endif
       if (tensor == 0) turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
       if (rot) rotate16<D>(x, p.block_h, p.c_h, hc, lane);
       float mn = fminf(x[0], x[1]), mx = fmaxf(x[0], x[1]);
@@ -613,7 +717,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
 }
 
 template <int D, bool F16IN, int LAYOUT>
-cudaError_t launch_bulk_l(const RopeParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_bulk_l(const Params& p, int sms, cudaStream_t stream) {
   const int parts = (p.num_q_heads + kQPart - 1) / kQPart + p.num_tensors;
   const int64_t items = int64_t(p.num_tokens) * parts;
   const int64_t want = (items + kBulkWarps - 1) / kBulkWarps;
@@ -635,7 +739,7 @@ cudaError_t launch_bulk_l(const RopeParams& p, int sms, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t launch_bulk(const RopeParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_bulk(const Params& p, int sms, cudaStream_t stream) {
   const int hc = p.rope_dim >> 4;
   const int layout = p.interleaved ? kInter : p.rope_dim == D ? kHalfWhole : hc & (hc - 1) ? kHalfPart : kHalfBit;
   auto with = [&](auto f16) {
@@ -652,6 +756,7 @@ cudaError_t launch_bulk(const RopeParams& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
+#ifndef SAW_ROPE_NORM
 cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t stream) {
   const int64_t items = int64_t(p.max_pos) * (p.pairs / 4);
   const int64_t want = (items + kTableThreads - 1) / kTableThreads;
@@ -666,8 +771,13 @@ cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t st
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, rope_table_kernel, p);
 }
+#endif
 
+#ifdef SAW_ROPE_NORM
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, int sms, cudaStream_t stream) {
+#else
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream) {
+#endif
   const bool bulk = int64_t(p.num_tokens) * (p.num_q_heads + 2 * p.num_kv_heads) * p.head_dim >= kBulkMinElems;
   switch (p.head_dim) {
     case 64: return bulk ? launch_bulk<64>(p, sms, stream) : launch_rows<64>(p, stream);

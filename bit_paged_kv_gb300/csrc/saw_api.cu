@@ -163,6 +163,87 @@ bool decode_pairs(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, i
   return int64_t(num_seqs) * (num_kv_heads / 2) * splits >= 2 * int64_t(sms > 0 ? sms : 148);
 }
 
+// The sparse decode's split counters: a region of one size, so that calls of
+// different sizes may share a workspace.
+size_t sparse_ticket_bytes(int32_t num_seqs, int32_t num_kv_heads) {
+  return std::max<size_t>(size_t(1) << 20, saw::decode_ticket_bytes(num_seqs, num_kv_heads));
+}
+
+// Checks of the rotary appends; fills the parameters (p.num_tokens is 0 when
+// there is nothing to do).
+int32_t prepare_rope(saw::RopeParams& p, const void* q, int64_t q_token_stride, const void* k,
+                     int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                     const int32_t* positions, const float* cos_sin, int32_t max_pos,
+                     int32_t rope_dim, int32_t interleaved, const int32_t* slot_mapping,
+                     int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                     int32_t head_dim, void* q_out, int64_t q_out_token_stride, void* k_cache,
+                     void* v_cache, int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                     int32_t rotate_v, int32_t block_h, int32_t formats, int32_t* dev_status) {
+  if (num_tokens < 0 || num_kv_heads <= 0 || num_q_heads < 0 || num_pages < 0 || max_pos < 0)
+    return SAW_ERR_INVALID_ARG;
+  if (!formats_ok(formats)) return SAW_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !page_size_ok(page_size)) return SAW_ERR_UNSUPPORTED;
+  if (rope_dim <= 0 || rope_dim > head_dim) return SAW_ERR_INVALID_ARG;
+  if (rope_dim % 16) return SAW_ERR_UNSUPPORTED;
+  if ((rotate_k != 0 && rotate_k != 1) || (rotate_v != 0 && rotate_v != 1) ||
+      (interleaved != 0 && interleaved != 1))
+    return SAW_ERR_INVALID_ARG;
+  const bool has_v = v != nullptr, has_q = q != nullptr && num_q_heads > 0;
+  if (rotate_k || (has_v && rotate_v)) {
+    if (!pow2(block_h) || block_h > head_dim || head_dim % block_h) return SAW_ERR_INVALID_ARG;
+    if (!block_h_ok(block_h)) return SAW_ERR_UNSUPPORTED;
+  }
+  // (a token's elements are counted in 32 bits)
+  if (num_q_heads > 65535 || num_kv_heads > 65535 ||
+      int64_t(num_tokens) * (int64_t(num_q_heads) + 2 * int64_t(num_kv_heads)) > INT32_MAX / 2)
+    return SAW_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return SAW_OK;
+  if (!k || !positions || !cos_sin || !slot_mapping || !k_cache || (has_v && !v_cache) ||
+      (has_q && !q_out))
+    return SAW_ERR_INVALID_ARG;
+  auto rows_ok = [&](const void* x, int64_t stride, int32_t heads) {
+    return aligned16(x) && stride >= int64_t(heads) * head_dim && (stride & 7) == 0;
+  };
+  if (!rows_ok(k, k_token_stride, num_kv_heads) || !aligned16(k_cache) || !aligned16(cos_sin) ||
+      (has_v && (!rows_ok(v, v_token_stride, num_kv_heads) || !aligned16(v_cache))) ||
+      (has_q && (!rows_ok(q, q_token_stride, num_q_heads) ||
+                 !rows_ok(q_out, q_out_token_stride, num_q_heads))))
+    return SAW_ERR_INVALID_ARG;
+  if (has_q && q_out == q && q_out_token_stride != q_token_stride) return SAW_ERR_INVALID_ARG;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.q_stride = q_token_stride;
+  p.k_stride = k_token_stride;
+  p.v_stride = v_token_stride;
+  p.q_out_stride = q_out_token_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.slot_mapping = slot_mapping;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.dev_status = dev_status;
+  p.num_slots = int64_t(num_pages) * page_size;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = has_q ? num_q_heads : 0;
+  p.num_kv_heads = num_kv_heads;
+  p.num_tensors = has_v ? 2 : 1;
+  p.head_dim = head_dim;
+  p.rope_dim = rope_dim;
+  p.max_pos = max_pos;
+  p.interleaved = interleaved;
+  p.rotate_k = rotate_k;
+  p.rotate_v = has_v ? rotate_v : 0;
+  p.block_h = block_h;
+  p.page_size = page_size;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+  p.c_h = (rotate_k || rotate_v) ? float(1.0 / std::sqrt(double(block_h))) : 1.0f;
+  p.in_f16 = (formats & SAW_FMT_F16_INPUT) ? 1 : 0;
+  p.meta_bf16 = (formats & SAW_FMT_BF16_META) ? 1 : 0;
+  return SAW_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -839,71 +920,204 @@ int32_t saw_rope_append(const void* q, int64_t q_token_stride, const void* k,
                         void* v_cache, int32_t num_pages, int32_t page_size, int32_t rotate_k,
                         int32_t rotate_v, int32_t block_h, int32_t formats, int32_t* dev_status,
                         void* stream) {
-  if (num_tokens < 0 || num_kv_heads <= 0 || num_q_heads < 0 || num_pages < 0 || max_pos < 0)
+  saw::RopeParams p{};
+  const int32_t rc = prepare_rope(p, q, q_token_stride, k, k_token_stride, v, v_token_stride,
+                                  positions, cos_sin, max_pos, rope_dim, interleaved, slot_mapping,
+                                  num_tokens, num_q_heads, num_kv_heads, head_dim, q_out,
+                                  q_out_token_stride, k_cache, v_cache, num_pages, page_size,
+                                  rotate_k, rotate_v, block_h, formats, dev_status);
+  if (rc != SAW_OK || num_tokens == 0) return rc;
+  const int sms = sm_count();
+  const cudaError_t err = saw::launch_rope_append(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+int32_t saw_norm_rope_append(const void* q, int64_t q_token_stride, const void* k,
+                             int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                             const void* q_weight, const void* k_weight, float weight_offset,
+                             float eps, const int32_t* positions, const float* cos_sin,
+                             int32_t max_pos, int32_t rope_dim, int32_t interleaved,
+                             const int32_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, void* q_out,
+                             int64_t q_out_token_stride, void* k_cache, void* v_cache,
+                             int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                             int32_t rotate_v, int32_t block_h, int32_t formats,
+                             int32_t* dev_status, void* stream) {
+  saw::NormRopeParams p{};
+  const bool f32 = (formats & SAW_FMT_F32_WEIGHT) != 0;
+  int32_t rc = prepare_rope(p, q, q_token_stride, k, k_token_stride, v, v_token_stride, positions,
+                            cos_sin, max_pos, rope_dim, interleaved, slot_mapping, num_tokens,
+                            num_q_heads, num_kv_heads, head_dim, q_out, q_out_token_stride, k_cache,
+                            v_cache, num_pages, page_size, rotate_k, rotate_v, block_h,
+                            formats & ~int32_t(SAW_FMT_F32_WEIGHT), dev_status);
+  if (rc != SAW_OK) return rc;
+  if (!(eps > 0.0f) || std::isinf(eps) || !std::isfinite(weight_offset)) return SAW_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 15u)
+    return SAW_ERR_INVALID_ARG;
+  if (num_tokens == 0) return SAW_OK;
+  p.weight[0] = q_weight;
+  p.weight[1] = k_weight;
+  p.weight_f32 = f32 ? 1 : 0;
+  p.weight_offset = weight_offset;
+  p.eps = eps;
+  const int sms = sm_count();
+  const cudaError_t err = saw::launch_norm_rope_append(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- sparse decode
+
+size_t saw_summary_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim) {
+  if (num_pages <= 0 || num_kv_heads <= 0 || head_dim <= 0 || (head_dim & 1)) return 0;
+  return size_t(num_pages) * size_t(saw::summary_stride(num_kv_heads, head_dim));
+}
+
+int32_t saw_page_summary(const void* k_cache, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         const int32_t* new_lens, int32_t num_seqs, int32_t max_new_len,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                         int32_t page_size, void* summary, int32_t formats, int32_t* dev_status,
+                         void* stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || num_pages < 0 || max_blocks_per_seq < 0 || max_new_len < 0)
+    return SAW_ERR_INVALID_ARG;
+  if (formats & ~int32_t(SAW_FMT_BF16_META)) return SAW_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !page_size_ok(page_size)) return SAW_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return SAW_ERR_UNSUPPORTED;
+  if ((int64_t(max_new_len) / page_size + 1) * num_kv_heads > (int64_t(1) << 30)) return SAW_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return SAW_OK;
+  if (!k_cache || !block_tables || !seq_lens || !summary || !aligned16(k_cache) || !aligned16(summary))
+    return SAW_ERR_INVALID_ARG;
+  saw::SummaryParams p{};
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.summary = static_cast<uint8_t*>(summary);
+  p.dev_status = dev_status;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.max_new_len = max_new_len;
+  p.num_kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
+  p.meta_bf16 = (formats & SAW_FMT_BF16_META) ? 1 : 0;
+  const int sms = sm_count();
+  const cudaError_t err = saw::launch_page_summary(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+int32_t saw_select_pages(const void* q, const void* summary, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                         int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                         int32_t block_h, int32_t max_selected, int32_t first_pages,
+                         int32_t last_pages, int32_t* sel_tables, int32_t* sel_pages,
+                         int32_t* sel_lens, int32_t formats, int32_t* dev_status, void* stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_pages < 0 || max_seq_len < 0 ||
+      max_blocks_per_seq < 0)
     return SAW_ERR_INVALID_ARG;
   if (!formats_ok(formats)) return SAW_ERR_INVALID_ARG;
   if (!head_dim_ok(head_dim) || !page_size_ok(page_size)) return SAW_ERR_UNSUPPORTED;
-  if (rope_dim <= 0 || rope_dim > head_dim) return SAW_ERR_INVALID_ARG;
-  if (rope_dim % 16) return SAW_ERR_UNSUPPORTED;
-  if ((rotate_k != 0 && rotate_k != 1) || (rotate_v != 0 && rotate_v != 1) ||
-      (interleaved != 0 && interleaved != 1))
-    return SAW_ERR_INVALID_ARG;
-  const bool has_v = v != nullptr, has_q = q != nullptr && num_q_heads > 0;
-  if (rotate_k || (has_v && rotate_v)) {
+  if (num_q_heads % num_kv_heads || (rotate_k != 0 && rotate_k != 1)) return SAW_ERR_INVALID_ARG;
+  if (num_q_heads / num_kv_heads > saw::kMaxGroup) return SAW_ERR_UNSUPPORTED;
+  if (rotate_k) {
     if (!pow2(block_h) || block_h > head_dim || head_dim % block_h) return SAW_ERR_INVALID_ARG;
     if (!block_h_ok(block_h)) return SAW_ERR_UNSUPPORTED;
   }
-  // (a token's elements are counted in 32 bits)
-  if (num_q_heads > 65535 || num_kv_heads > 65535 ||
-      int64_t(num_tokens) * (int64_t(num_q_heads) + 2 * int64_t(num_kv_heads)) > INT32_MAX / 2)
+  if (first_pages < 0 || last_pages < 1 || int64_t(first_pages) + last_pages > max_selected)
+    return SAW_ERR_INVALID_ARG;
+  if (int64_t(max_blocks_per_seq) * page_size < int64_t(max_seq_len)) return SAW_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || max_selected > saw::kSelectMaxPages ||
+      ceil_div(max_seq_len, page_size) > saw::kSelectMaxPages)
     return SAW_ERR_UNSUPPORTED;
-  if (num_tokens == 0) return SAW_OK;
-  if (!k || !positions || !cos_sin || !slot_mapping || !k_cache || (has_v && !v_cache) ||
-      (has_q && !q_out))
+  if (num_seqs == 0) return SAW_OK;
+  if (!q || !summary || !block_tables || !seq_lens || !sel_tables || !sel_lens || !aligned16(q) ||
+      !aligned16(summary))
     return SAW_ERR_INVALID_ARG;
-  auto rows_ok = [&](const void* x, int64_t stride, int32_t heads) {
-    return aligned16(x) && stride >= int64_t(heads) * head_dim && (stride & 7) == 0;
-  };
-  if (!rows_ok(k, k_token_stride, num_kv_heads) || !aligned16(k_cache) || !aligned16(cos_sin) ||
-      (has_v && (!rows_ok(v, v_token_stride, num_kv_heads) || !aligned16(v_cache))) ||
-      (has_q && (!rows_ok(q, q_token_stride, num_q_heads) ||
-                 !rows_ok(q_out, q_out_token_stride, num_q_heads))))
-    return SAW_ERR_INVALID_ARG;
-  if (has_q && q_out == q && q_out_token_stride != q_token_stride) return SAW_ERR_INVALID_ARG;
-  saw::RopeParams p{};
+  saw::SelectParams p{};
   p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.v = static_cast<const uint16_t*>(v);
-  p.q_out = static_cast<uint16_t*>(q_out);
-  p.q_stride = q_token_stride;
-  p.k_stride = k_token_stride;
-  p.v_stride = v_token_stride;
-  p.q_out_stride = q_out_token_stride;
-  p.positions = positions;
-  p.cos_sin = cos_sin;
-  p.slot_mapping = slot_mapping;
-  p.k_cache = static_cast<uint8_t*>(k_cache);
-  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.summary = static_cast<const uint8_t*>(summary);
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.sel_tables = sel_tables;
+  p.sel_pages = sel_pages;
+  p.sel_lens = sel_lens;
   p.dev_status = dev_status;
-  p.num_slots = int64_t(num_pages) * page_size;
-  p.num_tokens = num_tokens;
-  p.num_q_heads = has_q ? num_q_heads : 0;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.max_seq_len = max_seq_len;
+  p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
-  p.num_tensors = has_v ? 2 : 1;
+  p.group = num_q_heads / num_kv_heads;
   p.head_dim = head_dim;
-  p.rope_dim = rope_dim;
-  p.max_pos = max_pos;
-  p.interleaved = interleaved;
-  p.rotate_k = rotate_k;
-  p.rotate_v = has_v ? rotate_v : 0;
-  p.block_h = block_h;
+  p.num_pages = num_pages;
   p.page_size = page_size;
   p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
-  p.c_h = (rotate_k || rotate_v) ? float(1.0 / std::sqrt(double(block_h))) : 1.0f;
+  p.rotate_k = rotate_k;
+  p.block_h = block_h;
+  p.max_selected = max_selected;
+  p.first_pages = first_pages;
+  p.last_pages = last_pages;
+  p.c_h = rotate_k ? float(1.0 / std::sqrt(double(block_h))) : 1.0f;
   p.in_f16 = (formats & SAW_FMT_F16_INPUT) ? 1 : 0;
   p.meta_bf16 = (formats & SAW_FMT_BF16_META) ? 1 : 0;
   const int sms = sm_count();
-  const cudaError_t err = saw::launch_rope_append(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = saw::launch_select_pages(p, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+size_t saw_sparse_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t page_size, int32_t max_sel_len) {
+  if (!head_dim_ok(head_dim) || num_q_heads <= 0) return 0;
+  int32_t splits = 0, pps = 0;
+  if (make_plan(num_seqs, num_kv_heads, page_size, max_sel_len, 0, &splits, &pps) != SAW_OK || splits <= 1)
+    return 0;
+  const size_t rows = size_t(num_seqs) * size_t(num_q_heads) * size_t(splits);
+  return sparse_ticket_bytes(num_seqs, num_kv_heads) + rows * size_t(head_dim + 2) * 4;
+}
+
+int32_t saw_sparse_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* sel_tables, int32_t max_selected,
+                               const int32_t* sel_lens, int32_t num_seqs, int32_t max_sel_len,
+                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                               int32_t rotate_v, int32_t block_h, float sm_scale, void* out,
+                               void* workspace, size_t workspace_bytes, int32_t formats,
+                               int32_t* dev_status, void* stream) {
+  if (max_selected < 0) return SAW_ERR_INVALID_ARG;
+  const bool out16 = (formats & SAW_FMT_OUT_INPUT) != 0;
+  saw::DecodeParams p{};
+  // (one split, as far as these checks go: the plan and the workspace follow)
+  int32_t rc = prepare_decode(p, q, k_cache, v_cache, sel_tables, max_selected, sel_lens, num_seqs,
+                              max_sel_len, num_q_heads, num_kv_heads, head_dim, num_pages, page_size,
+                              rotate_k, rotate_v, block_h, sm_scale, static_cast<float*>(out), nullptr,
+                              0, INT32_MAX, formats & ~int32_t(SAW_FMT_OUT_INPUT), dev_status);
+  if (rc != SAW_OK || num_seqs == 0) return rc;
+  rc = make_plan(num_seqs, num_kv_heads, page_size, max_sel_len, 0, &p.num_splits, &p.pages_per_split, &p.warps);
+  if (rc != SAW_OK) return rc;
+  const size_t need = saw_sparse_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, page_size,
+                                                        max_sel_len);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SAW_ERR_INVALID_ARG;
+  p.pair = 0;
+  if (need > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.tickets = reinterpret_cast<uint32_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + sparse_ticket_bytes(num_seqs, num_kv_heads));
+    p.part_ml = p.part_o + size_t(num_seqs) * num_q_heads * p.num_splits * head_dim;
+  }
+  if (out16) p.out16 = static_cast<uint16_t*>(out);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if (head_dim == kHeadDim)
+    err = p.warps == 4   ? saw::launch_paged_decode_sparse_w4(p, s)
+          : p.warps == 8 ? saw::launch_paged_decode_sparse_w8(p, s)
+                         : saw::launch_paged_decode_sparse_w16(p, s);
+  else
+    err = p.warps <= 8 ? saw::launch_paged_decode_sparse_dims_w8(p, s)
+                       : saw::launch_paged_decode_sparse_dims_w16(p, s);
   return err == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
 }
 

@@ -117,8 +117,77 @@ struct RopeParams {
   int32_t meta_bf16;
 };
 
+// The same with a norm of every q and k row in front.
+struct NormRopeParams : RopeParams {
+  const void* weight[2];        // q's and k's gains [D], or NULL (all 1)
+  int32_t weight_f32;           // 1: the gains are binary32, else of the input type
+  float weight_offset;          // added to every gain
+  float eps;
+};
+
 cudaError_t launch_rope_table(const RopeTableParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- page summaries
+
+// Bytes of a page's summary: every kv-head's codes, then every kv-head's
+// {scale, zero} word.
+__host__ __device__ constexpr int64_t summary_stride(int num_kv_heads, int head_dim) {
+  return (int64_t(num_kv_heads) * (head_dim / 2 + 4) + 15) / 16 * 16;
+}
+
+struct SummaryParams {
+  const uint8_t* k_cache;
+  const int32_t* block_tables;  // [B][max_blocks]
+  const int32_t* seq_lens;      // [B]
+  const int32_t* new_lens;      // [B], or NULL (all tokens are new)
+  uint8_t* summary;             // [num_pages][summary_stride]
+  int32_t* dev_status;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t max_new_len;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t page_shift;
+  int32_t meta_bf16;
+};
+
+cudaError_t launch_page_summary(const SummaryParams& p, int sms, cudaStream_t stream);
+
+struct SelectParams {
+  const uint16_t* q;            // [B][Hq][D] bfloat16 (binary16 if in_f16) bits
+  const uint8_t* summary;
+  const int32_t* block_tables;  // [B][max_blocks]
+  const int32_t* seq_lens;      // [B]
+  int32_t* sel_tables;          // [B][Hkv][max_selected]
+  int32_t* sel_pages;           // the same, or NULL
+  int32_t* sel_lens;            // [B][Hkv]
+  int32_t* dev_status;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t max_seq_len;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t head_dim;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t page_shift;
+  int32_t rotate_k;
+  int32_t block_h;
+  int32_t max_selected;
+  int32_t first_pages;          // always taken
+  int32_t last_pages;           // always taken, >= 1
+  float c_h;
+  int32_t in_f16;
+  int32_t meta_bf16;
+};
+
+constexpr int kSelectMaxPages = 1 << 18;  // pages per sequence
+cudaError_t launch_select_pages(const SelectParams& p, int sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- decode
 
@@ -207,10 +276,10 @@ struct DecodeParams {
   int32_t head_dim;             // 128, or 64 / 256
   int32_t in_f16;               // 1: q, k_new and v_new are binary16
   int32_t meta_bf16;            // 1: the caches' (scale, zero) words are bfloat16
-  // shared-prefix decode only: the groups, and the output type
+  // shared-prefix decode only: the groups
   PrefixSide prefix;
   int32_t max_own_len;          // bound on the tokens behind the prefix
-  uint16_t* out16;              // output in the input type instead of `out`, or NULL
+  uint16_t* out16;              // (also the sparse decode) output in the input type instead of `out`, or NULL
   // 1: head_dim 64, GQA 4: each CTA serves two neighbouring kv-heads as one
   // head_dim-128 "pair" head with 8 q-head columns (part_o rows are 128
   // floats wide, the grid has num_kv_heads / 2 rows)
@@ -228,6 +297,12 @@ cudaError_t launch_paged_decode_shared_w16(const DecodeParams& p, cudaStream_t s
 cudaError_t launch_paged_decode_shared_w8(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_paged_decode_shared_w4(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_paged_decode_dims_w8(const DecodeParams& p, cudaStream_t stream);
+// decode over a list of pages per (sequence, kv-head) (SAW_DECODE_SPARSE)
+cudaError_t launch_paged_decode_sparse_w16(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_paged_decode_sparse_w8(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_paged_decode_sparse_w4(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_paged_decode_sparse_dims_w16(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_paged_decode_sparse_dims_w8(const DecodeParams& p, cudaStream_t stream);
 // head_dim 64 and 256 append (variants.cu); bulk appends run the tiled
 // kernels of quantize_append.cu
 cudaError_t launch_quantize_append_var(const AppendParams& p, int head_dim, cudaStream_t stream);

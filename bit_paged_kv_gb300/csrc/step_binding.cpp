@@ -1,6 +1,7 @@
 // step_binding.cpp -- the Python binding of the serving step's calls
-// (saw_build_tables, saw_rope_table, saw_rope_append, saw_prefix_decode_int4):
-// a CPython extension without torch headers, which reads tensors through their
+// (saw_build_tables, saw_rope_table, saw_rope_append, saw_prefix_decode_int4) and
+// of a sparse decode step (saw_norm_rope_append, saw_page_summary,
+// saw_select_pages, saw_sparse_decode_int4): a CPython extension without torch headers, which reads tensors through their
 // own methods and calls the C ABI by address.
 //
 // These calls run once or more per layer on small batches, where the host's
@@ -25,6 +26,13 @@ struct Entry {
   decltype(&saw_prefix_decode_int4) prefix_decode;
   decltype(&saw_cache_bytes) cache_bytes;
 } g_entry;
+struct SparseEntry {
+  decltype(&saw_norm_rope_append) norm_rope_append;
+  decltype(&saw_page_summary) page_summary;
+  decltype(&saw_select_pages) select_pages;
+  decltype(&saw_sparse_decode_int4) sparse_decode;
+  decltype(&saw_summary_bytes) summary_bytes;
+} g_sparse;
 PyObject *g_int32, *g_f32, *g_bf16, *g_f16;     // dtypes
 PyObject *g_device, *g_raw_stream;              // current device; its current stream
 PyObject *n_dtype, *n_data_ptr, *n_contiguous, *n_numel, *n_shape, *n_stride, *n_get_device,
@@ -307,48 +315,222 @@ PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 18)) return nullptr;
-  PyObject *q = a[0], *k = a[1], *v = a[2];
-  int64_t dev, dims[3], table[2];
-  Rows rq, rk, rv, ro;
+// What the rotary appends have in common.
+struct RopeArgs {
+  Rows q, k, v, out;
   int32_t *positions, *slots, *status;
   int32_t num_pages, page_size, rot_k, rot_v, h, inter, formats, T, D, hq, hkv, max_pos, rope_dim;
   void *cos_sin, *kc, *vc = nullptr, *stream;
-  if (!on_current(k, &dev) || !shape(k, "k", 3, dims) || !formats_of(k, a[17], &formats)) return nullptr;
-  PyObject* dtype = (formats & SAW_FMT_F16_INPUT) ? g_f16 : g_bf16;
-  if (!rows_of(k, dtype, dev, dims[0], dims[2], "k", &rk) || !f32_table(a[4], "cos_sin", dev, table, &cos_sin))
-    return nullptr;
+  int64_t dev;
+  PyObject* dtype;
+};
+// Places of a call's arguments (q, k and v come first).
+struct RopePlaces {
+  int positions, cos_sin, slots, q_out, k_cache, v_cache, num_pages, page_size, rot_k, rot_v, h, inter, status, stream,
+      meta;
+};
+bool rope_args(PyObject* const* a, const RopePlaces& at, RopeArgs* r) {
+  PyObject *q = a[0], *k = a[1], *v = a[2];
+  int64_t dims[3], table[2];
+  if (!on_current(k, &r->dev) || !shape(k, "k", 3, dims) || !formats_of(k, a[at.meta], &r->formats)) return false;
+  const int64_t dev = r->dev;
+  r->dtype = (r->formats & SAW_FMT_F16_INPUT) ? g_f16 : g_bf16;
+  if (!rows_of(k, r->dtype, dev, dims[0], dims[2], "k", &r->k) ||
+      !f32_table(a[at.cos_sin], "cos_sin", dev, table, &r->cos_sin))
+    return false;
   if (q != Py_None) {
-    if (!rows_of(q, dtype, dev, dims[0], dims[2], "q", &rq) ||
-        !rows_of(a[6], dtype, dev, dims[0], dims[2], "q_out", &ro))
-      return nullptr;
-    if (rq.heads != ro.heads) {
+    if (!rows_of(q, r->dtype, dev, dims[0], dims[2], "q", &r->q) ||
+        !rows_of(a[at.q_out], r->dtype, dev, dims[0], dims[2], "q_out", &r->out))
+      return false;
+    if (r->q.heads != r->out.heads) {
       PyErr_SetString(PyExc_ValueError, "q_out must have q's heads");
-      return nullptr;
+      return false;
     }
   }
   if (v != Py_None) {
-    if (!rows_of(v, dtype, dev, dims[0], dims[2], "v", &rv)) return nullptr;
-    if (rv.heads != rk.heads) {
+    if (!rows_of(v, r->dtype, dev, dims[0], dims[2], "v", &r->v)) return false;
+    if (r->v.heads != r->k.heads) {
       PyErr_SetString(PyExc_ValueError, "v must have k's heads");
+      return false;
+    }
+  }
+  if (!words(a[at.positions], "positions", dev, dims[0], &r->positions) ||
+      !words(a[at.slots], "slot_mapping", dev, dims[0], &r->slots) || !int32_of(a[at.num_pages], &r->num_pages) ||
+      !int32_of(a[at.page_size], &r->page_size) || !flag_of(a[at.rot_k], &r->rot_k) ||
+      !flag_of(a[at.rot_v], &r->rot_v) || !int32_of(a[at.h], &r->h) || !flag_of(a[at.inter], &r->inter) ||
+      !status_word(a[at.status], dev, &r->status) || !stream_of(a[at.stream], dev, &r->stream) ||
+      !size32(dims[0], &r->T) || !size32(dims[2], &r->D) || !size32(r->q.heads, &r->hq) ||
+      !size32(r->k.heads, &r->hkv) || !size32(table[0], &r->max_pos) || !size32(table[1], &r->rope_dim))
+    return false;
+  const size_t need = g_entry.cache_bytes(r->num_pages, r->page_size, r->hkv, r->D);
+  return memory(a[at.k_cache], "k_cache", dev, need, &r->kc) &&
+         (v == Py_None || memory(a[at.v_cache], "v_cache", dev, need, &r->vc));
+}
+
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 18)) return nullptr;
+  RopeArgs r;
+  if (!rope_args(a, {3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16, 17}, &r)) return nullptr;
+  return status_of([&] {
+    return g_entry.rope_append(r.q.p, r.q.stride, r.k.p, r.k.stride, r.v.p, r.v.stride, r.positions,
+                               as<float>(r.cos_sin), r.max_pos, r.rope_dim, r.inter, r.slots, r.T, r.hq, r.hkv, r.D,
+                               r.out.p, r.out.stride, r.kc, r.vc, r.num_pages, r.page_size, r.rot_k, r.rot_v, r.h,
+                               r.formats, r.status, r.stream);
+  });
+}
+
+// A norm's gains [D] of the rows' type or float32 (*f32), or None.
+bool gains_of(PyObject* t, PyObject* dtype, int64_t dev, int32_t D, const char* what, void** out, int* f32) {
+  *out = nullptr;
+  *f32 = -1;
+  if (t == Py_None) return true;
+  bool same, wide, cont;
+  int64_t have;
+  if (!on_device(t, what, dev) || !has_dtype(t, dtype, &same) || !has_dtype(t, g_f32, &wide) ||
+      !contiguous(t, &cont) || !call_i64(t, n_numel, &have) || !address(t, out))
+    return false;
+  *f32 = wide;
+  if ((same || wide) && cont && have == D) return true;
+  PyErr_Format(PyExc_ValueError, "%s must be %d contiguous entries of k's type or float32", what, int(D));
+  return false;
+}
+
+PyObject* norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 22)) return nullptr;
+  RopeArgs r;
+  void *wq, *wk;
+  int fq, fk;
+  double eps, offset;
+  if (!rope_args(a, {5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 18, 19, 20, 21}, &r) ||
+      !gains_of(a[3], r.dtype, r.dev, r.D, "q_weight", &wq, &fq) ||
+      !gains_of(a[4], r.dtype, r.dev, r.D, "k_weight", &wk, &fk) || !real_of(a[16], &eps) || !real_of(a[17], &offset))
+    return nullptr;
+  if (fq >= 0 && fk >= 0 && fq != fk) {
+    PyErr_SetString(PyExc_ValueError, "q_weight and k_weight must be of one type");
+    return nullptr;
+  }
+  if (fq == 1 || fk == 1) r.formats |= SAW_FMT_F32_WEIGHT;
+  return status_of([&] {
+    return g_sparse.norm_rope_append(r.q.p, r.q.stride, r.k.p, r.k.stride, r.v.p, r.v.stride, wq, wk, float(offset),
+                                     float(eps), r.positions, as<float>(r.cos_sin), r.max_pos, r.rope_dim, r.inter,
+                                     r.slots, r.T, r.hq, r.hkv, r.D, r.out.p, r.out.stride, r.kc, r.vc, r.num_pages,
+                                     r.page_size, r.rot_k, r.rot_v, r.h, r.formats, r.status, r.stream);
+  });
+}
+
+// A table [rows, width] of int32 on the device with this many rows.
+bool table_of(PyObject* t, const char* what, int64_t dev, int64_t rows, int32_t** out, int32_t* width) {
+  int64_t td[2];
+  if (!shape(t, what, 2, td)) return false;
+  if (td[0] != rows) {
+    PyErr_Format(PyExc_ValueError, "%s must have %lld rows, not %lld", what, (long long)rows, (long long)td[0]);
+    return false;
+  }
+  return words(t, what, dev, -1, out) && size32(td[1], width);
+}
+// Lists [seqs, kv-heads, width] of int32.
+bool lists_of(PyObject* t, const char* what, int64_t dev, int64_t seqs, int32_t hkv, int32_t** out, int32_t* width) {
+  int64_t td[3];
+  if (!shape(t, what, 3, td)) return false;
+  if (td[0] != seqs || td[1] != hkv) {
+    PyErr_Format(PyExc_ValueError, "%s must be [%lld, %d, pages]", what, (long long)seqs, int(hkv));
+    return false;
+  }
+  return words(t, what, dev, -1, out) && size32(td[2], width);
+}
+
+PyObject* page_summary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 13)) return nullptr;
+  int64_t dev, seqs;
+  int32_t *tables, *seq_lens, *new_lens, *status;
+  int32_t max_new, hkv, D, num_pages, page_size, formats, B, width;
+  void *kc, *summary, *stream;
+  if (!on_current(a[0], &dev) || !words(a[2], "seq_lens", dev, -1, &seq_lens, &seqs) ||
+      !table_of(a[1], "block_tables", dev, seqs, &tables, &width) || !words(a[3], "new_lens", dev, seqs, &new_lens) ||
+      !int32_of(a[4], &max_new) || !int32_of(a[5], &hkv) || !int32_of(a[6], &D) || !int32_of(a[7], &num_pages) ||
+      !int32_of(a[8], &page_size) || !status_word(a[10], dev, &status) || !stream_of(a[11], dev, &stream) ||
+      !flag_of(a[12], &formats) || !size32(seqs, &B) ||
+      !memory(a[0], "k_cache", dev, g_entry.cache_bytes(num_pages, page_size, hkv, D), &kc) ||
+      !memory(a[9], "summary", dev, g_sparse.summary_bytes(num_pages, hkv, D), &summary))
+    return nullptr;
+  return status_of([&] {
+    return g_sparse.page_summary(kc, tables, width, seq_lens, new_lens, B, max_new, hkv, D, num_pages, page_size,
+                                 summary, formats ? SAW_FMT_BF16_META : 0, status, stream);
+  });
+}
+
+PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 18)) return nullptr;
+  PyObject* q = a[0];
+  int64_t dev, dims[3];
+  int32_t *tables, *seq_lens, *sel_tables, *sel_lens, *sel_pages = nullptr, *status;
+  int32_t max_len, hkv, num_pages, page_size, rot_k, h, first, last, formats, B, hq, D, width, take, take2;
+  void *pq, *summary, *stream;
+  bool cq;
+  if (!on_current(q, &dev) || !shape(q, "q", 3, dims) || !formats_of(q, a[17], &formats) || !contiguous(q, &cq) ||
+      !address(q, &pq) || !size32(dims[0], &B) || !size32(dims[1], &hq) || !size32(dims[2], &D))
+    return nullptr;
+  if (!cq) {
+    PyErr_SetString(PyExc_ValueError, "q must be contiguous");
+    return nullptr;
+  }
+  if (!table_of(a[2], "block_tables", dev, dims[0], &tables, &width) ||
+      !words(a[3], "seq_lens", dev, dims[0], &seq_lens) || !int32_of(a[4], &max_len) || !int32_of(a[5], &hkv) ||
+      !int32_of(a[6], &num_pages) || !int32_of(a[7], &page_size) || !flag_of(a[8], &rot_k) || !int32_of(a[9], &h) ||
+      !int32_of(a[10], &first) || !int32_of(a[11], &last) ||
+      !lists_of(a[12], "sel_tables", dev, dims[0], hkv, &sel_tables, &take) ||
+      !words(a[13], "sel_lens", dev, dims[0] * hkv, &sel_lens) || !status_word(a[15], dev, &status) ||
+      !stream_of(a[16], dev, &stream) ||
+      !memory(a[1], "summary", dev, g_sparse.summary_bytes(num_pages, hkv, D), &summary))
+    return nullptr;
+  if (a[14] != Py_None) {
+    if (!lists_of(a[14], "sel_pages", dev, dims[0], hkv, &sel_pages, &take2)) return nullptr;
+    if (take2 != take) {
+      PyErr_SetString(PyExc_ValueError, "sel_pages must be of sel_tables' shape");
       return nullptr;
     }
   }
-  if (!words(a[3], "positions", dev, dims[0], &positions) || !words(a[5], "slot_mapping", dev, dims[0], &slots) ||
-      !int32_of(a[9], &num_pages) || !int32_of(a[10], &page_size) || !flag_of(a[11], &rot_k) ||
-      !flag_of(a[12], &rot_v) || !int32_of(a[13], &h) || !flag_of(a[14], &inter) ||
-      !status_word(a[15], dev, &status) || !stream_of(a[16], dev, &stream) || !size32(dims[0], &T) ||
-      !size32(dims[2], &D) || !size32(rq.heads, &hq) || !size32(rk.heads, &hkv) || !size32(table[0], &max_pos) ||
-      !size32(table[1], &rope_dim))
+  return status_of([&] {
+    return g_sparse.select_pages(pq, summary, tables, width, seq_lens, B, max_len, hq, hkv, D, num_pages, page_size,
+                                 rot_k, h, take, first, last, sel_tables, sel_pages, sel_lens, formats, status, stream);
+  });
+}
+
+PyObject* sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 18)) return nullptr;
+  PyObject *q = a[0], *out = a[12], *ws = a[13];
+  int64_t dev, dims[3], od[3], bytes = 0;
+  int32_t *tables, *lens, *status;
+  int32_t max_len, hkv, num_pages, page_size, rot_k, rot_v, h, formats, B, hq, D, take;
+  double scale;
+  void *pq, *kc, *vc, *po, *pw, *stream;
+  bool cq, co, same, f32;
+  if (!on_current(q, &dev) || !shape(q, "q", 3, dims) || !formats_of(q, a[17], &formats) ||
+      !on_device(out, "out", dev) || !shape(out, "out", 3, od) || !contiguous(q, &cq) || !contiguous(out, &co) ||
+      !has_dtype(out, (formats & SAW_FMT_F16_INPUT) ? g_f16 : g_bf16, &same) || !has_dtype(out, g_f32, &f32))
+    return nullptr;
+  if (!same && !f32) {
+    PyErr_SetString(PyExc_ValueError, "out must be float32 or q's type");
+    return nullptr;
+  }
+  if (same) formats |= SAW_FMT_OUT_INPUT;
+  if (!cq || !co || dims[0] != od[0] || dims[1] != od[1] || dims[2] != od[2]) {
+    PyErr_SetString(PyExc_ValueError, "q and out must be contiguous and of one shape");
+    return nullptr;
+  }
+  if (!int32_of(a[5], &max_len) || !int32_of(a[6], &hkv) ||
+      !lists_of(a[3], "sel_tables", dev, dims[0], hkv, &tables, &take) ||
+      !words(a[4], "sel_lens", dev, dims[0] * hkv, &lens) || !int32_of(a[7], &num_pages) ||
+      !int32_of(a[8], &page_size) || !flag_of(a[9], &rot_k) || !flag_of(a[10], &rot_v) || !int32_of(a[11], &h) ||
+      !memory(ws, "workspace", dev, 0, &pw, &bytes) || !real_of(a[14], &scale) || !status_word(a[15], dev, &status) ||
+      !stream_of(a[16], dev, &stream) || !address(q, &pq) || !address(out, &po) || !size32(dims[0], &B) ||
+      !size32(dims[1], &hq) || !size32(dims[2], &D))
     return nullptr;
   const size_t need = g_entry.cache_bytes(num_pages, page_size, hkv, D);
-  if (!memory(a[7], "k_cache", dev, need, &kc) || (v != Py_None && !memory(a[8], "v_cache", dev, need, &vc)))
-    return nullptr;
+  if (!memory(a[1], "k_cache", dev, need, &kc) || !memory(a[2], "v_cache", dev, need, &vc)) return nullptr;
   return status_of([&] {
-    return g_entry.rope_append(rq.p, rq.stride, rk.p, rk.stride, rv.p, rv.stride, positions, as<float>(cos_sin),
-                               max_pos, rope_dim, inter, slots, T, hq, hkv, D, ro.p, ro.stride, kc, vc, num_pages,
-                               page_size, rot_k, rot_v, h, formats, status, stream);
+    return g_sparse.sparse_decode(pq, kc, vc, tables, take, lens, B, max_len, hq, hkv, D, num_pages, page_size, rot_k,
+                                  rot_v, h, float(scale), po, pw, size_t(bytes), formats, status, stream);
   });
 }
 
@@ -416,12 +598,34 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// (five entry points' addresses; after init, whose other arguments hold here too)
+PyObject* init_sparse(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 5)) return nullptr;
+  uint64_t at[5];
+  for (int i = 0; i < 5; ++i) {
+    at[i] = PyLong_AsUnsignedLongLong(a[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  g_sparse = {reinterpret_cast<decltype(SparseEntry::norm_rope_append)>(at[0]),
+              reinterpret_cast<decltype(SparseEntry::page_summary)>(at[1]),
+              reinterpret_cast<decltype(SparseEntry::select_pages)>(at[2]),
+              reinterpret_cast<decltype(SparseEntry::sparse_decode)>(at[3]),
+              reinterpret_cast<decltype(SparseEntry::summary_bytes)>(at[4])};
+  Py_RETURN_NONE;
+}
+
 PyMethodDef g_methods[] = {
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(init)), METH_FASTCALL, nullptr},
     {"build_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(build_tables)), METH_FASTCALL, nullptr},
     {"rope_table", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_table)), METH_FASTCALL, nullptr},
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_append)), METH_FASTCALL, nullptr},
     {"prefix_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_decode)), METH_FASTCALL, nullptr},
+    {"init_sparse", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(init_sparse)), METH_FASTCALL, nullptr},
+    {"norm_rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rope_append)), METH_FASTCALL,
+     nullptr},
+    {"page_summary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(page_summary)), METH_FASTCALL, nullptr},
+    {"select_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(select_pages)), METH_FASTCALL, nullptr},
+    {"sparse_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sparse_decode)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_saw_step", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

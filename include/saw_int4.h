@@ -597,6 +597,165 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
                                int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------
+ * A sparse decode step: at long contexts a query attends over a few pages
+ * that a cheap score picks for it, so that a step reads a summary of the cache
+ * (1/17 to 1/65 of K) and the chosen pages instead of all of it.  A page is the block.
+ * Models that norm q and k per head append with saw_norm_rope_append;
+ * saw_page_summary keeps the mean key of every complete page, whichever call
+ * appended it; saw_select_pages and saw_sparse_decode_int4 follow per layer.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * saw_norm_rope_append -- a norm of every q and k head, then saw_rope_append.
+ *
+ * q_weight, k_weight  device [head_dim], 16-byte aligned: gains of the input type, or of
+ *               float32 with SAW_FMT_F32_WEIGHT in `formats`.  NULL: all 1
+ *               (weight_offset is then not used).
+ * weight_offset finite; added to every gain: 0, or 1 for gains kept as w - 1.
+ * eps           positive and finite.
+ * q_out may be q itself, as in saw_rope_append, whose other arguments, limits
+ * and errors hold.  v is not normed.
+ *
+ * Per row x of q or k, in binary32, each step rounded once: ss = the sum of
+ * the squares by a binary tree over the element index (neighbours, then pairs
+ * of neighbours, ...), r = 1 / sqrt(ss / head_dim + eps), y = (x r) g with g =
+ * w + weight_offset (no second product without weights).  The whole head is normed, also where only part of it is
+ * turned.  y is not rounded to 16 bits before the turn, and the rest is
+ * saw_rope_append's rule, so the bytes are fully determined.  Squares have to
+ * be within binary32.
+ */
+#define SAW_FMT_F32_WEIGHT 8
+int32_t saw_norm_rope_append(const void* q, int64_t q_token_stride, const void* k,
+                             int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                             const void* q_weight, const void* k_weight, float weight_offset,
+                             float eps, const int32_t* positions, const float* cos_sin,
+                             int32_t max_pos, int32_t rope_dim, int32_t interleaved,
+                             const int32_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, void* q_out,
+                             int64_t q_out_token_stride, void* k_cache, void* v_cache,
+                             int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                             int32_t rotate_v, int32_t block_h, int32_t formats,
+                             int32_t* dev_status, void* stream);
+
+/*
+ * Bytes of the summaries of one layer's pages: [num_pages][stride], stride =
+ * num_kv_heads * (head_dim/2 + 4) rounded up to 16.  A page's summary holds
+ * every kv-head's packed codes (head_dim/2 bytes each), then every kv-head's
+ * {scale, zero} word, in the cache's metadata format; a row dequantizes as
+ * code*scale + zero, like a cache row.  0 for a nonpositive argument.
+ */
+size_t saw_summary_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * saw_page_summary -- the mean key of every page that a step completed.  Call
+ * it after the step's append (any of them), with the same lengths.
+ *
+ * seq_lens      device int32 [num_seqs]: cached tokens, the new ones included.
+ * new_lens      device int32 [num_seqs]: tokens that the step appended, or NULL
+ *               (all of them; a count above seq_lens counts as all too).
+ * max_new_len   host bound on the smaller of the two; sizes the grid.
+ * summary       device, saw_summary_bytes(...), 16-byte aligned.  Summaries go by physical page, so
+ *               forks of a sequence share them.
+ * Pages floor((L - n) / page_size) to floor(L / page_size) - 1 of a sequence
+ * are written; a page that is not full has no summary (and none is needed: the
+ * last page is always taken).
+ *
+ * Per (page, kv-head): A_d = sum of code*scale, Z = sum of the zeros, each the
+ * even tokens in order plus the odd tokens in order; mean_d = (A_d + Z) /
+ * page_size; the row is quantized by saw_quantize_append's rule (unrotated: it
+ * is in the cache's domain already).  Each step is one binary32 rounding, so the bytes are
+ * fully determined.
+ *
+ * formats: SAW_FMT_BF16_META or 0.  A length below 0 or beyond
+ * max_blocks_per_seq pages, or more new tokens than max_new_len: the sequence
+ * is skipped and SAW_ERR_DEVICE_INDEX reported; so is a page id out of range.
+ * head_dim 64, 128 or 256; page_size 16, 32 or 64; at most 65535 sequences and
+ * kv-heads, and 2^30 pages x kv-heads of a step's sequence (else SAW_ERR_UNSUPPORTED).
+ */
+int32_t saw_page_summary(const void* k_cache, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         const int32_t* new_lens, int32_t num_seqs, int32_t max_new_len,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                         int32_t page_size, void* summary, int32_t formats, int32_t* dev_status,
+                         void* stream);
+
+/*
+ * saw_select_pages -- for each (sequence, kv-head), the pages that its queries
+ * attend over: the first first_pages and the last last_pages, and of the
+ * others those with the best scores, max_selected in all.  A sequence of at
+ * most max_selected pages keeps them all.
+ *
+ * q             device bfloat16 (binary16 with SAW_FMT_F16_INPUT)
+ *               [num_seqs][num_q_heads][head_dim], 16-byte aligned.
+ * summary       saw_page_summary's, of every page but the last of each sequence.
+ * max_seq_len   host bound on seq_lens; max_blocks_per_seq pages must hold it.
+ * last_pages    at least 1; first_pages + last_pages at most max_selected.
+ * sel_tables    device int32 [num_seqs][num_kv_heads][max_selected]: physical
+ *               ids from block_tables, in the order of the sequence, -1 behind
+ *               the last: a block table per (sequence, kv-head).
+ * sel_pages     the same as page numbers of the sequence, or NULL.
+ * sel_lens      device int32 [num_seqs][num_kv_heads]: tokens in those pages.
+ *
+ * Per q-head: q' = H q / sqrt(h) by saw_quantize_append's butterfly (q itself with rotate_k 0), qs =
+ * max|q'| / 127, m_d = round-half-even(q'_d (1/qs)) in -127 .. 127 (0 where qs is
+ * below 2^-126); with the summary's codes n, scale s and zero z: score = qs (s
+ * (sum m n) + z (sum m)), the largest over the kv-head's q-heads.  The sums are whole
+ * numbers and exact, every other step one binary32 rounding, so the lists are
+ * fully determined: equal scores (-0 and 0 are equal, a NaN counts as -infinity) go to the lower page.
+ *
+ * A length below 0 or above max_seq_len is treated as 0 (an empty list) and
+ * reported as SAW_ERR_DEVICE_INDEX; a page id outside [0, num_pages) among
+ * the scored pages scores -infinity and is reported; ids are passed on as they
+ * are.  Outputs must not overlap inputs.
+ * formats: SAW_FMT_F16_INPUT, SAW_FMT_BF16_META.  head_dim 64, 128 or 256;
+ * page_size 16, 32 or 64; at most 8 q-heads per kv-head, 65535 sequences and
+ * kv-heads and 262144 pages in max_seq_len (else SAW_ERR_UNSUPPORTED).
+ */
+int32_t saw_select_pages(const void* q, const void* summary, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                         int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                         int32_t block_h, int32_t max_selected, int32_t first_pages,
+                         int32_t last_pages, int32_t* sel_tables, int32_t* sel_pages,
+                         int32_t* sel_lens, int32_t formats, int32_t* dev_status, void* stream);
+
+/*
+ * Workspace bytes of saw_sparse_decode_int4 for these sizes on the current
+ * device; 0 when it needs none or the sizes are bad.  Zero-fill a workspace
+ * before its first use; each call leaves it ready for the next, of whatever
+ * sizes (up to 131072 (sequence, kv-head) pairs; a larger batch wants one of
+ * its own).  It is not one for the other decode calls, whose layouts differ.
+ */
+size_t saw_sparse_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t page_size, int32_t max_sel_len);
+
+/*
+ * saw_sparse_decode_int4 -- saw_paged_decode_int4 with a list of pages per
+ * (sequence, kv-head) instead of one per sequence.
+ *
+ * sel_tables    device int32 [num_seqs][num_kv_heads][max_selected] page ids
+ *               (saw_select_pages, or the caller's own; a page listed twice
+ *               counts twice).
+ * sel_lens      device int32 [num_seqs][num_kv_heads]: tokens, all pages full
+ *               but the last.  0: a zero output row for the kv-head's q-heads.
+ * max_sel_len   host bound on sel_lens, at most max_selected * page_size.
+ * out           [num_seqs][num_q_heads][head_dim]: float32, or with
+ *               SAW_FMT_OUT_INPUT in `formats` the input type (one rounding).
+ * workspace     saw_sparse_decode_workspace_bytes(...) bytes, 16-byte aligned.
+ *               Calls sharing one must be ordered (one stream).
+ * Other arguments, the arithmetic and the errors as saw_paged_decode_int4_ex.
+ */
+int32_t saw_sparse_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* sel_tables, int32_t max_selected,
+                               const int32_t* sel_lens, int32_t num_seqs, int32_t max_sel_len,
+                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t num_pages, int32_t page_size, int32_t rotate_k,
+                               int32_t rotate_v, int32_t block_h, float sm_scale, void* out,
+                               void* workspace, size_t workspace_bytes, int32_t formats,
+                               int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
  * BF16 baseline.  gist.science "SAW-INT4: System-Aware 4-Bit KV-Cache
  * Quantization for Real-World LLM Serving", s.4 measures SAW-INT4's serving
  * throughput against an unquantized BF16 KV cache.  These two calls are that
