@@ -14,10 +14,12 @@
 // carries 2^-4), m as binary16.  |I| <= 127 15 D < 2^24 in units of 2^-24, so
 // the binary32 sums are exact in any order.
 //
-// A cluster of CTAs takes one (sequence, kv-head); each scores its run of the
-// pages and keeps their keys in shared memory.  The threshold is found digit by
-// digit from histograms that the CTAs read from one another, then every CTA
-// writes its part of the list in order.
+// One CTA takes one (sequence, kv-head), or a cluster of them a run of its pages
+// each; the pages' keys stay in shared memory.  A warp scores 32 pages at a time,
+// the next 32 pages' rows under way meanwhile.  The threshold comes from one
+// histogram of the scores between their extremes (radix digits of the keys would
+// put nearly all of them in a few bins) and a ranking of the keys in its bin;
+// where that bin holds too many (ties, far outliers), digit by digit.
 #include <cooperative_groups.h>
 
 #include "saw_device.cuh"
@@ -31,10 +33,13 @@ namespace cg = cooperative_groups;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBins = 256;
-constexpr int kTile = 16;                            // pages per MMA
+constexpr int ctas_per_sm(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }  // what the registers of two strips leave
+constexpr int kAlone = 512;                          // pages that a CTA takes before more join it
+constexpr int kBins = 1024;
+constexpr int kCands = 256;                          // keys ranked against one another
+constexpr int kStrip = 32;                           // pages per warp and step: two MMA tiles
 constexpr int kMaxChunk = kSelectMaxPages / 8;       // pages per CTA
-static_assert(kMaxChunk % kTile == 0, "whole tiles");
+static_assert(kMaxChunk % kStrip == 0, "whole strips");
 
 // The larger, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -48,19 +53,64 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
 struct Shared {
+  alignas(16) uint32_t hist[kBins];                  // (read four bins at a time)
   float qs[kMaxGroup], j[kMaxGroup];
-  uint32_t hist[4][kBins];
+  float least[kWarps], most[kWarps];                 // each warp's finite scores
+  float range[2];                                    // this CTA's
+  uint32_t cands, cand[kCands];                      // this CTA's keys in the threshold's bin
+  uint32_t all[kCands];                              // the cluster's
   uint32_t count[2];                                 // this CTA's keys above the threshold, and equal to it
   uint32_t warp_count[kWarps][2];
-  uint32_t digit, want;
+  uint32_t bin, want, key;
 };
 
+// Thread t's share of a histogram's bins, largest first: the bin that holds the
+// want-th largest key, and how many are wanted of that bin.  v: its N bins.
+template <int N>
+__device__ __forceinline__ void find_bin(Shared& sh, const uint32_t (&v)[N], uint32_t want, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  uint32_t sum = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) sum += v[j];
+  uint32_t above = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(kAll, above, d);
+    if (lane >= d) above += o;
+  }
+  if (lane == 31) sh.warp_count[warp][0] = above;
+  above -= sum;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) above += w < warp ? sh.warp_count[w][0] : 0u;
+  if (above < want && want <= above + sum) {         // (one thread)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (above < want && want <= above + v[j]) {
+        sh.bin = uint32_t(kThreads * N - 1 - N * tid - j);
+        sh.want = want - above;
+      }
+      above += v[j];
+    }
+  }
+  __syncthreads();
+}
+
 template <int D, bool BFM>
-__global__ void __launch_bounds__(kThreads) select_pages_kernel(const SelectParams p, int chunk) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
+    select_pages_kernel(const SelectParams p, int chunk) {
   pdl_wait_then_release();
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  auto sync_all = [&] {
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+  };
   constexpr int kKS = D / 16;                        // k-steps
   constexpr int kE = D / 32;
   constexpr int kW = D / 32;                         // words of a row per thread-in-group
@@ -157,11 +207,12 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const SelectPara
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
     if (lane == 0) {
-      sh.qs[h] = qs;
+      sh.qs[h] = h < G ? qs : __uint_as_float(0x7FC00000u);  // (a NaN's scores are passed over)
       sh.j[h] = float(sum);
     }
   }
-  for (int i = tid; i < 4 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+  if (tid == 0) sh.cands = 0;
   __syncthreads();
   uint32_t b[kKS][2];
 #pragma unroll
@@ -170,97 +221,225 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const SelectPara
     b[t][0] = v.x;
     b[t][1] = v.y;
   }
-  const float qs0 = sh.qs[2 * c], qs1 = sh.qs[2 * c + 1], j0 = sh.j[2 * c], j1 = sh.j[2 * c + 1];
+  const float2 qs = make_float2(sh.qs[2 * c], sh.qs[2 * c + 1]), jj = make_float2(sh.j[2 * c], sh.j[2 * c + 1]);
 
   // ---- keys of this CTA's run of the pages
   const int begin = min(rank * chunk, mid), count = min(mid - begin, chunk);
+  const int32_t* run = bt + lo + begin;
   const int64_t stride = summary_stride(hkv, D);
+  const uint8_t* codes = p.summary + kvh * (D / 2) + c * (D / 8);
+  const uint8_t* words = p.summary + hkv * (D / 2) + 4 * kvh;
+  struct Rows {
+    uint32_t w[4][kW], m[4];                         // rows g, g + 8, g + 16, g + 24 of a strip
+  };
   bool bad = false;
-  for (int t0 = warp * kTile; t0 < count; t0 += kWarps * kTile) {
-    uint32_t w[2][kW], meta[2];
+  // this lane's page of the strip at i0 (-1: none, or bad)
+  auto page_of = [&](int i0) { return i0 + lane < count ? run[i0 + lane] : -1; };
+  // Loads the strip's rows; a page that is not there reads the first one that is.
+  // Returns whether this lane's is.
+  auto load = [&](int id, Rows& r) {
+    const bool ok = uint32_t(id) < uint32_t(p.num_pages);
+    const uint32_t there = __ballot_sync(kAll, ok);
+    if (there == 0) return false;
+    const int any = __shfl_sync(kAll, id, __ffs(int(there)) - 1);
+    if (!ok) id = any;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = t0 + g + 8 * u;
-      const int id = i < count ? bt[lo + begin + i] : -1;
-      const bool ok = id >= 0 && id < p.num_pages;
-      bad = bad || (i < count && !ok);
-      const uint8_t* s = p.summary + id * stride;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(s + kvh * (D / 2)) + kW * c;
+    for (int u = 0; u < 4; ++u) {
+      const int64_t off = __shfl_sync(kAll, id, g + 8 * u) * stride;
+      const uint8_t* src = codes + off;
+      if constexpr (kW == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        r.w[u][0] = x.x; r.w[u][1] = x.y;
+      } else {
 #pragma unroll
-      for (int k = 0; k < kW; ++k) w[u][k] = ok ? src[k] : 0u;
-      // (NaN: counts as -infinity)
-      meta[u] = ok ? *reinterpret_cast<const uint32_t*>(s + hkv * (D / 2) + 4 * kvh) : 0xFFFFFFFFu;
-    }
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < kW; ++k)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t x = hh ? w[0][k] >> 8 : w[0][k], y = hh ? w[1][k] >> 8 : w[1][k];
-        const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
-        mma_16816(d, a, b[2 * k + hh][0], b[2 * k + hh][1]);
+        for (int k = 0; k < kW; k += 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + k / 4);
+          r.w[u][k] = x.x; r.w[u][k + 1] = x.y; r.w[u][k + 2] = x.z; r.w[u][k + 3] = x.w;
+        }
       }
+      r.m[u] = __ldg(reinterpret_cast<const uint32_t*>(words + off));
+    }
+    return ok;
+  };
+  float least = INFINITY, most = -INFINITY;
+  auto score = [&](int i0, const Rows& r, bool ok) {
+    float v[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float s = meta_lo(meta[u], BFM), z = meta_hi(meta[u], BFM);
-      const float i0 = __fmul_rn(d[2 * u], 0x1p24f), i1 = __fmul_rn(d[2 * u + 1], 0x1p24f);
-      float best = -INFINITY;                        // (fmaxf passes over NaN)
-      if (2 * c < G) best = fmaxf(best, __fmul_rn(qs0, __fadd_rn(__fmul_rn(s, i0), __fmul_rn(z, j0))));
-      if (2 * c + 1 < G) best = fmaxf(best, __fmul_rn(qs1, __fadd_rn(__fmul_rn(s, i1), __fmul_rn(z, j1))));
-      best = fmaxf(best, __shfl_xor_sync(kAll, best, 1));
-      best = fmaxf(best, __shfl_xor_sync(kAll, best, 2));
-      const int i = t0 + g + 8 * u;
-      if (c == 0 && i < count) keys[i] = key_of(best);
+    for (int t = 0; t < 2; ++t) {
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < kW; ++k)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t x = hh ? r.w[2 * t][k] >> 8 : r.w[2 * t][k];
+          const uint32_t y = hh ? r.w[2 * t + 1][k] >> 8 : r.w[2 * t + 1][k];
+          const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+          mma_16816(d, a, b[2 * k + hh][0], b[2 * k + hh][1]);
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t m = r.m[2 * t + u];
+        float s = meta_lo(m, BFM);
+        const float z = meta_hi(m, BFM);
+        float2 i = make_float2(d[2 * u], d[2 * u + 1]);
+        // I = 2^24 d, exactly; a binary16 scale takes the factor as well
+        if constexpr (BFM) i = mul2(i, make_float2(0x1p24f, 0x1p24f));
+        else s *= 0x1p24f;
+        const float2 x = mul2(qs, add2(mul2(make_float2(s, s), i), mul2(make_float2(z, z), jj)));
+        v[2 * t + u] = fmaxf(x.x, x.y);              // (fmaxf passes over a NaN)
+      }
+    }
+    // over the thread-in-group: c is left with row g + 8 c
+    const bool odd = c & 1, high = c & 2;
+    const float a = fmaxf(odd ? v[1] : v[0], __shfl_xor_sync(kAll, odd ? v[0] : v[1], 1));
+    const float e = fmaxf(odd ? v[3] : v[2], __shfl_xor_sync(kAll, odd ? v[2] : v[3], 1));
+    float best = fmaxf(high ? e : a, __shfl_xor_sync(kAll, high ? a : e, 2));
+    best = fmaxf(best, -INFINITY);
+    // lane's own page's score (lane = g + 8 c of the strip is at lane 4 g + c)
+    best = __shfl_sync(kAll, best, 4 * (lane & 7) + (lane >> 3));
+    if (!ok) best = -INFINITY;
+    const int i = i0 + lane;
+    if (i < count) {
+      bad = bad || !ok;
+      keys[i] = key_of(best);
+      if (fabsf(best) < INFINITY) {
+        least = fminf(least, best);
+        most = fmaxf(most, best);
+      }
+    }
+  };
+  {
+    Rows r[2];
+    constexpr int kStep = kWarps * kStrip;
+    int i0 = warp * kStrip;
+    int next = page_of(i0 + kStep);
+    bool ok0 = i0 < count && load(page_of(i0), r[0]), ok1;
+    // (the branches are the same in every lane of a warp)
+    for (; i0 < count; i0 += 2 * kStep) {
+      const int after = page_of(i0 + 2 * kStep);
+      ok1 = i0 + kStep < count && load(next, r[1]);
+      score(i0, r[0], ok0);
+      next = page_of(i0 + 3 * kStep);
+      ok0 = i0 + 2 * kStep < count && load(after, r[0]);
+      if (i0 + kStep < count) score(i0 + kStep, r[1], ok1);
     }
   }
   if (bad) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    least = fminf(least, __shfl_xor_sync(kAll, least, d));
+    most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
+  }
+  if (lane == 0) {
+    sh.least[warp] = least;
+    sh.most[warp] = most;
+  }
   __syncthreads();
-
-  // ---- the threshold: the want-th largest key of the cluster, digit by digit
-  uint32_t prefix = 0, mask = 0, need = uint32_t(want);
-#pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int i = tid; i < count; i += kThreads) {
-      const uint32_t k = keys[i];
-      if ((k & mask) == prefix) atomicAdd(&sh.hist[pass][(k >> shift) & 255u], 1u);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    least = fminf(least, sh.least[w]);
+    most = fmaxf(most, sh.most[w]);
+  }
+  if (ctas > 1) {
+    if (tid == 0) {
+      sh.range[0] = least;
+      sh.range[1] = most;
     }
     cluster.sync();
-    if (warp == 0) {
-      // eight bins per lane, from the top; lane 0 has the largest digits
-      uint32_t v[8], sum = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const float* o = cluster.map_shared_rank(sh.range, r);
+      least = fminf(least, o[0]);
+      most = fmaxf(most, o[1]);
+    }
+  }
+
+  // ---- the threshold: the want-th largest key of the cluster.  A score's bin
+  // grows with the score: a difference and a product, each rounded monotonously.
+  const float scale = float(kBins - 1) / (most - least);
+  bool done = false;
+  uint32_t prefix = 0, need = uint32_t(want);
+  if (most - least < INFINITY && scale < INFINITY) {  // (not: one value, or none that is finite)
+    auto bin_of = [&](uint32_t key) {
+      return min(__float2int_rz(fmaxf(__fmul_rn(__fsub_rn(score_of(key), least), scale), 0.0f)), kBins - 1);
+    };
+    for (int i = tid; i < count; i += kThreads) atomicAdd(&sh.hist[bin_of(keys[i])], 1u);
+    sync_all();
+    constexpr int kPer = kBins / kThreads;
+    uint32_t v[kPer];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0;
-      for (int r = 0; r < ctas; ++r) {
-        const uint32_t* h = cluster.map_shared_rank(sh.hist[pass], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += h[255 - 8 * lane - j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += v[j];
-      uint32_t above = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t o = __shfl_up_sync(kAll, above, d);
-        if (lane >= d) above += o;
-      }
-      above -= sum;                                  // keys in larger digits
-      if (above < need && need <= above + sum) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (above < need && need <= above + v[j]) {
-            sh.digit = uint32_t(255 - 8 * lane - j);
-            sh.want = need - above;
-          }
-          above += v[j];
-        }
+    for (int j = 0; j < kPer; ++j) v[j] = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const uint4 h = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(sh.hist, r) + kBins - kPer * (tid + 1));
+      static_assert(kPer == 4, "a thread's bins in one load");
+      v[0] += h.w; v[1] += h.z; v[2] += h.y; v[3] += h.x;
+    }
+    find_bin(sh, v, need, tid);
+    const int bin = int(sh.bin);
+    need = sh.want;
+    for (int i = tid; i < count; i += kThreads) {
+      const uint32_t k = keys[i];
+      if (bin_of(k) == bin) {
+        const uint32_t at = atomicAdd(&sh.cands, 1u);
+        if (at < kCands) sh.cand[at] = k;
       }
     }
+    sync_all();
+    uint32_t n_all = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const uint32_t m = *cluster.map_shared_rank(&sh.cands, r);
+      const uint32_t* o = cluster.map_shared_rank(sh.cand, r);
+      for (uint32_t i = tid; i < m && n_all + i < kCands; i += kThreads) sh.all[n_all + i] = o[i];
+      n_all += m;
+    }
     __syncthreads();
-    prefix |= sh.digit << shift;
-    mask |= 255u << shift;
-    need = sh.want;
+    done = n_all <= kCands;
+    if (done) {
+      if (tid < int(n_all)) {
+        const uint32_t k = sh.all[tid];
+        uint32_t gt = 0, eq = 0;
+        for (uint32_t i = 0; i < n_all; ++i) {
+          gt += sh.all[i] > k;
+          eq += sh.all[i] == k;
+        }
+        if (gt < need && need <= gt + eq) {          // (equal keys write the same)
+          sh.key = k;
+          sh.want = need - gt;
+        }
+      }
+      __syncthreads();
+      prefix = sh.key;
+      need = sh.want;
+    } else {
+      need = uint32_t(want);
+    }
+  }
+  if (!done) {
+    // (every CTA of the cluster is past its reads of the others' histograms)
+    uint32_t mask = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
     __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      static_assert(kBins == 4 * 256 && kThreads == 256, "a histogram per pass, a bin per thread");
+      uint32_t* hist = sh.hist + 256 * pass;
+      for (int i0 = 0; i0 < count; i0 += kThreads) {
+        const uint32_t k = i0 + tid < count ? keys[i0 + tid] : 0u;
+        const bool in = i0 + tid < count && (k & mask) == prefix;
+        // one count per digit and warp: equal keys would queue up
+        const uint32_t digit = in ? (k >> shift) & 255u : 256u;
+        const uint32_t same = __match_any_sync(kAll, digit);
+        if (in && lane == __ffs(int(same)) - 1) atomicAdd(&hist[digit], uint32_t(__popc(same)));
+      }
+      sync_all();
+      uint32_t v[1] = {0};
+      for (int r = 0; r < ctas; ++r) v[0] += cluster.map_shared_rank(hist, r)[255 - tid];
+      find_bin(sh, v, need, tid);
+      prefix |= sh.bin << shift;
+      mask |= 255u << shift;
+      need = sh.want;
+      __syncthreads();
+    }
   }
 
   // ---- the list: keys above the threshold, and `need` of those equal to it,
@@ -283,18 +462,20 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const SelectPara
     for (int w = 0; w < kWarps; ++w) s += sh.warp_count[w][tid];
     sh.count[tid] = s;
   }
-  cluster.sync();
   gt = eq = 0;
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* o = cluster.map_shared_rank(sh.count, r);
-    gt += o[0];
-    eq += o[1];
+  if (ctas > 1) {
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      const uint32_t* o = cluster.map_shared_rank(sh.count, r);
+      gt += o[0];
+      eq += o[1];
+    }
   }
   for (int w = 0; w < warp; ++w) {
     gt += sh.warp_count[w][0];
     eq += sh.warp_count[w][1];
   }
-  cluster.sync();  // no CTA ends while another reads its memory
+  if (ctas > 1) cluster.sync();  // no CTA ends while another reads its memory
   const uint32_t below = (1u << lane) - 1u;
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const uint32_t k = i0 + lane < w1 ? keys[i0 + lane] : 0u;
@@ -312,10 +493,10 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
   const int max_pages = (p.max_seq_len + p.page_size - 1) / p.page_size;
   const int64_t units = int64_t(p.num_seqs) * p.num_kv_heads;
   int ctas = 1;
-  while (ctas < 8 && units * ctas < sms && max_pages > ctas * 256) ctas *= 2;
+  while (ctas < 8 && units * ctas < sms && max_pages > ctas * kAlone) ctas *= 2;
   while (max_pages > ctas * kMaxChunk) ctas *= 2;
   const int mid = max_pages > 0 ? max_pages : 1;
-  const int chunk = ((mid + ctas - 1) / ctas + kTile - 1) / kTile * kTile;
+  const int chunk = ((mid + ctas - 1) / ctas + kStrip - 1) / kStrip * kStrip;
   auto kernel = select_pages_kernel<D, BFM>;
   const int smem = chunk * 4;
   // (the most that any call needs, so that no thread lowers another's)
@@ -334,7 +515,7 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, chunk);
 }
 
