@@ -16,7 +16,7 @@
 //
 // One CTA takes one (sequence, kv-head), or a cluster of them a run of its pages
 // each; the pages' keys stay in shared memory.  A warp scores 32 pages at a time,
-// the next 32 pages' rows under way meanwhile.  The threshold comes from one
+// the next 64's rows under way meanwhile.  The threshold comes from one
 // histogram of the scores between their extremes (radix digits of the keys would
 // put nearly all of them in a few bins) and a ranking of the keys in its bin;
 // where that bin holds too many (ties, far outliers), digit by digit.
@@ -33,13 +33,25 @@ namespace cg = cooperative_groups;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int ctas_per_sm(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }  // what the registers of two strips leave
+constexpr int ctas_per_sm(int D) { return D == 256 ? 2 : 4; }
 constexpr int kAlone = 512;                          // pages that a CTA takes before more join it
 constexpr int kBins = 1024;
 constexpr int kCands = 256;                          // keys ranked against one another
+constexpr int kTile = 16;                            // pages per MMA
 constexpr int kStrip = 32;                           // pages per warp and step: two MMA tiles
 constexpr int kMaxChunk = kSelectMaxPages / 8;       // pages per CTA
 static_assert(kMaxChunk % kStrip == 0, "whole strips");
+constexpr int kRing = 2;                             // strips under way per warp
+// a strip in shared memory: 32 rows of codes, 32 words
+__host__ __device__ constexpr int strip_bytes(int D) { return kStrip * (D / 2 + 4); }
+__host__ __device__ constexpr int ring_bytes(int D) { return kWarps * kRing * strip_bytes(D); }
+
+__device__ __forceinline__ void async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 
 // The larger, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -114,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   constexpr int kKS = D / 16;                        // k-steps
   constexpr int kE = D / 32;
   constexpr int kW = D / 32;                         // words of a row per thread-in-group
-  extern __shared__ __align__(16) uint32_t keys[];   // [chunk]
+  extern __shared__ __align__(16) uint8_t dyn[];     // each warp's ring, then keys [chunk]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(dyn + ring_bytes(D));
   __shared__ Shared sh;
   __shared__ __align__(16) __half qh[kKS * 32 * 4];  // m in the B-fragment order
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -148,6 +161,40 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     if (i < lo) put(i, i);
     else put(want + i, n - p.last_pages + i - lo);
   if (want == 0) return;
+
+  // ---- this CTA's run of the pages; its first strips' rows start here
+  const int begin = min(rank * chunk, mid), count = min(mid - begin, chunk);
+  const int32_t* run = bt + lo + begin;
+  const int64_t stride = summary_stride(hkv, D);
+  const uint8_t* codes = p.summary + kvh * (D / 2);
+  const uint8_t* words = p.summary + hkv * (D / 2) + 4 * kvh;
+  uint8_t* ring = dyn + warp * (kRing * strip_bytes(D));
+  constexpr int kStep = kWarps * kStrip;
+  // this lane's page of the strip at i0 (-1: none, or bad)
+  auto page_of = [&](int i0) { return i0 + lane < count ? run[i0 + lane] : -1; };
+  // Starts the copies of a strip's rows; a page that is not there has the first
+  // one that is.  Returns whether this lane's is.
+  auto issue = [&](int id, int stage) {
+    const bool ok = uint32_t(id) < uint32_t(p.num_pages);
+    const uint32_t there = __ballot_sync(kAll, ok);
+    if (there != 0) {
+      const int any = __shfl_sync(kAll, id, __ffs(int(there)) - 1);
+      if (!ok) id = any;
+      uint8_t* dst = ring + stage * strip_bytes(D);
+      constexpr int kParts = D / 32;                 // 16-byte parts of a row
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        const int at = 32 * u + lane;                // of the strip's parts
+        const int64_t off = __shfl_sync(kAll, id, at / kParts) * stride;
+        async16(dst + 16 * at, codes + off + 16 * (at % kParts));
+      }
+      async4(dst + kStrip * (D / 2) + 4 * lane, words + id * stride);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return ok;
+  };
+  bool ok0 = issue(page_of(warp * kStrip), 0), ok1 = issue(page_of(warp * kStrip + kStep), 1);
+  int next = page_of(warp * kStrip + 2 * kStep);
 
   // ---- m, qs and J of the group's heads
   for (int h = warp; h < kMaxGroup; h += kWarps) {
@@ -223,62 +270,41 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   }
   const float2 qs = make_float2(sh.qs[2 * c], sh.qs[2 * c + 1]), jj = make_float2(sh.j[2 * c], sh.j[2 * c + 1]);
 
-  // ---- keys of this CTA's run of the pages
-  const int begin = min(rank * chunk, mid), count = min(mid - begin, chunk);
-  const int32_t* run = bt + lo + begin;
-  const int64_t stride = summary_stride(hkv, D);
-  const uint8_t* codes = p.summary + kvh * (D / 2) + c * (D / 8);
-  const uint8_t* words = p.summary + hkv * (D / 2) + 4 * kvh;
-  struct Rows {
-    uint32_t w[4][kW], m[4];                         // rows g, g + 8, g + 16, g + 24 of a strip
-  };
+  // ---- keys
   bool bad = false;
-  // this lane's page of the strip at i0 (-1: none, or bad)
-  auto page_of = [&](int i0) { return i0 + lane < count ? run[i0 + lane] : -1; };
-  // Loads the strip's rows; a page that is not there reads the first one that is.
-  // Returns whether this lane's is.
-  auto load = [&](int id, Rows& r) {
-    const bool ok = uint32_t(id) < uint32_t(p.num_pages);
-    const uint32_t there = __ballot_sync(kAll, ok);
-    if (there == 0) return false;
-    const int any = __shfl_sync(kAll, id, __ffs(int(there)) - 1);
-    if (!ok) id = any;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t off = __shfl_sync(kAll, id, g + 8 * u) * stride;
-      const uint8_t* src = codes + off;
-      if constexpr (kW == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-        r.w[u][0] = x.x; r.w[u][1] = x.y;
-      } else {
-#pragma unroll
-        for (int k = 0; k < kW; k += 4) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + k / 4);
-          r.w[u][k] = x.x; r.w[u][k + 1] = x.y; r.w[u][k + 2] = x.z; r.w[u][k + 3] = x.w;
-        }
-      }
-      r.m[u] = __ldg(reinterpret_cast<const uint32_t*>(words + off));
-    }
-    return ok;
-  };
   float least = INFINITY, most = -INFINITY;
-  auto score = [&](int i0, const Rows& r, bool ok) {
+  auto score = [&](int i0, int stage, bool ok) {
+    const uint8_t* st = ring + stage * strip_bytes(D);
     float v[4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+      uint32_t x[kW], y[kW];                         // rows g and g + 8 of the tile
+      const uint8_t* src = st + (kTile * t + g) * (D / 2) + c * (D / 8);
+      if constexpr (kW == 2) {
+        const uint2 a = *reinterpret_cast<const uint2*>(src), e = *reinterpret_cast<const uint2*>(src + 8 * (D / 2));
+        x[0] = a.x; x[1] = a.y;
+        y[0] = e.x; y[1] = e.y;
+      } else {
+#pragma unroll
+        for (int k = 0; k < kW; k += 4) {
+          const uint4 a = *reinterpret_cast<const uint4*>(src + 4 * k);
+          const uint4 e = *reinterpret_cast<const uint4*>(src + 8 * (D / 2) + 4 * k);
+          x[k] = a.x; x[k + 1] = a.y; x[k + 2] = a.z; x[k + 3] = a.w;
+          y[k] = e.x; y[k + 1] = e.y; y[k + 2] = e.z; y[k + 3] = e.w;
+        }
+      }
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < kW; ++k)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t x = hh ? r.w[2 * t][k] >> 8 : r.w[2 * t][k];
-          const uint32_t y = hh ? r.w[2 * t + 1][k] >> 8 : r.w[2 * t + 1][k];
-          const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+          const uint32_t xx = hh ? x[k] >> 8 : x[k], yy = hh ? y[k] >> 8 : y[k];
+          const uint32_t a[4] = {xx & 0x000F000Fu, yy & 0x000F000Fu, xx & 0x00F000F0u, yy & 0x00F000F0u};
           mma_16816(d, a, b[2 * k + hh][0], b[2 * k + hh][1]);
         }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t m = r.m[2 * t + u];
+        const uint32_t m = reinterpret_cast<const uint32_t*>(st + kStrip * (D / 2))[kTile * t + 8 * u + g];
         float s = meta_lo(m, BFM);
         const float z = meta_hi(m, BFM);
         float2 i = make_float2(d[2 * u], d[2 * u + 1]);
@@ -308,21 +334,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
       }
     }
   };
-  {
-    Rows r[2];
-    constexpr int kStep = kWarps * kStrip;
-    int i0 = warp * kStrip;
-    int next = page_of(i0 + kStep);
-    bool ok0 = i0 < count && load(page_of(i0), r[0]), ok1;
-    // (the branches are the same in every lane of a warp)
-    for (; i0 < count; i0 += 2 * kStep) {
-      const int after = page_of(i0 + 2 * kStep);
-      ok1 = i0 + kStep < count && load(next, r[1]);
-      score(i0, r[0], ok0);
-      next = page_of(i0 + 3 * kStep);
-      ok0 = i0 + 2 * kStep < count && load(after, r[0]);
-      if (i0 + kStep < count) score(i0 + kStep, r[1], ok1);
-    }
+  for (int i0 = warp * kStrip, stage = 0; i0 < count; i0 += kStep, stage ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    __syncwarp();
+    score(i0, stage, ok0);
+    ok0 = ok1;
+    __syncwarp();                                    // the strip is read: its place takes the next but one
+    ok1 = issue(next, stage);
+    next = page_of(i0 + 3 * kStep);
   }
   if (bad) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
 #pragma unroll
@@ -493,14 +512,15 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
   const int max_pages = (p.max_seq_len + p.page_size - 1) / p.page_size;
   const int64_t units = int64_t(p.num_seqs) * p.num_kv_heads;
   int ctas = 1;
-  while (ctas < 8 && units * ctas < sms && max_pages > ctas * kAlone) ctas *= 2;
+  while (ctas < 8 && 2 * units * ctas <= int64_t(sms) * ctas_per_sm(D) && max_pages > ctas * kAlone) ctas *= 2;
   while (max_pages > ctas * kMaxChunk) ctas *= 2;
   const int mid = max_pages > 0 ? max_pages : 1;
   const int chunk = ((mid + ctas - 1) / ctas + kStrip - 1) / kStrip * kStrip;
   auto kernel = select_pages_kernel<D, BFM>;
-  const int smem = chunk * 4;
+  const int smem = ring_bytes(D) + chunk * 4;
   // (the most that any call needs, so that no thread lowers another's)
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunk * 4);
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               ring_bytes(D) + kMaxChunk * 4);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas), unsigned(p.num_kv_heads), unsigned(p.num_seqs));
