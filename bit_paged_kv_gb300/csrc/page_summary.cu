@@ -7,6 +7,13 @@
 // quantized by the append's rule.  n s is exact in binary32 (4 by at most 11
 // bits), so fma(n, s, A) rounds once like a product and a sum, and every step
 // is one rounding: the bytes are determined.
+//
+// The codes need no conversion (which runs at a quarter of the issue rate): a
+// nibble left in place in a word of zeros is the binary32 16^j n 2^-149, up to j =
+// 5 (bit 23 is the first exponent's, whose step is the subnormals').  s 2^111 is
+// finite for every binary16 s, and the sums, kept times 16^j 2^-38, round as the
+// plain ones do.  bfloat16 scales leave no room for that: there the nibble goes
+// under the exponent of 2^23, which is taken off again.
 #include <algorithm>
 
 #include "saw_device.cuh"
@@ -19,18 +26,35 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
 
-// A warp sums one kv-head's page (head_dim 64: two kv-heads', a half-warp
-// each).  A lane owns 8 dims, one 32-bit word of codes per token; D / 8 lanes
-// hold a row, and the halves of what is left take the even and the odd tokens
-// (head_dim 256: every lane takes both).
+// a[j] += n_j s for the eight codes of a word; not BFM: s comes times 2^111 and
+// the sums are times 16^place_of(j) 2^-38.
+__host__ __device__ constexpr int place_of(int j) { return j < 6 ? j : j - 2; }
+template <bool BFM>
+__device__ __forceinline__ void add8(uint32_t w, float s, float2* a) {
+  const uint32_t up = w >> 8;
+  auto value = [&](int j) {
+    return BFM ? ((w >> (4 * j)) & 15u) | 0x4B000000u : (j < 6 ? w : up) & (15u << (4 * place_of(j)));
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 n = make_float2(__uint_as_float(value(2 * j)), __uint_as_float(value(2 * j + 1)));
+    if constexpr (BFM) n = add2(n, make_float2(-0x1p23f, -0x1p23f));
+    a[j] = fma2(n, make_float2(s, s), a[j]);
+  }
+}
+
+// A lane owns kWords 32-bit words of codes per token (two, at head_dim 64 one),
+// half of a row's lanes take the even tokens and half the odd ones; a warp sums
+// two kv-heads' pages, at head_dim 256 one's.  Then a lane finishes half of its
+// dims: one of its words, or half of its one.
 template <int D, int P, bool BFM>
 __global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const SummaryParams p) {
   pdl_wait_then_release();
-  constexpr int kRow = D / 8;                        // lanes per row
-  constexpr int kHeads = D == 64 ? 2 : 1;            // kv-heads per warp
-  constexpr bool kBoth = D == 256;                   // a lane takes even and odd tokens
+  constexpr int kWords = D == 64 ? 1 : 2;
+  constexpr int kRow = D / 8 / kWords;               // lanes per row of a token
+  constexpr int kHeads = 16 / kRow;                  // kv-heads per warp
   constexpr int kChunk = P * (D / 2 + 4);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.y;
   const int L = p.seq_lens[seq];
   const int fresh = p.new_lens ? p.new_lens[seq] : L;
@@ -41,77 +65,92 @@ __global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const Summary
   const int first = (L - min(fresh, L)) >> p.page_shift, end = L >> p.page_shift;
   const int hkv = p.num_kv_heads;
   const int per = (hkv + kHeads - 1) / kHeads;       // warps per page
-  const int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (i >= int64_t(end - first) * per) return;
-  const int page = first + int(i / per);
-  const int head = int(i % per) * kHeads + (kHeads == 2 ? lane >> 4 : 0);
+  const uint32_t i = blockIdx.x * kWarps + warp;
+  if (i >= uint32_t(end - first) * uint32_t(per)) return;
+  const int page = first + int(i / uint32_t(per));
+  const int head = int(i % uint32_t(per)) * kHeads + lane / (2 * kRow);
   const int id = p.block_tables[int64_t(seq) * p.max_blocks + page];
   if (id < 0 || id >= p.num_pages) {
     if (lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
     return;
   }
-  const int r = lane & (kRow - 1);                   // word of the row
-  const int odd = kBoth ? 0 : (lane / kRow) & 1;
+  const int r = lane & (kRow - 1);                   // lane of the row
+  const int odd = (lane / kRow) & 1;
   const uint8_t* chunk = p.k_cache + (int64_t(id) * hkv + min(head, hkv - 1)) * kChunk;
-  constexpr int kSums = kBoth ? 2 : 1;
-  float a[kSums][8], z[kSums];
+  const uint8_t* code = chunk + odd * (D / 2) + 4 * kWords * r;
+  const uint32_t* word = reinterpret_cast<const uint32_t*>(chunk + P * (D / 2)) + odd;
+  float2 a[kWords][4];
 #pragma unroll
-  for (int u = 0; u < kSums; ++u) {
-    z[u] = 0.0f;
+  for (int u = 0; u < kWords; ++u)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[u][j] = 0.0f;
-  }
+    for (int j = 0; j < 4; ++j) a[u][j] = make_float2(0.0f, 0.0f);
+  float z = 0.0f;
+  constexpr int kBatch = 8;                          // tokens under way
 #pragma unroll
-  for (int t = 0; t < P; t += 2) {
+  for (int t0 = 0; t0 < P / 2; t0 += kBatch) {
+    uint32_t w[kBatch][kWords], m[kBatch];
 #pragma unroll
-    for (int u = 0; u < kSums; ++u) {
-      const int tok = t + (kBoth ? u : odd);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(chunk + tok * (D / 2) + 4 * r);
-      const uint32_t m = *reinterpret_cast<const uint32_t*>(chunk + P * (D / 2) + 4 * tok);
-      const float s = meta_lo(m, BFM);
-      z[u] = __fadd_rn(z[u], meta_hi(m, BFM));
+    for (int t = 0; t < kBatch; ++t) {
+      const uint8_t* src = code + (t0 + t) * D;
+      if constexpr (kWords == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        w[t][0] = x.x;
+        w[t][kWords - 1] = x.y;
+      } else {
+        w[t][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      }
+      m[t] = __ldg(word + (t0 + t) * 2);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[u][j] = __fmaf_rn(float((w >> (4 * j)) & 15u), s, a[u][j]);
+    for (int t = 0; t < kBatch; ++t) {
+      z = __fadd_rn(z, meta_hi(m[t], BFM));
+      const float s = BFM ? meta_lo(m[t], BFM) : meta_lo(m[t], BFM) * 0x1p111f;
+#pragma unroll
+      for (int u = 0; u < kWords; ++u) add8<BFM>(w[t][u], s, a[u]);
     }
   }
-  float y[8], zz;
-  if constexpr (kBoth) {
-    zz = __fadd_rn(z[0], z[1]);
+  auto sum_of = [&](int u, int j) {
+    const float x = j & 1 ? a[u][j >> 1].y : a[u][j >> 1].x;
+    return BFM ? x : x * (0x1p38f / float(1 << (4 * place_of(j))));
+  };
+  // even + odd; this lane keeps word `odd`, or half `odd` of its word
+  constexpr int kMine = 4 * kWords;
+  float y[kMine], mn = INFINITY, mx = -INFINITY;
+  z = __fadd_rn(z, __shfl_xor_sync(kAll, z, kRow));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __fadd_rn(a[0][j], a[1][j]);
-  } else {
-    zz = __fadd_rn(z[0], __shfl_xor_sync(kAll, z[0], kRow));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __fadd_rn(a[0][j], __shfl_xor_sync(kAll, a[0][j], kRow));
-  }
-  float mn = INFINITY, mx = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = __fmul_rn(__fadd_rn(y[j], zz), 1.0f / P);
+  for (int j = 0; j < kMine; ++j) {
+    const float lo = sum_of(0, j), hi = kWords == 2 ? sum_of(kWords - 1, j) : sum_of(0, (4 + j) & 7);
+    y[j] = __fadd_rn(odd ? hi : lo, __shfl_xor_sync(kAll, odd ? lo : hi, kRow));
+    y[j] = __fmul_rn(__fadd_rn(y[j], z), 1.0f / P);
     mn = fminf(mn, y[j]);
     mx = fmaxf(mx, y[j]);
   }
 #pragma unroll
-  for (int d = 1; d < kRow; d <<= 1) {
+  for (int d = 1; d < 2 * kRow; d <<= 1) {
     mn = fminf(mn, __shfl_xor_sync(kAll, mn, d));
     mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
   }
   const RowMeta m = row_meta(mn, mx, BFM);
   uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int q = __float2int_rn(__fmul_rn(__fsub_rn(y[j], m.z), m.rcp));
-    w |= uint32_t(min(max(q, 0), 15)) << (4 * j);
+  for (int j = 0; j < kMine; ++j) {
+    // rounded half to even below 2^23's exponent; clamping first is the same
+    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(y[j], m.z), m.rcp), 0.0f), 15.0f);
+    w |= (__float_as_uint(__fadd_rn(q, 0x1p23f)) & 15u) << (4 * j);
   }
-  if (odd || head >= hkv) return;
+  if (head >= hkv) return;
   uint8_t* out = p.summary + id * summary_stride(hkv, D);
-  reinterpret_cast<uint32_t*>(out + head * (D / 2))[r] = w;
-  if (r == 0) *reinterpret_cast<uint32_t*>(out + hkv * (D / 2) + 4 * head) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
+  uint8_t* row = out + head * (D / 2) + 4 * kWords * r + 2 * kWords * odd;
+  if constexpr (kWords == 2) *reinterpret_cast<uint32_t*>(row) = w;
+  else *reinterpret_cast<uint16_t*>(row) = uint16_t(w);
+  if (r == 0 && !odd)
+    *reinterpret_cast<uint32_t*>(out + hkv * (D / 2) + 4 * head) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
 }
 
 template <int D, int P>
 cudaError_t launch_page(const SummaryParams& p, cudaStream_t stream) {
-  const int per = (p.num_kv_heads + (D == 64 ? 1 : 0)) / (D == 64 ? 2 : 1);
+  constexpr int kHeads = D == 256 ? 1 : 2;
+  const int per = (p.num_kv_heads + kHeads - 1) / kHeads;
   // a step of n tokens completes at most ceil(n / P) pages
   const int64_t warps = std::max<int64_t>((int64_t(p.max_new_len) + P - 1) / P, 1) * per;
   cudaLaunchConfig_t cfg = {};
