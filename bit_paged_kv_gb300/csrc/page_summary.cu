@@ -25,6 +25,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
+constexpr int kMaxPasses = 4;
 
 // a[j] += n_j s for the eight codes of a word; not BFM: s comes times 2^111 and
 // the sums are times 16^place_of(j) 2^-38.
@@ -46,9 +47,10 @@ __device__ __forceinline__ void add8(uint32_t w, float s, float2* a) {
 // A lane owns kWords 32-bit words of codes per token (two, at head_dim 64 one),
 // half of a row's lanes take the even tokens and half the odd ones; a warp sums
 // two kv-heads' pages, at head_dim 256 one's.  Then a lane finishes half of its
-// dims: one of its words, or half of its one.
+// dims: one of its words, or half of its one.  A warp goes through `passes` groups
+// of kv-heads of a page in batches of 16 tokens, the next batch under way.
 template <int D, int P, bool BFM>
-__global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const SummaryParams p) {
+__global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const SummaryParams p, int passes) {
   pdl_wait_then_release();
   constexpr int kWords = D == 64 ? 1 : 2;
   constexpr int kRow = D / 8 / kWords;               // lanes per row of a token
@@ -64,11 +66,12 @@ __global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const Summary
   }
   const int first = (L - min(fresh, L)) >> p.page_shift, end = L >> p.page_shift;
   const int hkv = p.num_kv_heads;
-  const int per = (hkv + kHeads - 1) / kHeads;       // warps per page
+  const int groups = (hkv + kHeads - 1) / kHeads;
+  const uint32_t per = uint32_t((groups + passes - 1) / passes);  // warps per page
   const uint32_t i = blockIdx.x * kWarps + warp;
-  if (i >= uint32_t(end - first) * uint32_t(per)) return;
-  const int page = first + int(i / uint32_t(per));
-  const int head = int(i % uint32_t(per)) * kHeads + lane / (2 * kRow);
+  if (i >= uint32_t(end - first) * per) return;
+  const int page = first + int(i / per);
+  const int group0 = int(i % per) * passes;
   const int id = p.block_tables[int64_t(seq) * p.max_blocks + page];
   if (id < 0 || id >= p.num_pages) {
     if (lane == 0) report(p.dev_status, SAW_ERR_DEVICE_INDEX);
@@ -76,83 +79,120 @@ __global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const Summary
   }
   const int r = lane & (kRow - 1);                   // lane of the row
   const int odd = (lane / kRow) & 1;
-  const uint8_t* chunk = p.k_cache + (int64_t(id) * hkv + min(head, hkv - 1)) * kChunk;
-  const uint8_t* code = chunk + odd * (D / 2) + 4 * kWords * r;
-  const uint32_t* word = reinterpret_cast<const uint32_t*>(chunk + P * (D / 2)) + odd;
-  float2 a[kWords][4];
-#pragma unroll
-  for (int u = 0; u < kWords; ++u)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a[u][j] = make_float2(0.0f, 0.0f);
-  float z = 0.0f;
-  constexpr int kBatch = 8;                          // tokens under way
-#pragma unroll
-  for (int t0 = 0; t0 < P / 2; t0 += kBatch) {
+  const int sub = lane / (2 * kRow);                 // kv-head of the group
+  constexpr int kBatch = 8, kBatches = P / 2 / kBatch;  // tokens of this lane
+  struct Batch {
     uint32_t w[kBatch][kWords], m[kBatch];
-#pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const uint8_t* src = code + (t0 + t) * D;
-      if constexpr (kWords == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-        w[t][0] = x.x;
-        w[t][kWords - 1] = x.y;
-      } else {
-        w[t][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-      }
-      m[t] = __ldg(word + (t0 + t) * 2);
-    }
-#pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      z = __fadd_rn(z, meta_hi(m[t], BFM));
-      const float s = BFM ? meta_lo(m[t], BFM) : meta_lo(m[t], BFM) * 0x1p111f;
-#pragma unroll
-      for (int u = 0; u < kWords; ++u) add8<BFM>(w[t][u], s, a[u]);
-    }
-  }
-  auto sum_of = [&](int u, int j) {
-    const float x = j & 1 ? a[u][j >> 1].y : a[u][j >> 1].x;
-    return BFM ? x : x * (0x1p38f / float(1 << (4 * place_of(j))));
   };
-  // even + odd; this lane keeps word `odd`, or half `odd` of its word
-  constexpr int kMine = 4 * kWords;
-  float y[kMine], mn = INFINITY, mx = -INFINITY;
-  z = __fadd_rn(z, __shfl_xor_sync(kAll, z, kRow));
+  const uint8_t* pages = p.k_cache + int64_t(id) * hkv * kChunk;
+  auto load = [&](int k, Batch& x) {                 // batch k of this warp
+    const int head = min((group0 + k / kBatches) * kHeads + sub, hkv - 1);
+    const uint8_t* chunk = pages + int64_t(head) * kChunk;
+    const uint8_t* code = chunk + (k % kBatches) * (kBatch * D) + odd * (D / 2) + 4 * kWords * r;
+    const uint32_t* word = reinterpret_cast<const uint32_t*>(chunk + P * (D / 2)) + (k % kBatches) * (2 * kBatch) + odd;
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    const float lo = sum_of(0, j), hi = kWords == 2 ? sum_of(kWords - 1, j) : sum_of(0, (4 + j) & 7);
-    y[j] = __fadd_rn(odd ? hi : lo, __shfl_xor_sync(kAll, odd ? lo : hi, kRow));
-    y[j] = __fmul_rn(__fadd_rn(y[j], z), 1.0f / P);
-    mn = fminf(mn, y[j]);
-    mx = fmaxf(mx, y[j]);
-  }
+    for (int t = 0; t < kBatch; ++t) {
+      const uint8_t* src = code + t * D;
+      if constexpr (kWords == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        x.w[t][0] = v.x;
+        x.w[t][kWords - 1] = v.y;
+      } else {
+        x.w[t][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      }
+      x.m[t] = __ldg(word + 2 * t);
+    }
+  };
+  float2 a[kWords][4] = {};
+  float z = 0.0f;
+  auto sum_of = [&](int u, int j) { return j & 1 ? a[u][j >> 1].y : a[u][j >> 1].x; };
+  auto add = [&](int k, const Batch& x) {
+    if (k % kBatches == 0) {
 #pragma unroll
-  for (int d = 1; d < 2 * kRow; d <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(kAll, mn, d));
-    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
-  }
-  const RowMeta m = row_meta(mn, mx, BFM);
-  uint32_t w = 0;
+      for (int u = 0; u < kWords; ++u)
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    // rounded half to even below 2^23's exponent; clamping first is the same
-    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(y[j], m.z), m.rcp), 0.0f), 15.0f);
-    w |= (__float_as_uint(__fadd_rn(q, 0x1p23f)) & 15u) << (4 * j);
+        for (int j = 0; j < 4; ++j) a[u][j] = make_float2(0.0f, 0.0f);
+      z = 0.0f;
+    }
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      z = __fadd_rn(z, meta_hi(x.m[t], BFM));
+      const float s = BFM ? meta_lo(x.m[t], BFM) : meta_lo(x.m[t], BFM) * 0x1p111f;
+#pragma unroll
+      for (int u = 0; u < kWords; ++u) add8<BFM>(x.w[t][u], s, a[u]);
+    }
+    if (k % kBatches != kBatches - 1) return;
+    // even + odd; this lane keeps word `odd`, or half `odd` of its word
+    constexpr int kMine = 4 * kWords;
+    float y[kMine], mn = INFINITY, mx = -INFINITY;
+    z = __fadd_rn(z, __shfl_xor_sync(kAll, z, kRow));
+    if constexpr (!BFM) z *= 1.0f / P;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int jo = kWords == 2 ? j : 4 + j;        // the other half's nibble
+      const float lo = sum_of(0, j), hi = sum_of(kWords - 1, jo);
+      const float x = __fadd_rn(odd ? hi : lo, __shfl_xor_sync(kAll, odd ? lo : hi, kRow));
+      if constexpr (BFM) {
+        y[j] = __fmul_rn(__fadd_rn(x, z), 1.0f / P);
+      } else {
+        // powers of two, far from either end of binary32's range: one rounding,
+        // that of A + Z
+        constexpr float kUnit = 0x1p38f / P;
+        const float one = kUnit / float(1 << (4 * place_of(j))), two = kUnit / float(1 << (4 * place_of(jo)));
+        y[j] = __fmaf_rn(x, kWords == 2 || !odd ? one : two, z);
+      }
+      mn = fminf(mn, y[j]);
+      mx = fmaxf(mx, y[j]);
+    }
+#pragma unroll
+    for (int d = 1; d < 2 * kRow; d <<= 1) {
+      mn = fminf(mn, __shfl_xor_sync(kAll, mn, d));
+      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
+    }
+    const RowMeta m = row_meta(mn, mx, BFM);
+    // rounded half to even below 2^23's exponent, whose bits the sum of the words
+    // takes 16^j times (clamping first is the same)
+    uint32_t w = 0u - 0x4B000000u * (kMine == 8 ? 0x11111111u : 0x1111u);
+    const bool clamp = __any_sync(kAll, !m.fast);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      float q = __fmul_rn(__fsub_rn(y[j], m.z), m.rcp);
+      if (clamp) q = fminf(fmaxf(q, 0.0f), 15.0f);
+      w += __float_as_uint(__fadd_rn(q, 0x1p23f)) << (4 * j);
+    }
+    const int head = (group0 + k / kBatches) * kHeads + sub;
+    if (head < hkv) {
+      uint8_t* out = p.summary + id * summary_stride(hkv, D);
+      uint8_t* row = out + head * (D / 2) + 4 * kWords * r + 2 * kWords * odd;
+      if constexpr (kWords == 2) *reinterpret_cast<uint32_t*>(row) = w;
+      else *reinterpret_cast<uint16_t*>(row) = uint16_t(w);
+      if (r == 0 && !odd)
+        *reinterpret_cast<uint32_t*>(out + hkv * (D / 2) + 4 * head) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
+    }
+  };
+  const int n = min(passes, groups - group0) * kBatches;
+  Batch x[2];
+  load(0, x[0]);
+#pragma unroll 1
+  for (int k = 0; k < n; k += 2) {
+    if (k + 1 < n) load(k + 1, x[1]);
+    add(k, x[0]);
+    if (k + 1 >= n) break;
+    if (k + 2 < n) load(k + 2, x[0]);
+    add(k + 1, x[1]);
   }
-  if (head >= hkv) return;
-  uint8_t* out = p.summary + id * summary_stride(hkv, D);
-  uint8_t* row = out + head * (D / 2) + 4 * kWords * r + 2 * kWords * odd;
-  if constexpr (kWords == 2) *reinterpret_cast<uint32_t*>(row) = w;
-  else *reinterpret_cast<uint16_t*>(row) = uint16_t(w);
-  if (r == 0 && !odd)
-    *reinterpret_cast<uint32_t*>(out + hkv * (D / 2) + 4 * head) = uint32_t(m.sb) | (uint32_t(m.zb) << 16);
 }
 
 template <int D, int P>
-cudaError_t launch_page(const SummaryParams& p, cudaStream_t stream) {
+cudaError_t launch_page(const SummaryParams& p, int sms, cudaStream_t stream) {
   constexpr int kHeads = D == 256 ? 1 : 2;
-  const int per = (p.num_kv_heads + kHeads - 1) / kHeads;
+  const int groups = (p.num_kv_heads + kHeads - 1) / kHeads;
   // a step of n tokens completes at most ceil(n / P) pages
-  const int64_t warps = std::max<int64_t>((int64_t(p.max_new_len) + P - 1) / P, 1) * per;
+  const int64_t pages = std::max<int64_t>((int64_t(p.max_new_len) + P - 1) / P, 1);
+  // more groups per warp where that leaves warps enough
+  int passes = 1;
+  while (passes < kMaxPasses && passes < groups && pages * groups * p.num_seqs >= int64_t(2 * passes) * 32 * sms) passes *= 2;
+  const int64_t warps = pages * ((groups + passes - 1) / passes);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((warps + kWarps - 1) / kWarps), unsigned(p.num_seqs));
   cfg.blockDim = dim3(32 * kWarps);
@@ -162,27 +202,27 @@ cudaError_t launch_page(const SummaryParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.meta_bf16 ? cudaLaunchKernelEx(&cfg, page_summary_kernel<D, P, true>, p)
-                     : cudaLaunchKernelEx(&cfg, page_summary_kernel<D, P, false>, p);
+  return p.meta_bf16 ? cudaLaunchKernelEx(&cfg, page_summary_kernel<D, P, true>, p, passes)
+                     : cudaLaunchKernelEx(&cfg, page_summary_kernel<D, P, false>, p, passes);
 }
 
 template <int D>
-cudaError_t launch_dim(const SummaryParams& p, cudaStream_t stream) {
+cudaError_t launch_dim(const SummaryParams& p, int sms, cudaStream_t stream) {
   switch (p.page_size) {
-    case 16: return launch_page<D, 16>(p, stream);
-    case 32: return launch_page<D, 32>(p, stream);
-    case 64: return launch_page<D, 64>(p, stream);
+    case 16: return launch_page<D, 16>(p, sms, stream);
+    case 32: return launch_page<D, 32>(p, sms, stream);
+    case 64: return launch_page<D, 64>(p, sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_page_summary(const SummaryParams& p, int, cudaStream_t stream) {
+cudaError_t launch_page_summary(const SummaryParams& p, int sms, cudaStream_t stream) {
   switch (p.head_dim) {
-    case 64: return launch_dim<64>(p, stream);
-    case 128: return launch_dim<128>(p, stream);
-    case 256: return launch_dim<256>(p, stream);
+    case 64: return launch_dim<64>(p, sms, stream);
+    case 128: return launch_dim<128>(p, sms, stream);
+    case 256: return launch_dim<256>(p, sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }

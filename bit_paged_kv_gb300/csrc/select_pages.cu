@@ -307,11 +307,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
         const uint32_t m = reinterpret_cast<const uint32_t*>(st + kStrip * (D / 2))[kTile * t + 8 * u + g];
         float s = meta_lo(m, BFM);
         const float z = meta_hi(m, BFM);
-        float2 i = make_float2(d[2 * u], d[2 * u + 1]);
-        // I = 2^24 d, exactly; a binary16 scale takes the factor as well
-        if constexpr (BFM) i = mul2(i, make_float2(0x1p24f, 0x1p24f));
-        else s *= 0x1p24f;
-        const float2 x = mul2(qs, add2(mul2(make_float2(s, s), i), mul2(make_float2(z, z), jj)));
+        // I = 2^24 d, exactly; a binary16 scale takes the factor as well.  (Scalar
+        // steps: packed products and packed sums get fused by the assembler.)
+        float i0 = d[2 * u], i1 = d[2 * u + 1];
+        if constexpr (BFM) {
+          i0 *= 0x1p24f;
+          i1 *= 0x1p24f;
+        } else {
+          s *= 0x1p24f;
+        }
+        const float2 x = mul2(qs, make_float2(__fadd_rn(__fmul_rn(s, i0), __fmul_rn(z, jj.x)),
+                                              __fadd_rn(__fmul_rn(s, i1), __fmul_rn(z, jj.y))));
         v[2 * t + u] = fmaxf(x.x, x.y);              // (fmaxf passes over a NaN)
       }
     }
