@@ -24,8 +24,10 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 // front (norm_row, norm16; SAW_ROPE_NORM).
 #ifdef SAW_ROPE_NORM
 using Params = NormRopeParams;
+constexpr bool kNorm = true;
 #else
 using Params = RopeParams;
+constexpr bool kNorm = false;
 #endif
 
 __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
@@ -124,9 +126,22 @@ __device__ __forceinline__ float gain(const Params& p, int tensor, int d) {
   }
   return __fadd_rn(g, p.weight_offset);
 }
+// The root and the reciprocal, correctly rounded: an approximation, its exact
+// remainder by a fused step, and one correction each (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990).  Equal
+// to the built-in ones for every mantissa and both parities of the exponent, in
+// the range that eps >= 2^-100 leaves; those, with their checks for the rest of
+// binary32, cost 22 us of 592 at 131072 tokens.
 template <int D>
 __device__ __forceinline__ float norm_factor(float ss, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps)));
+  const float t = __fadd_rn(__fmul_rn(ss, 1.0f / D), eps);
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(t));
+  float root = __fmul_rn(t, y);
+  root = __fmaf_rn(__fmaf_rn(-root, root, t), __fmul_rn(0.5f, y), root);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(root));
+  y = __fmaf_rn(y, __fmaf_rn(-root, y, 1.0f), y);
+  return t == INFINITY ? 0.0f : y;                   // (squares beyond binary32)
 }
 #endif
 
@@ -373,7 +388,9 @@ enum { kHalfWhole = 0, kHalfPart = 1, kInter = 2, kHalfBit = 3 };  // whole head
 // 527 with two; the layout that exchanges partners by shuffles keeps two (2047
 // tokens, half the head: 14.4 us, 22.3 with three and spills; by kHalfBit 12.7,
 // 8192 tokens 47.2 against 37.9).
-constexpr int bulk_ctas(int layout) { return layout == kHalfPart ? 2 : 3; }
+// With norms two: 131072 tokens 582 us, with three and spills 720, 16 warps in one
+// 571 but 1 to 2 us more for fewer tokens.
+constexpr int bulk_ctas(int layout) { return kNorm || layout == kHalfPart ? 2 : 3; }
 
 template <bool F16IN>
 __device__ __forceinline__ void widen8(const uint4& w, float* x) {
@@ -439,10 +456,23 @@ __device__ __forceinline__ void turn16(float (&x)[16], const Angles<LAYOUT>& t, 
   if constexpr (LAYOUT == kHalfWhole || LAYOUT == kHalfBit) {
     if (LAYOUT == kHalfBit && 16 * a >= r) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float u = x[e], v = x[8 + e];
-      x[e] = __fsub_rn(__fmul_rn(u, t.c[e]), __fmul_rn(v, t.s[e]));
-      x[8 + e] = __fadd_rn(__fmul_rn(v, t.c[e]), __fmul_rn(u, t.s[e]));
+    for (int e = 0; e < 8; e += 2) {
+      if constexpr (kNorm) {  // packed products, scalar sums
+        const float2 u = make_float2(x[e], x[e + 1]), v = make_float2(x[8 + e], x[9 + e]);
+        const float2 c = make_float2(t.c[e], t.c[e + 1]), s = make_float2(t.s[e], t.s[e + 1]);
+        const float2 uc = mul2(u, c), vs = mul2(v, s), vc = mul2(v, c), us = mul2(u, s);
+        x[e] = __fsub_rn(uc.x, vs.x);
+        x[e + 1] = __fsub_rn(uc.y, vs.y);
+        x[8 + e] = __fadd_rn(vc.x, us.x);
+        x[9 + e] = __fadd_rn(vc.y, us.y);
+      } else {
+#pragma unroll
+        for (int i = e; i < e + 2; ++i) {
+          const float u = x[i], v = x[8 + i];
+          x[i] = __fsub_rn(__fmul_rn(u, t.c[i]), __fmul_rn(v, t.s[i]));
+          x[8 + i] = __fadd_rn(__fmul_rn(v, t.c[i]), __fmul_rn(u, t.s[i]));
+        }
+      }
     }
   } else if constexpr (LAYOUT == kInter) {
 #pragma unroll
@@ -523,40 +553,94 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int h
   for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], c_h);
 }
 
-#ifdef SAW_ROPE_NORM
-// The norm of a lane's 16 values; g: the tensor's gains in shared memory, a
-// and hc as below.
+// The same, two sums per instruction (with norms the kernel is bound by issue:
+// 16 us of 608 at 131072 tokens; without, bound by memory, it loses 30 of 482).
 template <int D>
-__device__ __forceinline__ void norm16(float (&x)[16], const float* g, float eps, int a, int hc) {
+__device__ __forceinline__ void rotate16_packed(float (&x)[16], int h, float c_h, int hc, int lane) {
+  auto pair = [&](int i) { return make_float2(x[i], x[i + 1]); };
+  auto put = [&](int i, const float2& v) {
+    x[i] = v.x;
+    x[i + 1] = v.y;
+  };
+  auto step = [&](int i, int j) {  // x[i], x[i + 1] with x[j], x[j + 1]
+    const float2 a = pair(i), b = pair(j);
+    put(i, add2(a, b));
+    put(j, fma2(b, make_float2(-1.0f, -1.0f), a));
+  };
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {  // (h >= 16)
+    const float2 a = pair(i);
+    put(i, make_float2(__fadd_rn(a.x, a.y), __fsub_rn(a.x, a.y)));
+  }
+#pragma unroll
+  for (int s = 2; s < 8; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      if (!(i & s)) step(i, i + s);
+#pragma unroll
+  for (int s = 8; s < D; s <<= 1) {
+    if (s >= h) continue;
+    if (s == 8 * hc) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) step(i, i + 8);
+    } else {
+      const int m = s < 8 * hc ? s >> 3 : s >> 4;
+      const float sign = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2)
+        put(i, fma2(pair(i), make_float2(sign, sign),
+                    make_float2(__shfl_xor_sync(kAll, x[i], m), __shfl_xor_sync(kAll, x[i + 1], m))));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) put(i, mul2(pair(i), make_float2(c_h, c_h)));
+}
+
+#ifdef SAW_ROPE_NORM
+// The norm of a lane's 16 values; g: the tensor's gains in shared memory (the
+// chunks' first quads, then their second ones), a and hc as below.  (Packed products: no sum of theirs is packed, see turn16.)
+template <int D>
+__device__ __forceinline__ void norm16(float (&x)[16], const float* g, float eps, int a, int hc, int lane) {
   float s[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = __fmul_rn(x[i], x[i]);
+  for (int i = 0; i < 16; i += 2) {
+    const float2 v = make_float2(x[i], x[i + 1]), w = mul2(v, v);
+    s[i] = w.x;
+    s[i + 1] = w.y;
+  }
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1)
 #pragma unroll
     for (int i = 0; i < 16; i += 2 * d) s[i] = __fadd_rn(s[i], s[i + d]);
+  // the sums of the lane's two chunks: while they are apart, one lane of a pair
+  // goes on with the first chunks' and the other with the second's
   float u = s[0], v = s[8];
-  bool joined = false;
+  int at = 0;                                        // 1: joined, 2: split over pairs of lanes
 #pragma unroll
   for (int d = 8; d < D; d <<= 1) {
     if (d == 8 * hc) {
-      u = __fadd_rn(u, v);
-      joined = true;
-    } else if (!joined) {
-      u = __fadd_rn(u, __shfl_xor_sync(kAll, u, d >> 3));
-      v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d >> 3));
+      u = __fadd_rn(u, at == 2 ? __shfl_xor_sync(kAll, u, 1) : v);
+      at = 1;
+    } else if (at == 0) {
+      const bool odd = lane & 1;
+      const float o = __shfl_xor_sync(kAll, odd ? u : v, 1);
+      u = __fadd_rn(odd ? v : u, o);
+      at = 2;
     } else {
-      u = __fadd_rn(u, __shfl_xor_sync(kAll, u, d >> 4));
+      u = __fadd_rn(u, __shfl_xor_sync(kAll, u, at == 2 ? d >> 3 : d >> 4));
     }
   }
   const float r = norm_factor<D>(u, eps);
+  const float2 rr = make_float2(r, r);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 w = *reinterpret_cast<const float4*>(g + 8 * (j < 2 ? a : a + hc) + 4 * (j & 1));
-    x[4 * j] = __fmul_rn(__fmul_rn(x[4 * j], r), w.x);
-    x[4 * j + 1] = __fmul_rn(__fmul_rn(x[4 * j + 1], r), w.y);
-    x[4 * j + 2] = __fmul_rn(__fmul_rn(x[4 * j + 2], r), w.z);
-    x[4 * j + 3] = __fmul_rn(__fmul_rn(x[4 * j + 3], r), w.w);
+    const float4 w = *reinterpret_cast<const float4*>(g + 4 * ((j & 1) * (D / 8) + (j < 2 ? a : a + hc)));
+    const float2 p = mul2(mul2(make_float2(x[4 * j], x[4 * j + 1]), rr), make_float2(w.x, w.y));
+    const float2 q = mul2(mul2(make_float2(x[4 * j + 2], x[4 * j + 3]), rr), make_float2(w.z, w.w));
+    x[4 * j] = p.x;
+    x[4 * j + 1] = p.y;
+    x[4 * j + 2] = q.x;
+    x[4 * j + 3] = q.y;
   }
 }
 #endif
@@ -593,7 +677,10 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
   pdl_wait_then_release();
 #ifdef SAW_ROPE_NORM
   __shared__ __align__(16) float gains[2][D];
-  for (int i = threadIdx.x; i < 2 * D; i += 32 * kBulkWarps) gains[i / D][i % D] = gain(p, i / D, i % D);
+  for (int i = threadIdx.x; i < 2 * D; i += 32 * kBulkWarps) {
+    const int d = i % D;
+    gains[i / D][4 * (((d >> 2) & 1) * (D / 8) + (d >> 3)) + (d & 3)] = gain(p, i / D, d);
+  }
   __syncthreads();
 #endif
   constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp
@@ -611,12 +698,28 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
   // the next item's position and slot are under way while one is worked on
   int pos_next = it < items ? p.positions[it / parts] : 0;
   int slot_next = it < items ? p.slot_mapping[it / parts] : 0;
+  // (with norms the next item comes without a division; without them that costs
+  // registers which the loads in flight need)
+  const int step_t = int(warps / parts), step_part = int(warps - uint32_t(step_t) * parts);
+  int t_next = int(it / parts), part_next = int(it - uint32_t(t_next) * parts);
   for (; it < items; it += warps) {
-    const int t = int(it / parts), part = int(it - uint32_t(t) * parts);
+    int t = t_next, part = part_next;
+    if constexpr (kNorm) {
+      t_next += step_t;
+      part_next += step_part;
+      if (part_next >= int(parts)) {
+        part_next -= int(parts);
+        ++t_next;
+      }
+    } else {
+      t = int(it / parts);
+      part = int(it - uint32_t(t) * parts);
+      t_next = int((it + warps) / parts);
+    }
     const int pos = pos_next, slot = slot_next;
     if (it + warps < items) {
-      pos_next = p.positions[(it + warps) / parts];
-      slot_next = p.slot_mapping[(it + warps) / parts];
+      pos_next = p.positions[t_next];
+      slot_next = p.slot_mapping[t_next];
     }
     const bool pos_ok = pos >= 0 && pos < p.max_pos;
     if (part < nq) {
@@ -646,7 +749,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
           widen8<F16IN>(w[k][0], x);
           widen8<F16IN>(w[k][1], x + 8);
 #ifdef SAW_ROPE_NORM
-          norm16<D>(x, gains[0], p.eps, a, hc);
+          norm16<D>(x, gains[0], p.eps, a, hc, lane);
 #endif
           turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
           if (h < h1) {
@@ -687,10 +790,13 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
         w1 = *reinterpret_cast<const uint4*>(src + (h + RPW) * D + 8 * hc);
       }
 #ifdef SAW_ROPE_NORM
-      if (tensor == 0) norm16<D>(x, gains[1], p.eps, a, hc);
+      if (tensor == 0) norm16<D>(x, gains[1], p.eps, a, hc, lane);
 #endif
       if (tensor == 0) turn16<D, LAYOUT>(x, ang, p.rope_dim, a, lane);
-      if (rot) rotate16<D>(x, p.block_h, p.c_h, hc, lane);
+      if (rot) {
+        if constexpr (kNorm) rotate16_packed<D>(x, p.block_h, p.c_h, hc, lane);
+        else rotate16<D>(x, p.block_h, p.c_h, hc, lane);
+      }
       float mn = fminf(x[0], x[1]), mx = fmaxf(x[0], x[1]);
 #pragma unroll
       for (int i = 2; i < 16; ++i) {

@@ -951,7 +951,8 @@ int32_t saw_norm_rope_append(const void* q, int64_t q_token_stride, const void* 
                             v_cache, num_pages, page_size, rotate_k, rotate_v, block_h,
                             formats & ~int32_t(SAW_FMT_F32_WEIGHT), dev_status);
   if (rc != SAW_OK) return rc;
-  if (!(eps > 0.0f) || std::isinf(eps) || !std::isfinite(weight_offset)) return SAW_ERR_INVALID_ARG;
+  // (the norm's root is exact from 2^-100 on)
+  if (!(eps >= 0x1p-100f) || std::isinf(eps) || !std::isfinite(weight_offset)) return SAW_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 15u)
     return SAW_ERR_INVALID_ARG;
   if (num_tokens == 0) return SAW_OK;

@@ -612,7 +612,7 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
  *               float32 with SAW_FMT_F32_WEIGHT in `formats`.  NULL: all 1
  *               (weight_offset is then not used).
  * weight_offset finite; added to every gain: 0, or 1 for gains kept as w - 1.
- * eps           positive and finite.
+ * eps           at least 2^-100, finite.
  * q_out may be q itself, as in saw_rope_append, whose other arguments, limits
  * and errors hold.  v is not normed.
  *

@@ -28,7 +28,7 @@ def _norm(L, **kw):
 
 
 @pytest.mark.parametrize("kw,expect", [
-    (dict(eps=0.0), INV), (dict(eps=-1e-6), INV), (dict(eps=NAN), INV), (dict(eps=INF), INV), (dict(off=NAN), INV),
+    (dict(eps=0.0), INV), (dict(eps=-1e-6), INV), (dict(eps=NAN), INV), (dict(eps=INF), INV), (dict(eps=1e-31), INV), (dict(off=NAN), INV),
     (dict(off=INF), INV), (dict(wq=MIS), INV), (dict(wk=MIS), INV), (dict(fmt=4), INV), (dict(fmt=16), INV),
     (dict(fmt=12), INV), (dict(T=-1), INV), (dict(hkv=0), INV), (dict(d=96), UNS), (dict(P=8), UNS), (dict(r=24), UNS),
     (dict(inter=2), INV), (dict(h=48), INV), (dict(k=None), INV), (dict(qo=None), INV), (dict(vc=None), INV),
