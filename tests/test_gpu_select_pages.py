@@ -82,6 +82,27 @@ def test_long_and_many(B, L, take):
     check(*case, lens, 2, 16, True, 64, take, 1, 3, False)
 
 
+@pytest.mark.parametrize("hkv", [4, 5, 8, 9, 16, 17, 40])
+@pytest.mark.parametrize("D,B,L", [(64, 1, 9000), (128, 3, 5000), (256, 1, 3000), (128, 90, 700), (128, 200, 500), (64, 40, 2500)])
+def test_kv_heads(D, B, L, hkv):
+    """Many kv-heads to a sequence: clusters and single CTAs that share its rows, and sizes beyond them."""
+    if B > 3 and hkv > 9:
+        B = 20
+    rng = np.random.default_rng(hkv)
+    lens = [L] + [int(x) for x in rng.integers(1, L, B - 1)]
+    case = make(B + L, lens, 2 * hkv, hkv, D, 16, BF, hkv % 2 == 1)
+    check(*case, lens, hkv, 16, True, 64, 21, 1, 2, hkv % 2 == 1)
+
+
+@pytest.mark.parametrize("hkv", [1, 8])
+def test_longest(hkv):
+    """As many pages as a call takes."""
+    lens = [16 * (1 << 18), 16 * 200000 + 5]
+    q, s, bt, pages = make(1, [40000, 30000], hkv, hkv, 64, 16, BF, False)
+    t = np.stack([np.resize(bt[0, :2500], 1 << 18), np.resize(bt[1, :1875], 1 << 18)]).astype(np.int32)
+    check(q, s, t, pages, lens, hkv, 16, True, 64, 300, 1, 2, False)
+
+
 @pytest.mark.parametrize("L", [4000, 40000])
 def test_ties_go_to_the_lower_page(L):
     """Few different summaries, so that most scores are equal; all equal; all zero (and -0 beside 0)."""
