@@ -292,6 +292,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
   }
 
+  // SPARSE: this lane's q and the first of its warp's page ids are under way with
+  // the length (ids past the list are not used), so that a CTA starts one round of
+  // latency sooner
+  constexpr int kQWords = DM::kE / 2;
+  uint32_t qsp[SPARSE ? kQHeads : 1][SPARSE ? kQWords : 1];
+  int idsp = -1;
+  if constexpr (SPARSE) {
+#pragma unroll
+    for (int i = 0; i < kQHeads; ++i) {
+      const int h = min(warp + i * kWarps, G - 1);
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (int64_t(seq) * p.num_q_heads + hq0 + h) * D) + kQWords * lane;
+#pragma unroll
+      for (int u = 0; u < kQWords; ++u) qsp[i][u] = src[u];
+    }
+    const int lp = split * p.pages_per_split + (warp + lane * kWarps) / C::kStepsPerPage;
+    if (lp < p.max_blocks) idsp = p.block_tables[(int64_t(seq) * p.num_kv_heads + kvh) * p.max_blocks + lp];
+  }
+
   const int64_t trow = SPARSE ? int64_t(seq) * p.num_kv_heads + kvh : seq;  // of the tables and lengths
   int L = behind ? __ldcg(p.seq_lens + trow) : p.seq_lens[trow];
   if (L < 0 || L > p.max_seq_len) {
@@ -356,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   // the (page, kv-head) chunk index of this warp's step i (-1: invalid page)
   auto chunk_id = [&](int i) {
     const int lp = p_begin + (warp + i * kWarps) / C::kStepsPerPage;
-    const int id = behind ? __ldcg(btab + lp) : btab[lp];
+    const int id = SPARSE && i == lane ? idsp : behind ? __ldcg(btab + lp) : btab[lp];
     if (id < 0 || id >= p.num_pages) {
       report(p.dev_status, SAW_ERR_DEVICE_INDEX);
       return -1;
@@ -544,7 +562,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
                                kE * (PAIR ? (lane & 15) : lane);
         const bool f16 = p.in_f16 != 0;
         uint32_t raw[kE / 2];
-        if (SHARED && behind) {
+        if constexpr (SPARSE) {
+#pragma unroll
+          for (int u = 0; u < kE / 2; ++u) raw[u] = qsp[qi][u];
+        } else if (SHARED && behind) {
           raw[0] = qpre[qi].x;
           raw[kE / 2 - 1] = qpre[qi].y;
         } else if (kE == 2) {
@@ -1132,6 +1153,80 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
   }
   __syncthreads();
+
+  if constexpr (SPARSE) {
+    if (direct) {
+      // ---- one split: a warp per head from here, lane l holding dims kE l ..,
+      // the inverse rotation in shuffles.  A list is short, so that a CTA's end
+      // counts: through shared memory, with a barrier per stride, 256 x 2048
+      // tokens took 126 us.
+      for (int h = warp; h < G; h += kWarps) {
+        const bool in = lane < min(kWarps, n_steps);
+        const float m = in ? red_m[lane * kMaxGroup + h] : -INFINITY;
+        float den = in ? red_l[lane * kMaxGroup + h] : 0.0f, zz = in ? red_z[lane * kMaxGroup + h] : 0.0f;
+        float M = m;
+#pragma unroll
+        for (int x = 1; x < kWarps; x <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+        const float f = in ? ex2(m - ((M == -INFINITY) ? 0.0f : M)) : 0.0f;
+        den *= f;
+        zz *= f;
+#pragma unroll
+        for (int x = 1; x < kWarps; x <<= 1) {
+          den += __shfl_xor_sync(kFull, den, x);
+          zz += __shfl_xor_sync(kFull, zz, x);
+        }
+        den = __shfl_sync(kFull, den, 0);
+        zz = __shfl_sync(kFull, zz, 0);
+        float x[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) x[e] = zz;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w >= n_steps) break;
+          const float fw = __shfl_sync(kFull, f, w);
+          const float* a = red_acc + (w * kMaxGroup + h) * kRedStride + red_col(kE * lane);
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[e] = fmaf(a[e], fw, x[e]);
+        }
+        const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+        if (p.rotate_v) {
+#pragma unroll
+          for (int d = 1; d < kE; d <<= 1)
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+              if (!(e & d)) {
+                const float a = x[e], b = x[e + d];
+                x[e] = a + b;
+                x[e + d] = a - b;
+              }
+          for (int d = kE; d < p.block_h; d <<= 1) {
+            const float sign = (lane & (d / kE)) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) x[e] = fmaf(x[e], sign, __shfl_xor_sync(kFull, x[e], d / kE));
+          }
+        }
+        const float post = p.rotate_v ? inv * p.c_h : inv;
+        const int64_t at = (int64_t(seq) * p.num_q_heads + hq0 + h) * D + kE * lane;
+        if (p.out16) {  // the one rounding of a 16-bit output
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) {
+            uint32_t w;
+            if (p.in_f16) {
+              w = pack_half2(x[e] * post, x[e + 1] * post);
+            } else {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(x[e] * post, x[e + 1] * post);
+              w = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            reinterpret_cast<uint32_t*>(p.out16 + at)[e / 2] = w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) *reinterpret_cast<float2*>(p.out + at + e) = make_float2(x[e] * post, x[e + 1] * post);
+        }
+      }
+      return;
+    }
+  }
 
   // ---- merge the warps.  Weights 2^(m_w - M) per (head, warp): thread
   // 16h + w of warps 0-3, reduced over the 16 warps with shuffles inside
