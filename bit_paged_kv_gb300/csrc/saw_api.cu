@@ -129,6 +129,35 @@ int32_t make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t page_size, int
   return SAW_OK;
 }
 
+// Split plan of the sparse decode, whose lists are short.  Where the units leave
+// SMs idle, 16-warp CTAs in one wave, split down to 256 tokens, but not lists of
+// 512: a split list is merged, which takes about 3 us (8 units, us, splits of 256 /
+// 512 / 1024 / 2048 tokens: 2048 tokens 8.5 / 9.1 / 10.6 / 9.8, 512 tokens 8.4 /
+// 5.7; 32 units of 2048: 13.7 / 9.3 / 10.7 / 10.1).  4-warp CTAs from two and a
+// half units per SM on (GQA 4, 384 units 27.2 against 30.8 with 8 warps; 320, GQA
+// 8, 33.7 against 31.1).
+int32_t make_sparse_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t page_size, int32_t max_len,
+                         int32_t* splits_out, int32_t* pps_out, int32_t* warps_out) {
+  int32_t warps = 16;
+  const int32_t rc = make_plan(num_seqs, num_kv_heads, page_size, max_len, 0, splits_out, pps_out, &warps);
+  if (rc != SAW_OK) return rc;
+  const int64_t units = int64_t(num_seqs > 0 ? num_seqs : 1) * num_kv_heads, pages = ceil_div(max_len, page_size);
+  const int sms_raw = sm_count();
+  const int64_t sms = sms_raw > 0 ? sms_raw : 148;
+  if (units <= sms) {
+    const int64_t most = max_len <= 512 ? 1 : std::min<int64_t>(ceil_div(max_len, 256), sms / units);
+    warps = 16;
+    const int64_t unit = std::max<int64_t>(1, warps / (page_size / 16));  // whole turns for every warp
+    const int64_t pps = std::max<int64_t>(ceil_div(ceil_div(std::max<int64_t>(pages, 1), most), unit) * unit, 1);
+    *pps_out = int32_t(pps);
+    *splits_out = int32_t(std::max<int64_t>(ceil_div(pages, pps), 1));
+  } else if (*splits_out == 1 && 2 * units >= 5 * sms) {
+    warps = 4;
+  }
+  if (warps_out) *warps_out = warps;
+  return SAW_OK;
+}
+
 // Split plan of the BF16 baseline: one 8-warp CTA per SM, at least 1024
 // tokens per split, the split count with the least wave quantisation.
 int32_t make_plan_bf16(int32_t num_seqs, int32_t num_kv_heads, int32_t page_size,
@@ -1074,7 +1103,7 @@ size_t saw_sparse_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
                                          int32_t page_size, int32_t max_sel_len) {
   if (!head_dim_ok(head_dim) || num_q_heads <= 0) return 0;
   int32_t splits = 0, pps = 0;
-  if (make_plan(num_seqs, num_kv_heads, page_size, max_sel_len, 0, &splits, &pps) != SAW_OK || splits <= 1)
+  if (make_sparse_plan(num_seqs, num_kv_heads, page_size, max_sel_len, &splits, &pps, nullptr) != SAW_OK || splits <= 1)
     return 0;
   const size_t rows = size_t(num_seqs) * size_t(num_q_heads) * size_t(splits);
   return sparse_ticket_bytes(num_seqs, num_kv_heads) + rows * size_t(head_dim + 2) * 4;
@@ -1097,7 +1126,7 @@ int32_t saw_sparse_decode_int4(const void* q, const void* k_cache, const void* v
                               rotate_k, rotate_v, block_h, sm_scale, static_cast<float*>(out), nullptr,
                               0, INT32_MAX, formats & ~int32_t(SAW_FMT_OUT_INPUT), dev_status);
   if (rc != SAW_OK || num_seqs == 0) return rc;
-  rc = make_plan(num_seqs, num_kv_heads, page_size, max_sel_len, 0, &p.num_splits, &p.pages_per_split, &p.warps);
+  rc = make_sparse_plan(num_seqs, num_kv_heads, page_size, max_sel_len, &p.num_splits, &p.pages_per_split, &p.warps);
   if (rc != SAW_OK) return rc;
   const size_t need = saw_sparse_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, page_size,
                                                         max_sel_len);
