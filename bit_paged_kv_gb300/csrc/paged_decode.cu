@@ -224,7 +224,9 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves
 // the first half; each column's output is its own half.  The tensor cores do the
 // zero products; every per-tile cost is shared by the two kv-heads.
 // SPARSE (saw_sparse_decode_int4): block_tables has a row, and seq_lens an
-// entry, per (sequence, kv-head).
+// entry, per (sequence, kv-head).  Lists are short, so a CTA's start and end weigh
+// as much as its loop: 256 sequences of 128 16-token pages, GQA 8 (570 MB), 115 us,
+// 5.0 TB/s (GQA 4 99.6), in 3.4 waves of 4-warp CTAs; 8-warp ones 128.
 // FINE (sparse, outputs of more than 8 bits): p*s enters the PV product as a
 // binary16 and its remainder, 22 bits together.  As one binary16 its rounding
 // (2^-11) is of the size of a binary16 output's own and shows where few pages

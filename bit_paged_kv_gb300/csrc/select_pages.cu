@@ -16,10 +16,20 @@
 //
 // One CTA takes one (sequence, kv-head), or a cluster of them a run of its pages
 // each; the pages' keys stay in shared memory.  A warp scores 32 pages at a time,
-// the next 64's rows under way meanwhile.  The threshold comes from one
+// the next 64's rows under way meanwhile.  The last entry of the list comes from one
 // histogram of the scores between their extremes (radix digits of the keys would
 // put nearly all of them in a few bins) and a ranking of the keys in its bin;
 // where that bin holds too many (ties, far outliers), digit by digit.
+//
+// Bound: many pages, by the rate at which an SM takes in pieces of lines: a page
+// costs a kv-head three 32-byte sectors in two places, and 0.8 to 0.9 sectors per ns
+// and SM come back (16 x 131072 tokens 47 us, the rows alone 28, without the words
+// 33; 10.6 at the measured copy rate; head_dim 256, half the pages and the same
+// bytes, 28.3).  Whole rows by bulk copies of 544 bytes, a cluster per sequence with
+// its kv-heads' keys dealt to owners, took 136 us; two kv-heads to a CTA 44, but 16.1
+// against 13.0 at 4 x 65536 tokens and 24 against 22 at 256 x 4096.  Few pages, by the
+// chain of rounds: length, page ids, rows, extremes, histogram, ranking, list (1 x
+// 32768 tokens 8.6 us in clusters, 64 x 4096 8.6).
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -38,21 +48,24 @@ constexpr int kStrip = 32;                           // pages per warp and step:
 constexpr int kRing = 2;                             // strips under way per warp
 constexpr int kCands = 128;                          // a CTA's keys in the threshold's bin
 constexpr int kAllCands = 512;                       // the cluster's, ranked against one another
-constexpr int kAlone = 256;                          // pages that a CTA takes before more join it
-constexpr int kSmall2 = 256, kSmall4 = 512;
+// Pages that a CTA takes before more join it: 1 x 32768 tokens 8.6 us with 256, 10.3
+// with 512, 12.0 with 1024; 4 x 65536 12.9, 13.0, 13.2.
+constexpr int kAlone = 256;
+// More units than 8-warp CTAs fit: 4-warp ones for at most so many pages, so that
+// more units are under way (256 sequences of 62 to 256 pages 21.6 us against 25.8,
+// 22.6 with 2 warps; 128 of 256 to 512 19.5 against 21.3).
+constexpr int kSmall = 512;
 constexpr int kMaxCtas = 8;                          // per cluster
 constexpr int kMaxChunk = kSelectMaxPages / kMaxCtas;  // pages per CTA
 static_assert(kMaxChunk % kStrip == 0, "whole strips");
 constexpr int warps_per_sm(int D) { return D == 256 ? 16 : 32; }
-// a strip in shared memory: 32 rows of codes, 32 words
-__host__ __device__ constexpr int strip_bytes(int D) { return kStrip * (D / 2 + 4); }
+// a strip in shared memory: 32 rows of codes, then the 16 bytes that hold each
+// row's word (copied past L1: 64 x 16384 tokens 15.8 us, by words through it 17.4)
+__host__ __device__ constexpr int strip_bytes(int D) { return kStrip * (D / 2 + 16); }
 __host__ __device__ constexpr int ring_bytes(int D, int warps) { return warps * kRing * strip_bytes(D); }
 
 __device__ __forceinline__ void async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // The larger, NaN if either is.
@@ -311,7 +324,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(D) / W) select_pages_kern
   const int32_t* run = bt + lo + begin;
   const int64_t stride = summary_stride(hkv, D);
   const uint8_t* codes = p.summary + kvh * (D / 2);
-  const uint8_t* words = p.summary + hkv * (D / 2) + 4 * kvh;
+  const uint8_t* words = p.summary + hkv * (D / 2) + (4 * kvh & ~15);
   uint8_t* ring = dyn + warp * (kRing * strip_bytes(D));
   constexpr int kStep = W * kStrip;
   // this lane's page of the strip at i0 (-1: none, or bad)
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(D) / W) select_pages_kern
         const int64_t off = __shfl_sync(kAll, id, at / kParts) * stride;
         async16(dst + 16 * at, codes + off + 16 * (at % kParts));
       }
-      async4(dst + kStrip * (D / 2) + 4 * lane, words + id * stride);
+      async16(dst + kStrip * (D / 2) + 16 * lane, words + id * stride);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     return ok;
@@ -366,7 +379,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(D) / W) select_pages_kern
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
     __syncwarp();
     const uint8_t* st = ring + stage * strip_bytes(D);
-    float best = score_strip<D, BFM>(st, D / 2, st + kStrip * (D / 2), 4, b, qs, jj, lane);
+    float best = score_strip<D, BFM>(st, D / 2, st + kStrip * (D / 2) + (4 * kvh & 15), 16, b, qs, jj, lane);
     if (!ok0) best = -INFINITY;
     const int i = i0 + lane;
     if (i < count) {
@@ -660,8 +673,7 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
   const int max_pages = (p.max_seq_len + p.page_size - 1) / p.page_size;
   const int64_t units = int64_t(p.num_seqs) * p.num_kv_heads;
   const int64_t slots = int64_t(sms) * warps_per_sm(D) / 8;  // 8-warp CTAs that are resident together
-  if (units > slots && max_pages <= kSmall2) return launch_select_w<D, BFM, 2>(p, 1, stream);
-  if (units > slots && max_pages <= kSmall4) return launch_select_w<D, BFM, 4>(p, 1, stream);
+  if (units > slots && max_pages <= kSmall) return launch_select_w<D, BFM, 4>(p, 1, stream);
   int ctas = 1;
   while (ctas < kMaxCtas && 2 * units * ctas <= slots && max_pages > ctas * kAlone) ctas *= 2;
   while (max_pages > ctas * kMaxChunk) ctas *= 2;

@@ -619,10 +619,10 @@ int32_t saw_prefix_decode_int4(const void* q, const void* k_cache, const void* v
  * Per row x of q or k, in binary32, each step rounded once: ss = the sum of
  * the squares by a binary tree over the element index (neighbours, then pairs
  * of neighbours, ...), r = 1 / sqrt(ss / head_dim + eps), y = (x r) g with g =
- * w + weight_offset (no second product without weights).  The whole head is normed, also where only part of it is
- * turned.  y is not rounded to 16 bits before the turn, and the rest is
- * saw_rope_append's rule, so the bytes are fully determined.  Squares have to
- * be within binary32.
+ * w + weight_offset (no second product without weights).  The whole head is normed, also
+ * where only part of it is turned.  y is not rounded to 16 bits before the turn, and the
+ * rest is saw_rope_append's rule, so the bytes are fully determined.  Squares have to be
+ * within binary32.
  */
 #define SAW_FMT_F32_WEIGHT 8
 int32_t saw_norm_rope_append(const void* q, int64_t q_token_stride, const void* k,
@@ -654,8 +654,8 @@ size_t saw_summary_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_d
  * new_lens      device int32 [num_seqs]: tokens that the step appended, or NULL
  *               (all of them; a count above seq_lens counts as all too).
  * max_new_len   host bound on the smaller of the two; sizes the grid.
- * summary       device, saw_summary_bytes(...), 16-byte aligned.  Summaries go by physical page, so
- *               forks of a sequence share them.
+ * summary       device, saw_summary_bytes(...), 16-byte aligned.  Summaries go by physical
+ *               page, so forks of a sequence share them.
  * Pages floor((L - n) / page_size) to floor(L / page_size) - 1 of a sequence
  * are written; a page that is not full has no summary (and none is needed: the
  * last page is always taken).
@@ -688,7 +688,8 @@ int32_t saw_page_summary(const void* k_cache, const int32_t* block_tables,
  * q             device bfloat16 (binary16 with SAW_FMT_F16_INPUT)
  *               [num_seqs][num_q_heads][head_dim], 16-byte aligned.
  * summary       saw_page_summary's, of every page but the last of each sequence.
- * max_seq_len   host bound on seq_lens; max_blocks_per_seq pages must hold it.
+ * max_seq_len   host bound on seq_lens; max_blocks_per_seq pages must hold it.  It sizes
+ *               shared memory: a loose one leaves less room for other work.
  * last_pages    at least 1; first_pages + last_pages at most max_selected.
  * sel_tables    device int32 [num_seqs][num_kv_heads][max_selected]: physical
  *               ids from block_tables, in the order of the sequence, -1 behind
@@ -696,12 +697,12 @@ int32_t saw_page_summary(const void* k_cache, const int32_t* block_tables,
  * sel_pages     the same as page numbers of the sequence, or NULL.
  * sel_lens      device int32 [num_seqs][num_kv_heads]: tokens in those pages.
  *
- * Per q-head: q' = H q / sqrt(h) by saw_quantize_append's butterfly (q itself with rotate_k 0), qs =
- * max|q'| / 127, m_d = round-half-even(q'_d (1/qs)) in -127 .. 127 (0 where qs is
- * below 2^-126); with the summary's codes n, scale s and zero z: score = qs (s
- * (sum m n) + z (sum m)), the largest over the kv-head's q-heads.  The sums are whole
- * numbers and exact, every other step one binary32 rounding, so the lists are
- * fully determined: equal scores (-0 and 0 are equal, a NaN counts as -infinity) go to the lower page.
+ * Per q-head: q' = H q / sqrt(h) by saw_quantize_append's butterfly (q itself with rotate_k
+ * 0), qs = max|q'| / 127, m_d = round-half-even(q'_d (1/qs)) in -127 .. 127 (0 where qs is
+ * below 2^-126); with the summary's codes n, scale s and zero z: score = qs (s (sum m n) +
+ * z (sum m)), the largest over the kv-head's q-heads.  The sums are whole numbers and
+ * exact, every other step one binary32 rounding, so the lists are fully determined: equal
+ * scores (-0 and 0 are equal, a NaN counts as -infinity) go to the lower page.
  *
  * A length below 0 or above max_seq_len is treated as 0 (an empty list) and
  * reported as SAW_ERR_DEVICE_INDEX; a page id outside [0, num_pages) among
