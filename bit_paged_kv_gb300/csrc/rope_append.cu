@@ -362,7 +362,7 @@ cudaError_t launch_rows(const Params& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------ bulk
 //
-// Large batches.  Item = (token, part): up to kQPart q-heads, or the token's K
+// Large batches.  Item = (token, part): up to q_part(D) q-heads, or the token's K
 // rows, or its V rows; every warp walks items on its own, so that the q parts
 // (pure traffic) and the K and V parts (150 or so instructions a row, which
 // alone would be bound by issue) of different warps share an SM.  A lane holds
@@ -385,7 +385,9 @@ constexpr int kRounds = 4;  // rounds of q-head loads in flight
 // tokens 6.1 / 4.4; 32 q-heads, half the head turned, 64 tokens 2.8 / 4.9, 256
 // tokens 5.0 / 4.9, 512 tokens 8.2 / 5.6.
 constexpr int64_t kBulkMinElems = int64_t(5) << 18;
-constexpr int kQPart = 16;  // q-heads per item
+// q-heads per item (with norms, 8192 tokens: head_dim 64 24.3 us with 32, 27.9 with
+// 16; 256 75.1 and 77.1; 128 41.2 and 41.9, but 131072 tokens 586 and 580)
+__host__ __device__ constexpr int q_part(int D) { return kNorm && D != 128 ? 32 : 16; }
 enum { kHalfWhole = 0, kHalfPart = 1, kInter = 2, kHalfBit = 3 };  // whole head; any part; -; r / 16 a power of two
 // CTAs per SM (85 or 128 registers a thread): 131072 tokens 484 us with three,
 // 527 with two; the layout that exchanges partners by shuffles keeps two (2047
@@ -686,6 +688,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
   }
   __syncthreads();
 #endif
+  constexpr int kQPart = q_part(D);
   constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR;
@@ -827,7 +830,7 @@ __global__ void __launch_bounds__(32 * kBulkWarps, bulk_ctas(LAYOUT))
 
 template <int D, bool F16IN, int LAYOUT>
 cudaError_t launch_bulk_l(const Params& p, int sms, cudaStream_t stream) {
-  const int parts = (p.num_q_heads + kQPart - 1) / kQPart + p.num_tensors;
+  const int parts = (p.num_q_heads + q_part(D) - 1) / q_part(D) + p.num_tensors;
   const int64_t items = int64_t(p.num_tokens) * parts;
   const int64_t want = (items + kBulkWarps - 1) / kBulkWarps;
   cudaLaunchConfig_t cfg = {};
