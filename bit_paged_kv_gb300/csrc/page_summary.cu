@@ -17,9 +17,9 @@
 //
 // Bound: issue (75 % of the slots where the pages are many), half of it the masks,
 // one per code on a pipe of half rate.  131072 tokens, 8 kv-heads, D 128 (76 MB):
-// 24.7 us (11.1 at the measured copy rate), four times as many 85 us; with
+// 22.1 us (11.1 at the measured copy rate), four times as many 74; with
 // conversions 37, the nibbles under 2^23's exponent 36, one kv-head a warp 26.
-// 64-token pages 22.3 us.
+// 64-token pages 21.1 us.
 #include <algorithm>
 
 #include "saw_device.cuh"
@@ -30,7 +30,7 @@ namespace saw {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;                            // (131072 tokens 22.1 us, with eight 24.4)
 // Groups of kv-heads per warp, one after another: 131072 tokens 37.0 us with one,
 // 28.8 with two, 24.8 with four and with eight.  (A ring in shared memory filled by
 // bulk copies instead of registers: 26.3 us, 37 chunks of 64-token pages 18.6

@@ -23,11 +23,11 @@
 //
 // Bound: many pages, by the rate at which an SM takes in pieces of lines: a page
 // costs a kv-head three 32-byte sectors in two places, and 0.8 to 0.9 sectors per ns
-// and SM come back (16 x 131072 tokens 47 us, the rows alone 28, without the words
-// 33; 10.6 at the measured copy rate; head_dim 256, half the pages and the same
-// bytes, 28.3).  Whole rows by bulk copies of 544 bytes, a cluster per sequence with
-// its kv-heads' keys dealt to owners, took 136 us; two kv-heads to a CTA 44, but 16.1
-// against 13.0 at 4 x 65536 tokens and 24 against 22 at 256 x 4096.  Few pages, by the
+// and SM come back (16 x 131072 tokens 42.6 us; in clusters of four 47, the rows
+// alone 28, without the words 33; 10.6 at the measured copy rate).  Whole rows by
+// bulk copies of 544 bytes, a cluster per sequence with its kv-heads' keys dealt to
+// owners, took 136 us; two kv-heads to a CTA 44, but 16.1 against 13.0 at 4 x 65536
+// tokens and 24 against 22 at 256 x 4096.  Few pages, by the
 // chain of rounds: length, page ids, rows, extremes, histogram, ranking, list (1 x
 // 32768 tokens 8.6 us in clusters, 64 x 4096 8.6).
 #include <algorithm>
@@ -49,7 +49,9 @@ constexpr int kRing = 2;                             // strips under way per war
 constexpr int kCands = 128;                          // a CTA's keys in the threshold's bin
 constexpr int kAllCands = 512;                       // the cluster's, ranked against one another
 // Pages that a CTA takes before more join it: 1 x 32768 tokens 8.6 us with 256, 10.3
-// with 512, 12.0 with 1024; 4 x 65536 12.9, 13.0, 13.2.
+// with 512, 12.0 with 1024; 4 x 65536 12.9, 13.0, 13.2.  Clusters grow while their
+// CTAs are a third of what is resident together, not half (16 x 131072 42.6 us
+// against 47.4, 16 x 32768 14.7 against 20.8, but 8 x 131072 29.2 against 26.4).
 constexpr int kAlone = 256;
 // More units than 8-warp CTAs fit: 4-warp ones for at most so many pages, so that
 // more units are under way (256 sequences of 62 to 256 pages 21.6 us against 25.8,
@@ -675,7 +677,7 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
   const int64_t slots = int64_t(sms) * warps_per_sm(D) / 8;  // 8-warp CTAs that are resident together
   if (units > slots && max_pages <= kSmall) return launch_select_w<D, BFM, 4>(p, 1, stream);
   int ctas = 1;
-  while (ctas < kMaxCtas && 2 * units * ctas <= slots && max_pages > ctas * kAlone) ctas *= 2;
+  while (ctas < kMaxCtas && 3 * units * ctas <= slots && max_pages > ctas * kAlone) ctas *= 2;
   while (max_pages > ctas * kMaxChunk) ctas *= 2;
   return launch_select_w<D, BFM, 8>(p, ctas, stream);
 }
