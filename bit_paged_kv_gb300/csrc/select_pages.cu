@@ -21,15 +21,14 @@
 // put nearly all of them in a few bins) and a ranking of the keys in its bin;
 // where that bin holds too many (ties, far outliers), digit by digit.
 //
-// Bound: many pages, by the rate at which an SM takes in pieces of lines: a page
-// costs a kv-head three 32-byte sectors in two places, and 0.8 to 0.9 sectors per ns
-// and SM come back (16 x 131072 tokens 42.6 us; in clusters of four 47, the rows
-// alone 28, without the words 33; 10.6 at the measured copy rate).  Whole rows by
-// bulk copies of 544 bytes, a cluster per sequence with its kv-heads' keys dealt to
-// owners, took 136 us; two kv-heads to a CTA 44, but 16.1 against 13.0 at 4 x 65536
-// tokens and 24 against 22 at 256 x 4096.  Few pages, by the
-// chain of rounds: length, page ids, rows, extremes, histogram, ranking, list (1 x
-// 32768 tokens 8.6 us in clusters, 64 x 4096 8.6).
+// Bound: many pages, by how fast an SM takes in pieces of lines (a page costs a
+// kv-head three 32-byte sectors in two places) and by issue behind it: 16 x 131072
+// tokens 33.0 us (10.6 at the measured copy rate), the registers and warps that a
+// unit gets counting for more than CTAs (below).  Whole rows by bulk copies of 544
+// bytes, a cluster per sequence with its kv-heads' keys dealt to owners, took 136 us,
+// two kv-heads to a CTA 44.  Few pages, by the chain of rounds: length, page ids,
+// rows, extremes, histogram, ranking, list (1 x 32768 tokens 8.5 us in clusters; all
+// keys to one CTA of the cluster, with fewer barriers, 9.5).
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -48,19 +47,22 @@ constexpr int kStrip = 32;                           // pages per warp and step:
 constexpr int kRing = 2;                             // strips under way per warp
 constexpr int kCands = 128;                          // a CTA's keys in the threshold's bin
 constexpr int kAllCands = 512;                       // the cluster's, ranked against one another
-// Pages that a CTA takes before more join it: 1 x 32768 tokens 8.6 us with 256, 10.3
-// with 512, 12.0 with 1024; 4 x 65536 12.9, 13.0, 13.2.  Clusters grow while their
-// CTAs are a third of what is resident together, not half (16 x 131072 42.6 us
-// against 47.4, 16 x 32768 14.7 against 20.8, but 8 x 131072 29.2 against 26.4).
+// Pages that a CTA takes before more join it, and more units than leave SMs idle.
+// (1 x 32768 tokens 8.5 us, in clusters of four 10.3, of two 12.0.)  A cluster's
+// barriers cost more than the SMs that it adds are worth soon: 16 x 32768, 128
+// units, 12.4 us alone, in pairs 14.4, in fours 20.8; 8 x 131072, 64 units, in pairs
+// 27.7, in fours 24.4, in eights 26.5.
 constexpr int kAlone = 256;
-// More units than 8-warp CTAs fit: 4-warp ones for at most so many pages, so that
-// more units are under way (256 sequences of 62 to 256 pages 21.6 us against 25.8,
-// 22.6 with 2 warps; 128 of 256 to 512 19.5 against 21.3).
-constexpr int kSmall = 512;
+// CTA shapes.  4 warps, eight per SM, for short lists, so that more units are under
+// way (256 sequences of 62 to 256 pages 21.6 us, with 8 warps 25.8); 16 warps for few
+// long ones (16 x 131072 tokens 33.0 us, with 8 warps 42); else 8 warps with what
+// registers the units leave (32 x 65536, 256 units, two per SM 28.1 us, with the
+// registers of three 37, of four 38.5; 64 x 16384, 512 units, 17.8, 14.1, 15.7).
+constexpr int kSmall = 512, kLong = 1024;
 constexpr int kMaxCtas = 8;                          // per cluster
 constexpr int kMaxChunk = kSelectMaxPages / kMaxCtas;  // pages per CTA
 static_assert(kMaxChunk % kStrip == 0, "whole strips");
-constexpr int warps_per_sm(int D) { return D == 256 ? 16 : 32; }
+constexpr int kMaxAlone = 16384;                     // pages of a 16-warp CTA
 // a strip in shared memory: 32 rows of codes, then the 16 bytes that hold each
 // row's word (copied past L1: 64 x 16384 tokens 15.8 us, by words through it 17.4)
 __host__ __device__ constexpr int strip_bytes(int D) { return kStrip * (D / 2 + 16); }
@@ -226,14 +228,14 @@ struct Cand {
 };
 template <int W>
 struct Shared {
-  static constexpr int kBins = W == 8 ? 1024 : 512;
+  static constexpr int kBins = W >= 8 ? 1024 : 512;
   alignas(16) uint32_t hist[kBins];
   alignas(8) float range[2];                         // this CTA's finite scores
   float qs[kMaxGroup], j[kMaxGroup];
   float least[W], most[W];                           // each warp's finite scores
   uint32_t above;                                    // this CTA's keys in larger bins
   uint32_t cands;
-  Cand cand[kCands], all[W == 8 ? kAllCands : 1];    // (fewer warps: never in clusters)
+  Cand cand[kCands], all[W == 8 ? kAllCands : 1];    // (clusters are of 8 warps)
   uint32_t run[W], sum[W];                           // of the warps: entries of the list; scratch
   uint32_t listed[kMaxCtas];                         // of the cluster's CTAs: entries of the list
   uint32_t bin, want, key;
@@ -273,8 +275,8 @@ __device__ __forceinline__ void find_bin(Shared<W>& sh, int nb, uint32_t wanted,
   __syncthreads();
 }
 
-template <int D, bool BFM, int W>
-__global__ void __launch_bounds__(32 * W, warps_per_sm(D) / W) select_pages_kernel(const SelectParams p) {
+template <int D, bool BFM, int W, int PER_SM>
+__global__ void __launch_bounds__(32 * W, PER_SM) select_pages_kernel(const SelectParams p) {
   pdl_wait_then_release();
   constexpr int kThr = 32 * W, kBins = Shared<W>::kBins;
   cg::cluster_group cluster = cg::this_cluster();
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(D) / W) select_pages_kern
         m += cnt[r];
       }
       fits = fits && m <= kAllCands;
-      static_assert(W < 8 || W == kMaxCtas, "a warp per CTA of the cluster");
+      static_assert(W != 8 || W == kMaxCtas, "a warp per CTA of the cluster");
       if (fits && mine > 0) {
         const Cand* o = cluster.map_shared_rank(sh.cand, warp);
         for (uint32_t i = lane; i < mine; i += 32) sh.all[at + i] = o[i];
@@ -644,14 +646,14 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(D) / W) select_pages_kern
   if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int D, bool BFM, int W>
+template <int D, bool BFM, int W, int PER_SM>
 cudaError_t launch_select_w(const SelectParams& p, int ctas, cudaStream_t stream) {
   const int max_pages = std::max((p.max_seq_len + p.page_size - 1) / p.page_size, 1);
   const int chunk = ((max_pages + ctas - 1) / ctas + kStrip - 1) / kStrip * kStrip;
-  auto kernel = select_pages_kernel<D, BFM, W>;
+  auto kernel = select_pages_kernel<D, BFM, W, PER_SM>;
   // (the most that any call needs, so that no thread lowers another's)
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               ring_bytes(D, W) + kMaxChunk * 4);
+                                               ring_bytes(D, W) + (W == 16 ? kMaxAlone : kMaxChunk) * 4);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas), unsigned(p.num_kv_heads), unsigned(p.num_seqs));
@@ -674,12 +676,16 @@ template <int D, bool BFM>
 cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
   const int max_pages = (p.max_seq_len + p.page_size - 1) / p.page_size;
   const int64_t units = int64_t(p.num_seqs) * p.num_kv_heads;
-  const int64_t slots = int64_t(sms) * warps_per_sm(D) / 8;  // 8-warp CTAs that are resident together
-  if (units > slots && max_pages <= kSmall) return launch_select_w<D, BFM, 4>(p, 1, stream);
+  constexpr int kWide = D == 256 ? 2 : 1;            // (its rows and queries take twice the registers)
+  if (units > 2 * int64_t(sms) && max_pages <= kSmall) return launch_select_w<D, BFM, 4, 8 / kWide>(p, 1, stream);
   int ctas = 1;
-  while (ctas < kMaxCtas && 3 * units * ctas <= slots && max_pages > ctas * kAlone) ctas *= 2;
+  while (ctas < kMaxCtas && (ctas == 1 ? 3 * units <= 2 * int64_t(sms) : units * ctas <= sms) && max_pages > ctas * kAlone)
+    ctas *= 2;
   while (max_pages > ctas * kMaxChunk) ctas *= 2;
-  return launch_select_w<D, BFM, 8>(p, ctas, stream);
+  if (ctas == 1 && units <= sms && max_pages > kLong && max_pages <= kMaxAlone)
+    return launch_select_w<D, BFM, 16, 1>(p, 1, stream);
+  if (units * ctas <= 2 * int64_t(sms)) return launch_select_w<D, BFM, 8, 2>(p, ctas, stream);
+  return launch_select_w<D, BFM, 8, kWide == 2 ? 2 : 3>(p, ctas, stream);
 }
 
 }  // namespace
