@@ -247,9 +247,10 @@ struct Shared {
 template <int W, class Count>
 __device__ __forceinline__ void find_bin(Shared<W>& sh, int nb, uint32_t wanted, int tid, Count&& count_of) {
   const int warp = tid >> 5, lane = tid & 31;
-  const int per = nb / (32 * W), top = nb - 1 - tid * per;  // this thread's bins: top, top - 1, ..
+  // this thread's bins: top, top - 1, ..  (16 warps: some threads have none of 256)
+  const int per = (nb + 32 * W - 1) / (32 * W), top = nb - 1 - tid * per;
   uint32_t sum = 0;
-  for (int j = 0; j < per; ++j) sum += count_of(top - j);
+  for (int j = 0; j < per && j <= top; ++j) sum += count_of(top - j);
   uint32_t above = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -262,7 +263,7 @@ __device__ __forceinline__ void find_bin(Shared<W>& sh, int nb, uint32_t wanted,
 #pragma unroll
   for (int w = 0; w < W; ++w) above += w < warp ? sh.sum[w] : 0u;
   if (above < wanted && wanted <= above + sum) {     // (one thread)
-    for (int j = 0; j < per; ++j) {
+    for (int j = 0; j < per && j <= top; ++j) {
       const uint32_t v = count_of(top - j);
       if (wanted <= above + v) {
         sh.bin = uint32_t(top - j);

@@ -181,3 +181,23 @@ def test_other_stream_and_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert np.array_equal(tables.cpu().numpy(), want[0]) and np.array_equal(out.cpu().numpy(), want[2])
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,hkv,L", [(13, 8, 20000), (30, 8, 9000), (60, 8, 8500), (80, 8, 4000), (8, 8, 20000)])
+def test_cta_shapes(B, hkv, L, D, ties):
+    """Grids that take 16-warp CTAs, 8-warp ones with either register count, 4-warp ones and
+    clusters; few different summaries, so that a histogram cannot part them, or many."""
+    rng = np.random.default_rng(B + D)
+    lens = [L] + [int(x) for x in rng.integers(L // 2, L, B - 1)]
+    q, s, bt, pages = make(B + D, lens[:3], hkv, hkv, D, 16, BF, False)
+    # (the sequences share the first three's pages)
+    t = np.full((B, bt.shape[1]), -1, np.int32)
+    for b in range(B):
+        t[b, :-(-lens[b] // 16)] = rng.permutation(pages)[:-(-lens[b] // 16)]
+    q = torch.from_numpy(rng.standard_normal((B, hkv, D)).astype(np.float32)).to(BF).cuda()
+    if ties:
+        row = s.reshape(pages, -1)
+        row[:] = row[np.arange(pages) % 2]
+    check(q, s, t, pages, lens, hkv, 16, True, 64, 70, 1, 2, False)
