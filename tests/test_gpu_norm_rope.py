@@ -97,6 +97,14 @@ def test_sizes_formats_and_gains(T, hq, hkv, P, dt, meta, wdt, offset, eps):
     check(*case, P, True, T % 2 == 0, 128, T % 3 == 0, meta, w=gains(128, wdt, offset), offset=offset, eps=eps)
 
 
+@pytest.mark.parametrize("D,hq,hkv", [(64, 40, 5), (64, 65, 1), (128, 33, 3), (128, 64, 8), (256, 40, 2)])
+def test_many_heads(D, hq, hkv):
+    """More q-heads than an item takes, and a rest."""
+    for T in (3, 700):
+        case = make(D + hq, T, hq, hkv, D, 32, D, BF)
+        check(*case, 32, True, True, 64, False, False, w=gains(D, torch.float32, 1.0), offset=1.0)
+
+
 @pytest.mark.parametrize("T", [50, 3000])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_without_gains_q_or_v_and_in_place(D, T):

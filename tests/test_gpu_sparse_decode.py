@@ -99,7 +99,8 @@ def test_rotations_and_scale(D, rot_k, rot_v):
 
 
 @pytest.mark.parametrize("hq,D", [(2, 128), (8, 128), (16, 128), (8, 64), (4, 256)])
-@pytest.mark.parametrize("B,n", [(1, 5000), (2, 1), (2, 15), (2, 17), (2, 16 * 40), (3, 2049), (180, 150), (400, 20)])
+@pytest.mark.parametrize("B,n", [(1, 5000), (2, 1), (2, 15), (2, 17), (2, 16 * 40), (3, 2049), (180, 150), (400, 20),
+                                 (190, 700)])
 def test_lengths_and_grids(B, n, hq, D):
     """One token to several splits; grids of one wave, of 8-warp and of 4-warp CTAs."""
     rng = np.random.default_rng(n)
