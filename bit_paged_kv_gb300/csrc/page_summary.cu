@@ -31,10 +31,10 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 4;                            // (131072 tokens 22.1 us, with eight 24.4)
-// Groups of kv-heads per warp, one after another: 131072 tokens 37.0 us with one,
-// 28.8 with two, 24.8 with four and with eight.  (A ring in shared memory filled by
-// bulk copies instead of registers: 26.3 us, 37 chunks of 64-token pages 18.6
-// against 11.9.)
+// Groups of kv-heads per warp, one after another (in 8-warp CTAs): 131072 tokens
+// 37.0 us with one, 28.8 with two, 24.8 with four and with eight.  (A ring in shared
+// memory filled by bulk copies instead of registers: 26.3 us, 37 chunks of 64-token
+// pages 18.6 against 11.9.)
 constexpr int kMaxPasses = 4;
 
 // a[j] += n_j s for the eight codes of a word; not BFM: s comes times 2^111 and
