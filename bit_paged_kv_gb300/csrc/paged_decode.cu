@@ -115,6 +115,10 @@ __device__ __forceinline__ void bulk_g2s_elect(uint32_t dst, const void* src, ui
 // conflicts
 __device__ __forceinline__ int red_col(int d) { return d + (d >> 4); }
 constexpr int kStepTok = 16;              // tokens per step (one MMA tile, one softmax update)
+// SPARSE's bounds of lift: all that binary16 scales (2^-24 to 65504) ask for, 36 to -3,
+// and bfloat16 ones from 2^-43 to 2^75; beyond, p s loses bits or ends at infinity.  Two
+// warps' weights stay within binary32 of each other.
+constexpr float kMaxLift = 40.0f, kMinLift = -60.0f;
 
 // What depends on the head dimension D (64, 128 or 256).
 template <int D>
@@ -225,13 +229,24 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves
 // zero products; every per-tile cost is shared by the two kv-heads.
 // SPARSE (saw_sparse_decode_int4): block_tables has a row, and seq_lens an
 // entry, per (sequence, kv-head).  Lists are short, so a CTA's start and end weigh
-// as much as its loop: 256 sequences of 128 16-token pages, GQA 8 (570 MB), 115 us,
-// 5.0 TB/s (GQA 4 99.6), in 3.4 waves of 4-warp CTAs; 8-warp ones 128.
-// FINE (sparse, outputs of more than 8 bits): p*s enters the PV product as a
-// binary16 and its remainder, 22 bits together.  As one binary16 its rounding
-// (2^-11) is of the size of a binary16 output's own and shows where few pages
-// are read; below a bfloat16 output's 2^-8 it does not.  PACKED: the remainder
-// is column 2h + 1, zero otherwise, at no product's cost; WIDE: a second product.
+// as much as its loop: 256 sequences of 128 16-token pages, GQA 8 (570 MB), 117 us,
+// 4.9 TB/s (GQA 4 100), in 3.4 waves of 4-warp CTAs; 8-warp ones 128.
+// p counts from 2^lift at the running maximum, with l, the z term and the
+// accumulators (it cancels in their quotient), lift being such that the largest V
+// scale s of the warp's tokens gives p s of 2^12 to 2^15: p s is a binary16, which
+// loses bits below 2^-14 and ends at 65504, and V is of any size.  A scale beyond
+// 2^15 lowers lift and rescales like a larger score, in the same vote.  (From 1 at
+// the maximum, values of 2^-13 lost two bits of a bfloat16 output and bfloat16 scales
+// beyond 65504 came out infinite; 256 x 2048 took 115.0 us, 116.7 with lift, 119.7
+// with factors on s and a vote per tile.)
+// FINE (outputs of more than 8 bits): p*s enters the PV product as a binary16 and
+// its remainder: off by at most 2^-22 of itself or 2^-37 of the largest s.  As one
+// binary16 its rounding (2^-11) is of the size of a binary16 output's own and shows
+// where few pages are read; below a bfloat16 output's 2^-8 it does not.  PACKED: the
+// remainder is column 2h + 1, zero otherwise, at no product's cost; WIDE: a second
+// product (256 x 2048 130 us; bfloat16 outputs do without it).  The sums of products
+// are cut at 2^-15 of a code step of a tile's largest p s (odd dims: 2^-19): the
+// tensor cores align a code, a subnormal, as if it were 2^-14.
 template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false, bool SPARSE = false,
           bool FINE = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
@@ -700,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   float l_run[2] = {0.0f, 0.0f};
   float z_run[2] = {0.0f, 0.0f};
   float2 nmu = make_float2(-0.0f, -0.0f);  // minus the running maxes (0 while they are -inf)
+  float lift = kMaxLift;  // SPARSE: added to nmu, see above
+  float vs_most = ex2(15.0f - lift);  // the largest scale that lift suits
   bool failed = false;
   int waited = 0;  // first of this warp's tiles not yet consumed
 
@@ -841,6 +858,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
     }
 
+    // SPARSE: the largest V scale of the tiles
+    float vs[SPARSE ? NT : 1][2], vs_top = 0.0f;
+    if constexpr (SPARSE) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint8_t* vst = ring + stage(t) * C::kStage + C::kHalf;
+        vs[t][0] = meta_lo(*reinterpret_cast<const uint32_t*>(vst + C::kmeta(sg, hkc)), BFM);
+        vs[t][1] = meta_lo(*reinterpret_cast<const uint32_t*>(vst + C::kmeta(sg + 8, hkc)), BFM);
+        if (!full[t]) {
+          vs[t][0] = sc[t][0] != -INFINITY ? vs[t][0] : 0.0f;
+          vs[t][1] = sc[t][2] != -INFINITY ? vs[t][1] : 0.0f;
+        }
+        vs_top = fmax3(vs_top, vs[t][0], vs[t][1]);
+      }
+    }
+
     // ---- online softmax: rescale only when a running max grows.  A head's
     // max over the warp exceeds its running max exactly when one lane's
     // does, so the lanes compare first and reduce only when one grew.
@@ -852,14 +885,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       mloc0 = fmaxf(sc[0][0], sc[0][2]);
       mloc1 = PACKED ? -INFINITY : fmaxf(sc[0][1], sc[0][3]);
     }
-    if (PACKED ? __any_sync(kFull, mloc0 > m_run[0])
-               : __any_sync(kFull, (mloc0 > m_run[0]) || (mloc1 > m_run[1]))) {
+    const bool grows = mloc0 > m_run[0] || (!PACKED && mloc1 > m_run[1]) || (SPARSE && vs_top > vs_most);
+    if (__any_sync(kFull, grows)) {
+      if constexpr (SPARSE) {
+        if (__any_sync(kFull, vs_top > vs_most)) {
+          // the largest scale to 2^12 .. 2^13
+          const int e = int(__reduce_max_sync(kFull, __float_as_uint(vs_top)) >> 23) - 127;
+          lift = fmaxf(float(12 - e), kMinLift);
+          vs_most = ex2(15.0f - lift);
+        }
+      }
       if constexpr (PACKED) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mloc0 = fmaxf(mloc0, __shfl_xor_sync(kFull, mloc0, x));
         const float mn0 = fmaxf(m_run[0], mloc0);
         const float mu0 = (mn0 == -INFINITY) ? 0.0f : mn0;
-        const float al0 = ex2(m_run[0] - mu0);
+        const float nmu0 = SPARSE ? lift - mu0 : -mu0;
+        const float al0 = SPARSE ? (m_run[0] == -INFINITY ? 0.0f : ex2(nmu0 - nmu.x)) : ex2(m_run[0] - mu0);
         m_run[0] = mn0;
         l_run[0] *= al0;
         z_run[0] *= al0;
@@ -872,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
             acc[k][3] *= al0;
           }
         }
-        nmu.x = -mu0;
+        nmu.x = nmu0;
       } else {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -880,8 +922,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           mloc1 = fmaxf(mloc1, __shfl_xor_sync(kFull, mloc1, x));
         }
         const float mn0 = fmaxf(m_run[0], mloc0), mn1 = fmaxf(m_run[1], mloc1);
-        const float al0 = ex2(m_run[0] - ((mn0 == -INFINITY) ? 0.0f : mn0));
-        const float al1 = ex2(m_run[1] - ((mn1 == -INFINITY) ? 0.0f : mn1));
+        const float mu0 = (mn0 == -INFINITY) ? 0.0f : mn0, mu1 = (mn1 == -INFINITY) ? 0.0f : mn1;
+        const float nmu0 = SPARSE ? lift - mu0 : -mu0, nmu1 = SPARSE ? lift - mu1 : -mu1;
+        const float al0 = SPARSE ? (m_run[0] == -INFINITY ? 0.0f : ex2(nmu0 - nmu.x)) : ex2(m_run[0] - mu0);
+        const float al1 = SPARSE ? (m_run[1] == -INFINITY ? 0.0f : ex2(nmu1 - nmu.y)) : ex2(m_run[1] - mu1);
         m_run[0] = mn0;
         m_run[1] = mn1;
         const float2 al = make_float2(al0, al1);  // columns 0, 2 are head A, 1, 3 head B
@@ -901,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           acc[k][3] = a23.y;
         }
         // x - mu = x + (-mu), exactly
-        nmu = make_float2(-((mn0 == -INFINITY) ? 0.0f : mn0), -((mn1 == -INFINITY) ? 0.0f : mn1));
+        nmu = make_float2(nmu0, nmu1);
       }
     }
 
@@ -922,8 +966,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       const uint32_t mv0 = *reinterpret_cast<const uint32_t*>(vst + C::kmeta(sg, hkc));
       const uint32_t mv1 = *reinterpret_cast<const uint32_t*>(vst + C::kmeta(sg + 8, hkc));
-      float sv0 = meta_lo(mv0, BFM), zv0 = meta_hi(mv0, BFM);
-      float sv1 = meta_lo(mv1, BFM), zv1 = meta_hi(mv1, BFM);
+      float sv0 = SPARSE ? vs[t][0] : meta_lo(mv0, BFM), zv0 = meta_hi(mv0, BFM);
+      float sv1 = SPARSE ? vs[t][1] : meta_lo(mv1, BFM), zv1 = meta_hi(mv1, BFM);
       if (!full[t]) {  // rows past the end may hold anything, even inf
         // (a valid row's score is never -inf: only the masking above sets it)
         const bool v0 = sc[t][0] != -INFINITY, v1 = sc[t][2] != -INFINITY;
@@ -1095,6 +1139,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   if (!direct && tid == 0)
     asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(tk) : "memory");
 
+  if constexpr (SPARSE) {  // (from here on the maximum is what p counted from)
+    m_run[0] = m_run[0] == -INFINITY ? -INFINITY : -nmu.x;
+    m_run[1] = m_run[1] == -INFINITY ? -INFINITY : -nmu.y;
+  }
   // ---- cross-thread reductions of l and the z term (lanes sharing c)
 #pragma unroll
   for (int x = 4; x < 32; x <<= 1) {

@@ -743,9 +743,13 @@ size_t saw_sparse_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
  * max_sel_len   host bound on sel_lens, at most max_selected * page_size.
  * out           [num_seqs][num_q_heads][head_dim]: float32, or with
  *               SAW_FMT_OUT_INPUT in `formats` the input type (one rounding).
+ *               A bfloat16 output's p*s have 11 bits, a float32 or binary16
+ *               one's 22: where 11 are too few, ask for float32.
  * workspace     saw_sparse_decode_workspace_bytes(...) bytes, 16-byte aligned.
  *               Calls sharing one must be ordered (one stream).
- * Other arguments, the arithmetic and the errors as saw_paged_decode_int4_ex.
+ * Other arguments and the errors as saw_paged_decode_int4_ex, and the arithmetic but
+ * for p*s: as binary16 numbers they are times a power of two that follows the scales,
+ * so that the error is the same for V of any size (bfloat16 scales 2^-43 to 2^75).
  */
 int32_t saw_sparse_decode_int4(const void* q, const void* k_cache, const void* v_cache,
                                const int32_t* sel_tables, int32_t max_selected,

@@ -1,0 +1,125 @@
+"""saw_sparse_decode_int4 over values of any magnitude: what it adds to the weights'
+own error does not depend on how large the values are.
+
+Keys are constant rows c_t in whole sixteenths, so that a score is c_t q_0 sm_scale
+without a sum: three roundings, one of the difference with the running maximum (all
+of at most 8.7 2^-24 in the exponent) and ex2's 2^-22 leave a weight off by less than
+2^-19, which moves an output by at most 2^-18 of A = sum w (15 s + |z|).  p s, held to
+22 bits or 2^-37 of the largest scale, adds 2^-22 and less; warps and splits add up in
+fewer than 40 roundings of 2^-24.
+
+The tensor cores add 16 products and the sum so far, each cut towards zero at 2^-25 of
+2^E, E the largest of their exponents, a product's being the sum of its operands' and a
+subnormal operand's -14 (measured).  The codes are subnormals, n 2^-24 at worst: beside
+2^e <= p s < 2^(e + 1) that is 2^(e - 14 - 25) or 2^(e - 15) of one code step, so that a
+tile loses less than 17 2^-15 of its largest p s; where the sum so far has the largest
+exponent, 17 2^-25 of it, twice a tile, at most four tiles a warp: 2^-18 A.  In all
+2^-16 A and 17 2^-15 of each tile's largest w s hold.
+
+A 16-bit output adds half a step of its type; a bfloat16 one takes p s in 11 bits, five
+standard deviations of that rounding (sparse_oracle.attend)."""
+import numpy as np
+import pytest
+import torch
+
+import bit_paged_kv_gb300 as saw
+from sparse_oracle import rows_of
+from test_gpu_sparse_decode import run
+
+pytestmark = pytest.mark.gpu
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+SCALE = 0.75
+
+
+def make(seed, B, lens, hq, hkv, D, P, dt, meta, size):
+    """size: of the values, [tokens] or one number."""
+    rng = np.random.default_rng(seed)
+    width = -(-max(lens) // P)
+    pages = width + 5
+    T = pages * P
+    tables = np.stack([[rng.permutation(pages)[:width] for _ in range(hkv)] for _ in range(B)]).astype(np.int32)
+    L = np.array([[lens[(b * hkv + k) % len(lens)] for k in range(hkv)] for b in range(B)], np.int32)
+    c = -rng.integers(0, 97, T) / 16.0
+    k = torch.tensor(c, dtype=dt).cuda()[:, None, None].expand(T, hkv, D).contiguous()
+    v = (rng.standard_normal((T, hkv, D)) * np.broadcast_to(size, T)[:, None, None]).astype(np.float32)
+    n = saw.saw_cache_bytes(pages, P, hkv, D)
+    kc, vc = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    saw.saw_quantize_append(k, torch.from_numpy(v).to(dt).cuda(), torch.arange(T, device="cuda").int(), kc, vc, pages, P,
+                            False, False, 64, meta_bf16=meta)
+    q = torch.zeros(B, hq, D, dtype=dt, device="cuda")
+    q[:, :, 0] = torch.tensor([1.0, 0.5, 1.25])[torch.arange(hq) % 3].to(dt).cuda()
+    return q, kc, vc, tables, L, pages
+
+
+def check(case, hkv, P, meta, odt):
+    q, kc, vc, tables, lens, pages = case
+    out, st = run(q, kc, vc, tables, lens, pages, P, False, False, 64, meta, odt=odt, scale=SCALE)
+    assert st == 0
+    B, hq, D = q.shape
+    G, kn, vn = hq // hkv, kc.cpu().numpy(), vc.cpu().numpy()
+    rows = {(e, h): tuple(rows_of(c, e, h, hkv, D, P, meta) for c in (kn, vn)) for e in range(pages) for h in range(hkv)}
+    got, x = out.double().cpu().numpy(), q.double().cpu().numpy()
+    for b in range(B):
+        for h in range(hkv):
+            n = int(lens[b, h])
+            ids = tables[b, h, :-(-n // P)]
+            K, s, z, c = (np.concatenate(a)[:n].astype(np.float64) for a in zip(*(
+                (rows[e, h][0][2], rows[e, h][1][1], rows[e, h][1][2], rows[e, h][1][0]) for e in ids)))
+            V = c * s[:, None] + z[:, None]
+            lg = x[b, h * G:(h + 1) * G, :1] * K * SCALE
+            w = np.exp(lg - lg.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            ref = w @ V
+            tiles = np.pad(w * s, ((0, 0), (0, -n % 16))).reshape(G, -1, 16).max(-1).sum(-1)
+            bound = (2.0 ** -16 * (w @ (15 * s + np.abs(z))) + 17 * 2.0 ** -15 * tiles)[:, None] + np.zeros_like(ref)
+            if out.dtype != F32:
+                fi = torch.finfo(out.dtype)
+                bound += np.maximum(np.abs(ref) * (fi.eps / 2) * (1 + 2.0 ** -7), fi.tiny * fi.eps / 2)
+            if out.dtype == BF:
+                bound += 5 * np.sqrt((w * w) @ ((c * s[:, None]) ** 2)) * 2.0 ** -11 / np.sqrt(3)
+            err = np.abs(got[b, h * G:(h + 1) * G] - ref)
+            assert (err <= bound).all(), (b, h, float((err / bound).max()))
+
+
+SIZES = {"one": 1.0, "2^-7": 2.0 ** -7, "2^-10": 2.0 ** -10, "2^-13": 2.0 ** -13, "2^10": 1024.0}
+
+
+@pytest.mark.parametrize("size", [*SIZES, "rows", "2^-40", "2^30"])
+@pytest.mark.parametrize("odt", [F32, F16, BF])
+@pytest.mark.parametrize("D,hq,hkv,P", [(64, 4, 1, 16), (64, 6, 1, 64), (128, 8, 2, 16), (128, 16, 2, 32), (256, 6, 2, 16),
+                                        (256, 7, 1, 32)])
+def test_values_of_any_size(D, hq, hkv, P, odt, size):
+    """Every list shape and output; rows of sizes 1 to 2^-14 in one list; bfloat16 words far beyond binary16."""
+    far = size in ("2^-40", "2^30")
+    if far and odt == F16:
+        odt, dt = F32, BF
+    else:
+        dt = F16 if odt == F16 else BF
+    mag = 2.0 ** float(size[2:]) if far else SIZES.get(size)
+    if mag is None:
+        mag = 2.0 ** -np.random.default_rng(7).integers(0, 15, 4096).astype(np.float64)
+    if not np.isscalar(mag):
+        mag = mag[:(-(-1500 // P) + 5) * P]
+    check(make(D + hq, 3, [1500, 40, 20, 130], hq, hkv, D, P, dt, far, mag), hkv, P, far, odt)
+
+
+@pytest.mark.parametrize("size", ["2^-10", "rows"])
+@pytest.mark.parametrize("B", [100, 210])
+@pytest.mark.parametrize("hq", [8, 14])
+def test_many_lists(hq, B, size):
+    """CTAs of 8 and of 4 warps."""
+    mag = SIZES.get(size)
+    if mag is None:
+        mag = 2.0 ** -np.random.default_rng(7).integers(0, 15, 4096).astype(np.float64)[:14 * 16]
+    check(make(B, B, [70, 20, 130], hq, 2, 128, 16, F16, False, mag), 2, 16, False, F32)
+
+
+@pytest.mark.parametrize("hq", [4, 8])
+def test_the_scale_grows_and_falls_along_a_list(hq):
+    """Sizes that rise by 2^14 over a list, or fall: the sums so far follow."""
+    n = 69 * 16
+    up = 2.0 ** (-14 * (1 - np.arange(n) / n))
+    for mag in (up, up[::-1]):
+        case = make(3, 40, [1000, 1024], hq, 4, 128, 16, F16, False, mag)
+        case[3][:] = np.arange(case[3].shape[-1])
+        check(case, 4, 16, False, F32)
