@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(32 * W, PER_SM) select_pages_kernel(const Sele
   const int w0 = min(warp * part, count), w1 = min(w0 + part, count);
   const float scale = float(kBins - 1) / (most - least);
   bool done = false;
-  if (most - least < INFINITY && scale < INFINITY) {  // (not: one value, or none that is finite)
+  if (most > least && most - least < INFINITY && scale < INFINITY) {  // (not: one value, or none that is finite)
     // A score's bin grows with the score: a difference and a product, each rounded
     // monotonously.
     auto bin_of = [&](uint32_t key) {
