@@ -135,7 +135,11 @@ int32_t make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t page_size, int
 // 512 / 1024 / 2048 tokens: 2048 tokens 8.5 / 9.1 / 10.6 / 9.8, 512 tokens 8.4 /
 // 5.7; 32 units of 2048: 13.7 / 9.3 / 10.7 / 10.1).  4-warp CTAs from two and a
 // half units per SM on (GQA 4, 384 units 27.2 against 30.8 with 8 warps; 320, GQA
-// 8, 33.7 against 31.1).
+// 8, 33.7 against 31.1), but for long lists only where seven in eight of the slots are
+// used, four per SM, and 16-warp ones else: 16384 tokens, 4 warps / 16 warps, GQA 4 and
+// 8: 432 units 179 / 152 and 219 / 177, 456 180 / 162 and 179 / 180, 760 302 / 268 and
+// 306 / 297, but 608 205 / 215 and 224 / 239, 2128 709 / 739 and 752 / 826; beyond 16384
+// tokens 4 warps read page ids as they go: 32768, 456 units, 392 / 313 and 446 / 335.
 int32_t make_sparse_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t page_size, int32_t max_len,
                          int32_t* splits_out, int32_t* pps_out, int32_t* warps_out) {
   int32_t warps = 16;
@@ -152,7 +156,8 @@ int32_t make_sparse_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t page_si
     *pps_out = int32_t(pps);
     *splits_out = int32_t(std::max<int64_t>(ceil_div(pages, pps), 1));
   } else if (*splits_out == 1 && 2 * units >= 5 * sms) {
-    warps = 4;
+    const int64_t slots = 4 * sms, used = ceil_div(units, slots) * slots;
+    if (int64_t(*pps_out) * page_size <= saw::kLongSplitTokens || 8 * units >= 7 * used) warps = 4;
   }
   if (warps_out) *warps_out = warps;
   return SAW_OK;
