@@ -14,6 +14,7 @@
 
 #include "saw_device.cuh"
 #include "saw_int4.h"
+#include "saw_norm.cuh"
 #include "saw_quant_row.cuh"
 
 namespace saw {
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const RopeTab
 // ss the sum of the squares by a binary tree over the bits of the element
 // index, lowest first: neighbours, pairs of neighbours, and so on.  A tree is
 // the same sum for every way of dealing a row's elements to lanes, so the row
-// and the bulk kernel give the same bits.
+// and the bulk kernel give the same bits.  The root and its reciprocal: saw_norm.cuh.
 #ifdef SAW_ROPE_NORM
 __device__ __forceinline__ float gain(const Params& p, int tensor, int d) {
   const void* w = p.weight[tensor];
@@ -125,23 +126,6 @@ __device__ __forceinline__ float gain(const Params& p, int tensor, int d) {
     g = in_lo(b, p.in_f16 != 0);
   }
   return __fadd_rn(g, p.weight_offset);
-}
-// The root and the reciprocal, correctly rounded: an approximation, its exact
-// remainder by a fused step, and one correction each (P. Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", 1990).  Equal
-// to the built-in ones for every mantissa and both parities of the exponent, in
-// the range that eps >= 2^-100 leaves; those, with their checks for the rest of
-// binary32, cost 22 us of 592 at 131072 tokens.
-template <int D>
-__device__ __forceinline__ float norm_factor(float ss, float eps) {
-  const float t = __fadd_rn(__fmul_rn(ss, 1.0f / D), eps);
-  float y;
-  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(t));
-  float root = __fmul_rn(t, y);
-  root = __fmaf_rn(__fmaf_rn(-root, root, t), __fmul_rn(0.5f, y), root);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(root));
-  y = __fmaf_rn(y, __fmaf_rn(-root, y, 1.0f), y);
-  return t == INFINITY ? 0.0f : y;                   // (squares beyond binary32)
 }
 #endif
 
@@ -271,7 +255,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) rope_append_row_kernel(const P
       for (int i = 0; i < E; i += 2 * d) s[i] = __fadd_rn(s[i], s[i + d]);
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], m));
-    const float r = norm_factor<D>(s[0], p.eps);
+    const float r = norm_factor(__fadd_rn(__fmul_rn(s[0], 1.0f / D), p.eps));
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), g[i]);
   }
@@ -635,7 +619,7 @@ __device__ __forceinline__ void norm16(float (&x)[16], const float* g, float eps
       u = __fadd_rn(u, __shfl_xor_sync(kAll, u, at == 2 ? d >> 3 : d >> 4));
     }
   }
-  const float r = norm_factor<D>(u, eps);
+  const float r = norm_factor(__fadd_rn(__fmul_rn(u, 1.0f / D), eps));
   const float2 rr = make_float2(r, r);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
