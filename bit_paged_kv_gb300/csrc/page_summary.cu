@@ -104,13 +104,13 @@ __global__ void __launch_bounds__(32 * kWarps) page_summary_kernel(const Summary
     for (int t = 0; t < kBatch; ++t) {
       const uint8_t* src = code + t * D;
       if constexpr (kWords == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
         x.w[t][0] = v.x;
         x.w[t][kWords - 1] = v.y;
       } else {
-        x.w[t][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        x.w[t][0] = *reinterpret_cast<const uint32_t*>(src);
       }
-      x.m[t] = __ldg(word + 2 * t);
+      x.m[t] = word[2 * t];
     }
   };
   float2 a[kWords][4] = {};

@@ -462,10 +462,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
 constexpr int kAppendRowsPerCta = 8;
 
 __global__ void __launch_bounds__(32 * kAppendRowsPerCta) bf16_append_kernel(
-    const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_stride,
-    int64_t v_stride, const int32_t* __restrict__ slots, int num_tokens, int hkv,
-    uint16_t* __restrict__ kc, uint16_t* __restrict__ vc, int64_t num_slots, int P,
-    int num_tensors, int32_t* dev_status) {
+    const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, const int32_t* slots, int num_tokens,
+    int hkv, uint16_t* kc, uint16_t* vc, int64_t num_slots, int P, int num_tensors, int32_t* dev_status) {
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31;
   const int64_t gw = int64_t(blockIdx.x) * kAppendRowsPerCta + (threadIdx.x >> 5);

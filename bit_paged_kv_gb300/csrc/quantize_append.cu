@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtasPerSm)
     if (live) {
       t = div_rows(uint32_t(row), p.hkv_mul, p.hkv_shift);
       hd = uint32_t(row) - t * uint32_t(hkv);
-      slot = __ldg(p.slot_mapping + t);
+      slot = p.slot_mapping[t];
     }
     cp_async_wait<kTileStages - 1>();  // this lane's copies of the current tile landed
     __syncwarp();                      // ... and the whole warp's
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtasPerSm)
     if (live) {
       t = div_rows(uint32_t(row), p.hkv_mul, p.hkv_shift);
       hd = uint32_t(row) - t * uint32_t(hkv);
-      slot = __ldg(p.slot_mapping + t);
+      slot = p.slot_mapping[t];
     }
     cp_async_wait<kTileStages - 1>();  // this lane's copies of the current tile landed
     __syncwarp();                      // ... and the whole warp's
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtasPerSm)
     if (live) {
       t = div_rows(uint32_t(row), p.hkv_mul, p.hkv_shift);
       hd = uint32_t(row) - t * uint32_t(hkv);
-      slot = __ldg(p.slot_mapping + t);
+      slot = p.slot_mapping[t];
     }
     cp_async_wait<kTileStages - 1>();  // this lane's copies of the current tile landed
     __syncwarp();                      // ... and the whole warp's

@@ -120,9 +120,9 @@ __device__ __forceinline__ float gain(const Params& p, int tensor, int d) {
   if (!w) return 1.0f;
   float g;
   if (p.weight_f32) {
-    g = __ldg(static_cast<const float*>(w) + d);
+    g = static_cast<const float*>(w)[d];
   } else {
-    const uint32_t b = __ldg(static_cast<const uint16_t*>(w) + d);
+    const uint32_t b = static_cast<const uint16_t*>(w)[d];
     g = in_lo(b, p.in_f16 != 0);
   }
   return __fadd_rn(g, p.weight_offset);
@@ -176,7 +176,7 @@ __device__ __forceinline__ void turn_row(float (&x)[D / 32], const float* cs, in
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         const int i = (d0 + e) >> 1;
-        const float c = __ldg(cs + i), s = __ldg(cs + half + i);
+        const float c = cs[i], s = cs[half + i];
         const float a = x[e], b = x[e + 1];
         x[e] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
         x[e + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
@@ -193,7 +193,7 @@ __device__ __forceinline__ void turn_row(float (&x)[D / 32], const float* cs, in
     for (int e = 0; e < E; ++e) {
       const float o = __shfl_sync(kAll, x[e], from);
       if (in) {
-        const float c = __ldg(cs + i0 + e), s = __ldg(cs + half + i0 + e);
+        const float c = cs[i0 + e], s = cs[half + i0 + e];
         const float u = __fmul_rn(x[e], c), v = __fmul_rn(o, s);
         x[e] = low ? __fsub_rn(u, v) : __fadd_rn(u, v);
       }
@@ -414,8 +414,8 @@ __device__ __forceinline__ void load_angles(Angles<LAYOUT>& t, const float* cs, 
     constexpr int n = decltype(count)::value;
 #pragma unroll
     for (int k = 0; k < n; k += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(cs + i + k));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + i + k));
+      const float4 x = *reinterpret_cast<const float4*>(cs + i + k);
+      const float4 y = *reinterpret_cast<const float4*>(cs + half + i + k);
       t.c[at + k] = x.x; t.c[at + k + 1] = x.y; t.c[at + k + 2] = x.z; t.c[at + k + 3] = x.w;
       t.s[at + k] = y.x; t.s[at + k + 1] = y.y; t.s[at + k + 2] = y.z; t.s[at + k + 3] = y.w;
     }

@@ -142,7 +142,10 @@ __device__ __forceinline__ uint16_t warp_quantize_row(const uint16_t* __restrict
 
 // Programmatic dependent launch: wait until the previous kernel in the stream
 // has completed (its writes visible), then let the next kernel start
-// launching.  Both are no-ops for a launch without the PDL attribute.
+// launching.  Both are no-ops for a launch without the PDL attribute.  A kernel
+// lives before its wait, while the one that writes its inputs may still run: its
+// loads are plain ones, not the non-coherent ones for memory that nothing writes
+// during a kernel's life (the times are the same).
 __device__ __forceinline__ void pdl_wait_then_release() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
