@@ -239,14 +239,17 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves
 // the maximum, values of 2^-13 lost two bits of a bfloat16 output and bfloat16 scales
 // beyond 65504 came out infinite; 256 x 2048 took 115.0 us, 116.7 with lift, 119.7
 // with factors on s and a vote per tile.)
-// FINE (outputs of more than 8 bits): p*s enters the PV product as a binary16 and
-// its remainder: off by at most 2^-22 of itself or 2^-37 of the largest s.  As one
-// binary16 its rounding (2^-11) is of the size of a binary16 output's own and shows
-// where few pages are read; below a bfloat16 output's 2^-8 it does not.  PACKED: the
-// remainder is column 2h + 1, zero otherwise, at no product's cost; WIDE: a second
-// product (256 x 2048 130 us; bfloat16 outputs do without it).  The sums of products
-// are cut at 2^-15 of a code step of a tile's largest p s (odd dims: 2^-19): the
-// tensor cores align a code, a subnormal, as if it were 2^-14.
+// FINE (all but WIDE with a bfloat16 output): p*s enters the PV product as a binary16
+// and its remainder: off by at most 2^-22 of itself or 2^-37 of the largest s.  PACKED:
+// the remainder is column 2h + 1, zero otherwise, at no product's cost (256 x 2048, GQA
+// 4, 99.7 us without, 100.4 with; 48 x 2048 27.6 and 28.6); WIDE: a second product (256 x
+// 2048 131 us with a binary16 output, 117 with a bfloat16 one without it, whose own 2^-8
+// the 2^-11 of p*s stay below).  And V's codes stand three bits further up: the tensor
+// cores add 16 products and the sum so far, each cut at 2^-25 of the largest exponent,
+// and take a subnormal's as 2^-14, so that n 2^-24 is cut at 2^-15 of a code step of the
+// tile's largest p*s, always downwards; n 2^-21 at 2^-18, n 2^-17 at 2^-22.  Error of a
+// float32 output, 1 x 2048 tokens: 7e-5 of it with codes in place, 6e-6 so, 2e-6 with all
+// of them at 2^-17 (two more shifts a word: 138 us for 131).
 template <int D, int P, bool PACKED, bool APPEND, bool BFM, bool PAIR = false, bool SHARED = false, bool SPARSE = false,
           bool FINE = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
@@ -1014,6 +1017,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       // tokens 2c, 2c + 1 of the block, which is, masked, the A fragment
       // over those tokens for the dims of the pair (see vdim below).
       constexpr int kKW = DM::kKWords;
+      constexpr uint32_t kLoV = FINE ? kLoNib << 3 : kLoNib, kHiV = FINE ? kHiNib << 3 : kHiNib;
       const uint8_t* vrow = PAIR ? vst + C::kcode(sg, c >> 1) + (D / 8) * (c & 1)
                                  : vst + C::kcode(sg) + (D / 8) * c;
       uint32_t vaw[kKW], vbw[kKW];
@@ -1037,13 +1041,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         const uint32_t tb = movm_t(vbw[db]);  // rows 8-15
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t x = hh ? (ta >> 8) : ta;
-          const uint32_t y = hh ? (tb >> 8) : tb;
+          const uint32_t x = FINE ? (hh ? (ta >> 5) : (ta << 3)) : hh ? (ta >> 8) : ta;
+          const uint32_t y = FINE ? (hh ? (tb >> 5) : (tb << 3)) : hh ? (tb >> 8) : tb;
           uint32_t a[4];
-          a[0] = x & kLoNib;  // dims of rows g: n * 2^-24
-          a[1] = x & kHiNib;  // dims of rows g + 8: n * 2^-20
-          a[2] = y & kLoNib;
-          a[3] = y & kHiNib;
+          a[0] = x & kLoV;  // dims of rows g: n * 2^-24 (FINE: 2^-21)
+          a[1] = x & kHiV;  // dims of rows g + 8: n * 2^-20 (2^-17)
+          a[2] = y & kLoV;
+          a[3] = y & kHiV;
           mma_16816(acc[2 * db + hh], a, b0, b1);
           if constexpr (FINE && !PACKED) mma_16816(acc[2 * db + hh], a, r0, r1);
         }
@@ -1151,17 +1155,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     z_run[0] += __shfl_xor_sync(kFull, z_run[0], x);
     z_run[1] += __shfl_xor_sync(kFull, z_run[1], x);
   }
-  // output rows g (even dims) carried n * 2^-24, rows g + 8 (odd) n * 2^-20
+  // output rows g (even dims) carried n * 2^-24, rows g + 8 (odd) n * 2^-20 (FINE:
+  // 2^-21, 2^-17)
+  constexpr float kEven = FINE ? 0x1p21f : 0x1p24f, kOdd = FINE ? 0x1p17f : 0x1p20f;
 #pragma unroll
   for (int k = 0; k < kMT; ++k) {
     if constexpr (FINE && PACKED) {
       acc[k][0] += acc[k][1];
       acc[k][2] += acc[k][3];
     }
-    acc[k][0] *= 16777216.0f;
-    acc[k][1] *= 16777216.0f;
-    acc[k][2] *= 1048576.0f;
-    acc[k][3] *= 1048576.0f;
+    acc[k][0] *= kEven;
+    acc[k][1] *= kEven;
+    acc[k][2] *= kOdd;
+    acc[k][3] *= kOdd;
   }
   __syncthreads();  // every warp is done with its ring: reuse it
 
@@ -1671,9 +1677,7 @@ cudaError_t launch_page_m(const DecodeParams& p, cudaStream_t stream) {
   return packed ? launch_p<D, P, true, false, BFM, false, true>(p, stream)
                 : launch_p<D, P, false, false, BFM, false, true>(p, stream);
 #elif defined(SAW_DECODE_SPARSE)
-  if (p.out16 && !p.in_f16)
-    return packed ? launch_p<D, P, true, false, BFM, false, false, true>(p, stream)
-                  : launch_p<D, P, false, false, BFM, false, false, true>(p, stream);
+  if (!packed && p.out16 && !p.in_f16) return launch_p<D, P, false, false, BFM, false, false, true>(p, stream);
   return packed ? launch_p<D, P, true, false, BFM, false, false, true, true>(p, stream)
                 : launch_p<D, P, false, false, BFM, false, false, true, true>(p, stream);
 #else

@@ -743,8 +743,8 @@ size_t saw_sparse_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
  * max_sel_len   host bound on sel_lens, at most max_selected * page_size.
  * out           [num_seqs][num_q_heads][head_dim]: float32, or with
  *               SAW_FMT_OUT_INPUT in `formats` the input type (one rounding).
- *               A bfloat16 output's p*s have 11 bits, a float32 or binary16
- *               one's 22: where 11 are too few, ask for float32.
+ *               p*s have 22 bits, with a bfloat16 output of more than 4
+ *               q-heads per kv-head 11: where those are too few, ask for float32.
  * workspace     saw_sparse_decode_workspace_bytes(...) bytes, 16-byte aligned.
  *               Calls sharing one must be ordered (one stream).
  * Other arguments and the errors as saw_paged_decode_int4_ex, and the arithmetic but
