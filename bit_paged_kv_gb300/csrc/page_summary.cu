@@ -15,11 +15,12 @@
 // plain ones do.  bfloat16 scales leave no room for that: there the nibble goes
 // under the exponent of 2^23, which is taken off again.
 //
-// Bound: issue (75 % of the slots where the pages are many), half of it the masks,
-// one per code on a pipe of half rate.  131072 tokens, 8 kv-heads, D 128 (76 MB):
-// 22.1 us (11.1 at the measured copy rate), four times as many 74; with
-// conversions 37, the nibbles under 2^23's exponent 36, one kv-head a warp 26.
-// 64-token pages 21.1 us.
+// Bound: issue, 65 % of the slots where the pages are many, with the ALU pipe at 62 %:
+// of 16.1 M warp instructions at 131072 tokens 4.2 M are the masks, one per code on a
+// pipe of half rate, 2.1 M the fused steps, about 2 M loads and the words' conversion,
+// the others what follows a sum.  131072 tokens, 8 kv-heads, D 128 (76 MB): 22.2 us
+// (11.1 at the measured copy rate), bfloat16 words 32.9, four times as many tokens 74;
+// with conversions 37, one kv-head a warp 26.  64-token pages 21.1 us.
 #include <algorithm>
 
 #include "saw_device.cuh"
@@ -30,11 +31,12 @@ namespace saw {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kWarps = 4;                            // (131072 tokens 22.1 us, with eight 24.4)
-// Groups of kv-heads per warp, one after another (in 8-warp CTAs): 131072 tokens
-// 37.0 us with one, 28.8 with two, 24.8 with four and with eight.  (A ring in shared
-// memory filled by bulk copies instead of registers: 26.3 us, 37 chunks of 64-token
-// pages 18.6 against 11.9.)
+constexpr int kWarps = 4;                            // (131072 tokens 22.2 us, with eight 24.7)
+// Groups of kv-heads per warp, one after another: 131072 tokens 30.0 us with one, 24.5
+// with two, 22.3 with four and with eight, four times as many 109, 85.7, 74.3, 74.3,
+// bfloat16 words 37.9, 33.7, 32.9, 32.8; 32768 tokens, where warps are few, 7.5 with any.
+// (A ring in shared memory filled by bulk copies instead of registers: 26.3 us, 37
+// chunks of 64-token pages 18.6 against 11.9.)
 constexpr int kMaxPasses = 4;
 
 // a[j] += n_j s for the eight codes of a word; not BFM: s comes times 2^111 and

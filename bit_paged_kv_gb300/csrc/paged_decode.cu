@@ -238,7 +238,8 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves
 // 2^15 lowers lift and rescales like a larger score, in the same vote.  (From 1 at
 // the maximum, values of 2^-13 lost two bits of a bfloat16 output and bfloat16 scales
 // beyond 65504 came out infinite; 256 x 2048 took 115.0 us, 116.7 with lift, 119.7
-// with factors on s and a vote per tile.)
+// with factors on s and a vote per tile.)  The exponent is larger by lift, and its
+// rounding moves p by 2^-19 at most.
 // FINE (all but WIDE with a bfloat16 output): p*s enters the PV product as a binary16
 // and its remainder: off by at most 2^-22 of itself or 2^-37 of the largest s.  PACKED:
 // the remainder is column 2h + 1, zero otherwise, at no product's cost (256 x 2048, GQA

@@ -356,8 +356,10 @@ cudaError_t launch_rows(const Params& p, cudaStream_t stream) {
 // 4 and that one too, and only the others cross lanes.  The lane's cosines and
 // sines serve all heads of the token.
 //
-// With norms (SAW_ROPE_NORM) issue binds as much as memory: 131072 tokens 580 us,
-// 8192 41.9, 256 tokens of 64 q-heads 4.8.
+// With norms (SAW_ROPE_NORM) 131072 tokens take 580 us, 8192 41.8, 256 tokens of 64
+// q-heads 4.8: HBM at 73 %, issue at 58 %, and latency between them, long_scoreboard
+// being the first stall: a warp's rows are under way within an item only, and 125
+// registers leave two CTAs per SM and none for the next item's.
 //
 // Bound: HBM.  131072 tokens, Hq 32, Hkv 8, D 128: 2.90 GB in 484 us, 6.0 TB/s
 // (426 us at the measured copy rate); 2047 tokens, half the head turned (45
@@ -542,7 +544,7 @@ __device__ __forceinline__ void rotate16(float (&x)[16], int h, float c_h, int h
   for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], c_h);
 }
 
-// The same, two sums per instruction (with norms the kernel is bound by issue:
+// The same, two sums per instruction (with norms, whose instructions are more:
 // 16 us of 608 at 131072 tokens; without, bound by memory, it loses 30 of 482).
 template <int D>
 __device__ __forceinline__ void rotate16_packed(float (&x)[16], int h, float c_h, int hc, int lane) {

@@ -21,14 +21,15 @@
 // put nearly all of them in a few bins) and a ranking of the keys in its bin;
 // where that bin holds too many (ties, far outliers), digit by digit.
 //
-// Bound: many pages, by how fast an SM takes in pieces of lines (a page costs a
-// kv-head three 32-byte sectors in two places) and by issue behind it: 16 x 131072
-// tokens 33.0 us (10.6 at the measured copy rate), the registers and warps that a
-// unit gets counting for more than CTAs (below).  Whole rows by bulk copies of 544
-// bytes, a cluster per sequence with its kv-heads' keys dealt to owners, took 136 us,
-// two kv-heads to a CTA 44.  Few pages, by the chain of rounds: length, page ids,
-// rows, extremes, histogram, ranking, list (1 x 32768 tokens 8.5 us in clusters; all
-// keys to one CTA of the cluster, with fewer barriers, 9.5).
+// Bound: many pages, by the scoring, 26.8 us of 32.7 at 16 x 131072 tokens (10.6 at the
+// measured copy rate): the latency of the rows' copies at the warps that fit, whose
+// first stall is long_scoreboard, with issue at 38 % and DRAM at 2.0 TB/s; a page costs
+// a kv-head three 32-byte sectors in two places.  Whole rows by bulk copies of 544 bytes,
+// a cluster per sequence with its kv-heads' keys dealt to owners, took 136 us, two
+// kv-heads to a CTA 44.  Choosing behind it is a chain of rounds: extremes, histogram,
+// ranking, list; with few pages most of the time (1 x 32768 tokens 8.5 us, 3.7 of them
+// the scoring; all keys to one CTA of the cluster, with fewer barriers, 9.5).  By digits:
+// 13.0 and 42.4 us where scores are equal.
 #include <algorithm>
 
 #include <cooperative_groups.h>

@@ -653,7 +653,8 @@ size_t saw_summary_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_d
  * seq_lens      device int32 [num_seqs]: cached tokens, the new ones included.
  * new_lens      device int32 [num_seqs]: tokens that the step appended, or NULL
  *               (all of them; a count above seq_lens counts as all too).
- * max_new_len   host bound on the smaller of the two; sizes the grid.
+ * max_new_len   host bound on the smaller of the two; sizes the grid for every sequence, so
+ *               that a long prompt beside many single tokens wants a call of its own.
  * summary       device, saw_summary_bytes(...), 16-byte aligned.  Summaries go by physical
  *               page, so forks of a sequence share them.
  * Pages floor((L - n) / page_size) to floor(L / page_size) - 1 of a sequence

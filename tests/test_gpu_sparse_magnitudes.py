@@ -2,9 +2,9 @@
 own error does not depend on how large the values are.
 
 Keys are constant rows c_t in whole sixteenths, so that a score is c_t q_0 sm_scale
-without a sum: three roundings, one of the difference with the running maximum (all
-of at most 8.7 2^-24 in the exponent) and ex2's 2^-22 leave a weight off by less than
-2^-19, which moves an output by at most 2^-18 of A = sum w (15 s + |z|).  p s, held to
+without a sum: three roundings (of at most 8.2 2^-24 in the exponent), one of the
+exponent itself (below 64, 2^-19) and ex2's 2^-22 leave a weight off by less than
+2^-18.6, which moves an output by at most 2^-17.6 of A = sum w (15 s + |z|).  p s, held to
 22 bits or 2^-37 of the largest scale, adds 2^-22 and less; warps and splits add up in
 fewer than 40 roundings of 2^-24.
 

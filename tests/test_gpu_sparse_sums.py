@@ -3,8 +3,7 @@ more than 4 q-heads per kv-head), and products that are small beside others of t
 tile.
 
 Keys are constant rows of whole numbers and the softmax scale makes the base-2 score
-half of them: a weight 2^(-c/2) is off by ex2's 2^-22, and by 2 roundings of the score of
-at most 6 2^-24 each, so that 2^-20.5 holds, of either sign.  The tensor cores add 16
+half of them, exactly: a weight 2^(-c/2) is off by ex2's 2^-22.  The tensor cores add 16
 products and the sum so far, each cut towards zero at 2^-25 of 2^E, E the largest of
 their exponents, a subnormal operand's counting as -14 (measured): codes n 2^-21 beside
 2^e <= p s < 2^(e + 1) are cut at 2^(e - 14 - 25), 2^-18 of a code step of the tile's
@@ -21,6 +20,10 @@ pytestmark = pytest.mark.gpu
 BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 SCALE = float(np.float32(0.5 / 1.4426950408889634))
 HALF = float(np.float32(SCALE * 1.4426950408889634))    # of a score, as the library rounds it
+assert HALF == 0.5
+# of sum w (n s + |z|): the weights, twice 2^-22; one tile per warp, two products' sums cut at 17 2^-25;
+# warps, the sum of the weights and the quotient in at most 34 roundings of 2^-24; p s 2^-22
+RELATIVE = 2.0 ** -18
 
 
 def case(seed, c, v, lens, hq, hkv, P, dt, meta):
@@ -39,8 +42,7 @@ def case(seed, c, v, lens, hq, hkv, P, dt, meta):
     return q, kc, vc, tables, np.repeat(np.asarray(lens, np.int32)[:, None], hkv, 1), pages
 
 
-def check(got_case, hkv, P, meta, odt, relative):
-    """relative: of sum w (n s + |z|), for the weights and the roundings of sums."""
+def check(got_case, hkv, P, meta, odt):
     q, kc, vc, tables, lens, pages = got_case
     out, st = run(q, kc, vc, tables, lens, pages, P, False, False, 64, meta, odt=odt, scale=SCALE)
     assert st == 0
@@ -55,7 +57,7 @@ def check(got_case, hkv, P, meta, odt, relative):
             w /= w.sum()
             ref = w @ (c[:n] * s[:n, None] + z[:n, None])
             tiles = np.pad(w * s[:n], (0, -n % 16)).reshape(-1, 16).max(-1).sum()
-            bound = relative * (w @ (c[:n] * s[:n, None] + np.abs(z[:n, None]))) + 17 * 2.0 ** -18 * tiles
+            bound = RELATIVE * (w @ (c[:n] * s[:n, None] + np.abs(z[:n, None]))) + 17 * 2.0 ** -18 * tiles
             if out.dtype != F32:
                 fi = torch.finfo(out.dtype)
                 bound = bound + np.maximum(np.abs(ref) * (fi.eps / 2) * (1 + 2.0 ** -7), fi.tiny * fi.eps / 2)
@@ -75,13 +77,13 @@ def outputs(hq, hkv, odt):
 @pytest.mark.parametrize("dt,odt,meta", OUTPUTS)
 @pytest.mark.parametrize("D,hq,hkv,P", SHAPES)
 def test_weights_times_scales(D, hq, hkv, P, dt, odt, meta):
-    """Few tokens: the weights 2^-20.5, twice, 20 roundings of 2^-24 (9 tiles in as many warps), p s 2^-22: 2^-18.5."""
+    """Few tokens, up to 9 tiles in as many warps."""
     outputs(hq, hkv, odt)
     rng = np.random.default_rng(D + hq)
     T = 192
     v = rng.standard_normal((T, hkv, D)) * np.exp2(rng.uniform(-1, 1, (T, 1, 1)))
     check(case(1, rng.integers(0, 13, T).astype(float), v, [1, 3, 7, 16, 20, 33, 60, 100, 130], hq, hkv, P, dt, meta), hkv, P,
-          meta, odt, 2.0 ** -18.5)
+          meta, odt)
 
 
 @pytest.mark.parametrize("dt,odt,meta", OUTPUTS)
@@ -97,4 +99,4 @@ def test_small_products_beside_a_large_scale(D, hq, hkv, P, dt, odt, meta):
     at = np.arange(0, T, 16) + rng.integers(0, 3, T // 16)
     v[at] = 15.0 * rng.integers(0, 2, (len(at), hkv, D))
     v[at, :, :2], v[at, :, 2:4] = 0.0, 15.0
-    check(case(2, np.zeros(T), v, [16, 32, 100, 130], hq, hkv, P, dt, meta), hkv, P, meta, odt, 2.0 ** -18.5)
+    check(case(2, np.zeros(T), v, [16, 32, 100, 130], hq, hkv, P, dt, meta), hkv, P, meta, odt)
